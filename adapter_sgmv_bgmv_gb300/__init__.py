@@ -10,6 +10,7 @@ without the built library raises: there is no other implementation.
 from __future__ import annotations
 
 import ctypes
+import math
 import weakref
 
 import numpy as np
@@ -19,6 +20,7 @@ from . import _lib
 
 __all__ = ["LoraError", "Context", "AdapterTable", "lora_plan_build", "lora_shrink",
            "lora_expand", "lora_fused", "lora_fused_noalloc", "lora_base_fused", "PreparedFused", "PreparedFusedDeviceIds", "lora_merge", "lora_unmerge", "lora_page_in", "lora_fused_device_ids", "lora_tune_shape",
+           "KvCache", "KvBatch", "lora_kv_write", "lora_kv_read", "lora_attention",
            "KIND_ROWS_FUSED", "KIND_SHRINK", "KIND_EXPAND", "KIND_TILE_FUSED", "KIND_MERGE",
            "OPT_TILE_PATH", "OPT_MERGE_KERNEL", "OPT_TILE_MIN_RUN", "OPT_EARLY_PAGES", "OPT_DEVICE_PLAN",
            "OPT_EARLY_INPUT", "OPT_ROWS_B_OVER_A",
@@ -109,7 +111,7 @@ class Context:
         self.handle = h.value
 
     def close(self):
-        """Destroy the context and every table registered with it."""
+        """Destroy the context and every table and cache registered with it."""
         if self.handle:
             for t in list(self._tables):
                 t.close()
@@ -445,6 +447,155 @@ def lora_page_in(ctx: Context, table: AdapterTable, adapter: int, host_a: torch.
     _check(_L.lora_page_in(ctx.handle, table.handle, int(adapter), host_a.data_ptr(),
                            host_a.shape[1], host_b.data_ptr(), host_b.shape[1],
                            _stream(stream, ctx.device)), ctx)
+
+
+_KV_FORMATS = {torch.bfloat16: 0, torch.int8: 1, torch.float8_e4m3fn: 2}
+
+
+class KvCache:
+    """A paged key/value cache over caller-owned device pools (see include/lora.h).
+
+    k_pool / v_pool: CUDA tensors [n_pages, page_size, n_heads, head_dim] of bf16, int8 or
+    float8_e4m3fn with the same strides, the last dimension contiguous; any other order
+    of memory is a view of this shape (heads first: pool.transpose(1, 2)).  k_scale /
+    v_scale: float32 [n_pages, page_size, n_heads] with the same strides, for the 8-bit
+    types.  The tensors are kept referenced here."""
+
+    def __init__(self, ctx: Context, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                 k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None):
+        self.handle = None
+        for t, nm in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+            if t.dim() != 4 or t.dtype not in _KV_FORMATS or t.stride(3) != 1:
+                raise ValueError(f"{nm} must be [n_pages, page_size, n_heads, head_dim] of bf16, int8 or "
+                                 "float8_e4m3fn with a contiguous last dimension")
+        if k_pool.shape != v_pool.shape or k_pool.dtype != v_pool.dtype or \
+                k_pool.stride() != v_pool.stride():
+            raise ValueError("k_pool and v_pool must have the same shape, type and strides")
+        d = _lib.KvDesc()
+        d.format = _KV_FORMATS[k_pool.dtype]
+        if d.format:
+            for t, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if t is None or t.dtype != torch.float32 or t.shape != k_pool.shape[:3]:
+                    raise ValueError(f"{nm} must be float32 [n_pages, page_size, n_heads] for 8-bit pools")
+            if k_scale.stride() != v_scale.stride():
+                raise ValueError("k_scale and v_scale must have the same strides")
+            d.scale_page_stride, d.scale_cell_stride, d.scale_head_stride = k_scale.stride()
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("bf16 pools have no scales")
+        d.n_pages, d.page_size, d.n_heads, d.head_dim = k_pool.shape
+        d.page_stride, d.cell_stride, d.head_stride = k_pool.stride()[:3]
+        if ctx.device is None:      # host-only context: pools are never dereferenced
+            ptr = lambda t, nm: t.data_ptr()  # noqa: E731
+        else:
+            ptr = _dev_ptr
+        d.k_pool, d.v_pool = ptr(k_pool, "k_pool"), ptr(v_pool, "v_pool")
+        if d.format:
+            d.k_scale, d.v_scale = ptr(k_scale, "k_scale"), ptr(v_scale, "v_scale")
+        self.ctx = ctx
+        self.k_pool, self.v_pool, self.k_scale, self.v_scale = k_pool, v_pool, k_scale, v_scale
+        self.n_pages, self.page_size, self.n_heads, self.head_dim = k_pool.shape
+        h = ctypes.c_void_p()
+        _check(_L.lora_kv_create(ctx.handle, ctypes.byref(d), ctypes.byref(h)), ctx)
+        self.handle = h.value
+        ctx._tables.add(self)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            _L.lora_kv_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KvBatch:
+    """The sequences of a cache call (see include/lora.h): starts [n_seqs + 1], lens
+    [n_seqs] and pages [n_seqs, n_cols], int32 CUDA tensors whose contents the kernels
+    read; update them in place between steps (or between replays of a graph).  max_new
+    bounds a sequence's new tokens (None: the call's rows)."""
+
+    def __init__(self, starts: torch.Tensor, lens: torch.Tensor, pages: torch.Tensor,
+                 max_new: int | None = None):
+        for t, nm, dim in ((starts, "starts", 1), (lens, "lens", 1), (pages, "pages", 2)):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dim or \
+                    (t.numel() and t.stride(-1) != 1):
+                raise ValueError(f"{nm} must be a {dim}-D int32 tensor, contiguous in its last dimension")
+        if starts.shape[0] != lens.shape[0] + 1 or pages.shape[0] != lens.shape[0]:
+            raise ValueError("shapes: starts [n_seqs + 1], lens [n_seqs], pages [n_seqs, n_cols]")
+        self.starts, self.lens, self.pages = starts, lens, pages
+        a = _lib.KvBatchArgs()
+        a.starts = _dev_ptr(starts, "starts")
+        a.lens = _dev_ptr(lens, "lens")
+        a.pages = _dev_ptr(pages, "pages")
+        a.n_seqs, a.n_cols = pages.shape
+        a.ld_pages = max(pages.stride(0), pages.shape[1]) if pages.shape[0] > 1 else pages.shape[1]
+        if pages.shape[0] > 1 and pages.stride(0) < pages.shape[1]:
+            raise ValueError("the rows of pages overlap")
+        a.max_new = (1 << 31) - 1 if max_new is None else int(max_new)
+        self._args = a
+        self._ref = ctypes.addressof(a)
+
+
+def _head_rows(t: torch.Tensor, what: str, head_dim: int):
+    """(pointer, row stride, rows, heads) of bf16 rows [n, heads, head_dim] (the heads one
+    after another) or [n, heads * head_dim]."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{what} must be a CUDA tensor")
+    st, sh = t.stride(), t.shape
+    if len(sh) == 3:
+        ok = sh[2] == head_dim and st[2] == 1 and (sh[1] == 1 or st[1] == head_dim)
+        heads = sh[1]
+    else:
+        ok = len(sh) == 2 and st[1] == 1 and sh[1] % head_dim == 0
+        heads = sh[1] // head_dim if ok else 0
+    if not ok or t.element_size() != 2:
+        raise ValueError(f"{what} must be bf16 [n, heads, {head_dim}] or [n, heads * {head_dim}] rows")
+    # the stride of a single row says nothing
+    return t.data_ptr(), st[0] if sh[0] > 1 else heads * head_dim, sh[0], heads
+
+
+def _kv_rows(ctx, cache, batch, k, v, stream, fn):
+    pk, ldk, n, hk = _head_rows(k, "k", cache.head_dim)
+    pv, ldv, nv, hv = _head_rows(v, "v", cache.head_dim)
+    if nv != n or hk != cache.n_heads or hv != cache.n_heads:
+        raise ValueError("k and v must have one row a token and the cache's heads")
+    rc = fn(ctx.handle, cache.handle, batch._ref, n, pk, ldk, pv, ldv, _stream(stream, ctx.device))
+    if rc:
+        _check(rc, ctx)
+
+
+def lora_kv_write(ctx: Context, cache: KvCache, batch: KvBatch, k: torch.Tensor, v: torch.Tensor,
+                  stream=None):
+    """Store the batch's new keys and values (bf16 [n, n_heads, head_dim]) in their cells,
+    in the cache's format."""
+    _kv_rows(ctx, cache, batch, k, v, stream, _L.lora_kv_write)
+
+
+def lora_kv_read(ctx: Context, cache: KvCache, batch: KvBatch, k: torch.Tensor, v: torch.Tensor,
+                 stream=None):
+    """The cells of the batch's rows back as bf16 rows k and v (written)."""
+    _kv_rows(ctx, cache, batch, k, v, stream, _L.lora_kv_read)
+
+
+def lora_attention(ctx: Context, cache: KvCache, batch: KvBatch, q: torch.Tensor, out: torch.Tensor,
+                   scale: float | None = None, window: int = 0, sinks: int = 0, stream=None):
+    """out <- attention of the batch's new tokens (q, bf16 [n, heads, head_dim]) over the
+    cache, which already holds their keys and values: causal by position, with a sliding
+    window and `sinks` first tokens that stay visible when window > 0.  scale: None for
+    head_dim ** -0.5."""
+    pq, ldq, n, hq = _head_rows(q, "q", cache.head_dim)
+    po, ldo, no, ho = _head_rows(out, "out", cache.head_dim)
+    if no != n or ho != hq:
+        raise ValueError("out must have the shape of q")
+    if scale is None:
+        scale = 1.0 / math.sqrt(cache.head_dim)
+    rc = _L.lora_attention(ctx.handle, cache.handle, batch._ref, n, pq, ldq, hq, scale, window, sinks,
+                           po, ldo, _stream(stream, ctx.device))
+    if rc:
+        _check(rc, ctx)
 
 
 def lora_tune_shape(ctx: Context, table: AdapterTable, kind: int, ids, x: torch.Tensor,

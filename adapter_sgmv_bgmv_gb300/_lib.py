@@ -28,6 +28,21 @@ class FusedArgs(ctypes.Structure):
                 ("y", P), ("ldy", I64), ("d_in", I), ("d_out", I), ("stream", P)]
 
 
+class KvDesc(ctypes.Structure):
+    """lora_kv_desc (include/lora.h)."""
+    _fields_ = [("k_pool", P), ("v_pool", P), ("k_scale", P), ("v_scale", P), ("n_pages", I64),
+                ("page_size", I), ("n_heads", I), ("head_dim", I), ("format", I),
+                ("page_stride", I64), ("cell_stride", I64), ("head_stride", I64),
+                ("scale_page_stride", I64), ("scale_cell_stride", I64),
+                ("scale_head_stride", I64)]
+
+
+class KvBatchArgs(ctypes.Structure):
+    """lora_kv_batch (include/lora.h)."""
+    _fields_ = [("starts", P), ("lens", P), ("pages", P), ("n_seqs", I64), ("n_cols", I64),
+                ("ld_pages", I64), ("max_new", I64)]
+
+
 SIGNATURES = {
     "lora_version": ([], I),
     "lora_strerror": ([I], ctypes.c_char_p),
@@ -49,6 +64,11 @@ SIGNATURES = {
     "lora_fused_device_ids": ([P, P, P, I64, P, I64, I, P, I64, I, P], I),
     "lora_fused_args_call": ([ctypes.POINTER(FusedArgs)], I),
     "lora_fused_device_ids_args_call": ([ctypes.POINTER(FusedArgs)], I),
+    "lora_kv_create": ([P, ctypes.POINTER(KvDesc), ctypes.POINTER(P)], I),
+    "lora_kv_destroy": ([P], I),
+    "lora_kv_write": ([P, P, P, I64, P, I64, P, I64, P], I),
+    "lora_kv_read": ([P, P, P, I64, P, I64, P, I64, P], I),
+    "lora_attention": ([P, P, P, I64, P, I64, I, F, I, I, P, I64, P], I),
     "lora_selftest_timeout": ([P, I64, P], I),
     "lora_tiles_load": ([P, ctypes.c_char_p], I),
     "lora_tiles_save": ([P, ctypes.c_char_p], I),

@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "../../include/lora.h"
+#include "ctx.h"
 #include "internal.h"
 #include "status.h"
 #include "plan.h"
@@ -127,6 +128,9 @@ struct lora_ctx {
     int dense_turn = 0;
     std::vector<int32_t> slot_of;   // adapter -> slot while a call's slots are assigned
     std::unique_ptr<TileParams> tparams;   // launch parameters of the tile kernels
+    int sms = 0;                    // SMs of the device
+    uint8_t *attn = nullptr;        // lora_attention: partial results and arrival counters,
+    size_t attn_bytes = 0;          //   made with the context's first cache
     uint8_t *flush = nullptr;       // lora_tune_shape: a buffer larger than L2, written
                                     // before each timed call so that it starts cold
 };
@@ -1101,6 +1105,50 @@ int merge_call(lora_ctx *ctx, const lora_table *t, int adapter, void *W, int64_t
 
 }  // namespace
 
+// What the cache's entry points (kv_api.cpp) use of a context.
+namespace lora {
+
+int ctx_begin(lora_ctx *ctx, cudaStream_t stream)
+{
+    ctx->last_path = ctx->last_launches = 0;
+    begin_call(ctx, stream);
+    return use_device(ctx);
+}
+
+int ctx_cuda_fail(lora_ctx *ctx, cudaError_t e) { return cuda_fail(ctx, e); }
+
+void ctx_launched(lora_ctx *ctx, cudaStream_t stream, int path)
+{
+    count_launch(ctx, stream);
+    ctx->last_path |= path;
+}
+
+unsigned *ctx_status(const lora_ctx *ctx) { return ctx->d_status; }
+int ctx_device(const lora_ctx *ctx) { return ctx->device; }
+int ctx_sms(const lora_ctx *ctx) { return ctx->sms; }
+
+int ctx_attn_scratch(lora_ctx *ctx, size_t bytes, uint8_t **out)
+{
+    if (!ctx->attn) {
+        void *p = nullptr;
+        if (cudaMalloc(&p, bytes) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return LORA_E_NOMEM;
+        }
+        const cudaError_t e = cudaMemset(p, 0, bytes);
+        if (e != cudaSuccess) {
+            cudaFree(p);
+            return cuda_fail(ctx, e);
+        }
+        ctx->attn = static_cast<uint8_t *>(p);
+        ctx->attn_bytes = bytes;
+    }
+    *out = ctx->attn;
+    return ctx->attn_bytes >= bytes ? LORA_OK : LORA_E_NOMEM;
+}
+
+}  // namespace lora
+
 extern "C" {
 
 int lora_version(void) { return 1; }
@@ -1156,6 +1204,7 @@ int lora_ctx_create(int device, int64_t max_rows, int max_rank, lora_ctx **out)
     if (!ctx)
         return LORA_E_NOMEM;
     ctx->device = device;
+    ctx->sms = prop.multiProcessorCount;
     ctx->max_rows = max_rows;
     ctx->max_rank = max_rank;
     // Plans up to max_rows never grow these again.
@@ -1243,6 +1292,8 @@ int lora_ctx_destroy(lora_ctx *ctx)
         cudaFree(ctx->aprep);
     if (ctx->dense)
         cudaFree(ctx->dense);
+    if (ctx->attn)
+        cudaFree(ctx->attn);
     if (ctx->flush)
         cudaFree(ctx->flush);
     cudaSetDevice(prev);
@@ -1923,7 +1974,8 @@ int lora_sync_status(lora_ctx *ctx, void *stream)
     CUDA_TRY(ctx, cudaMemcpy(&word, ctx->d_status, sizeof word, cudaMemcpyDeviceToHost));
     if (word != 0) {
         CUDA_TRY(ctx, cudaMemset(ctx->d_status, 0, sizeof word));
-        return word == kDevBadId ? LORA_E_ADAPTER : LORA_E_TIMEOUT;
+        return word == kDevBadId ? LORA_E_ADAPTER : word == kDevBadBatch ? LORA_E_INVAL
+               : word == kDevBadPage ? LORA_E_PAGE : LORA_E_TIMEOUT;
     }
     return LORA_OK;
 }

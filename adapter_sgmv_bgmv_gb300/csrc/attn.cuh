@@ -1,0 +1,235 @@
+// What the two attention kernels share: the spans of keys a tile of query rows reads,
+// the even split of all spans over the CTAs, and the rule for rows with a result that
+// is not finite.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "kv.cuh"
+#include "ptx.cuh"
+
+namespace lora {
+
+// A unit is one tile of query rows of one (sequence, key head): the `group` query heads
+// that share the key head, token by token, so rho = token * group + head in the group,
+// rho in [r * ROWS, (r + 1) * ROWS).  It reads the keys [0, sink) and [lo, hi) in tiles
+// of TOK keys: the window's union over its tokens and the first tokens ahead of it.
+struct Span {
+    int p0;                   // position of the tile's first token (may be negative)
+    int lo, hi, sink;
+    int n_sink, n;            // tiles of the first tokens, and in all (at least one)
+};
+
+template <int ROWS, int TOK>
+__device__ __forceinline__ Span span_of(const SeqInfo &q, int r, int group, int window, int sinks)
+{
+    Span s;
+    const int rho1 = min((r + 1) * ROWS, q.n_new * group) - 1;
+    const int base = q.len - q.n_new;
+    s.p0 = base + r * ROWS / group;
+    const int p1 = base + rho1 / group;
+    s.hi = max(p1 + 1, 0);
+    s.lo = window ? min(max(s.p0 - window + 1, 0), s.hi) : 0;
+    s.sink = min(sinks, s.lo);
+    s.n_sink = (s.sink + TOK - 1) / TOK;
+    s.n = max(1, s.n_sink + (s.hi - s.lo + TOK - 1) / TOK);
+    return s;
+}
+
+__device__ __forceinline__ int row_tiles(int n_new, int group, int rows)
+{
+    return int((int64_t(n_new) * group + rows - 1) / rows);
+}
+
+// The even split.  All units' tiles, one after another (sequence, then row tile, then key
+// head, then tile), are cut into equal shares, one per CTA; a CTA finds its own share
+// from the lengths in device memory, so no plan is made ahead and nothing is read on the
+// host.  Only sequences with min_rows <= rows < max_rows (rows = new tokens * group)
+// take part: the rest are another kernel's.
+struct Cursor {
+    int64_t at;               // the unit's first tile among all tiles
+    int s, r, h;              // the unit
+    SeqInfo q;
+    Span span;
+};
+
+template <int ROWS, int TOK>
+struct Split {
+    static __device__ __forceinline__ bool mine(const AttnParams &p, const SeqInfo &q)
+    {
+        const int64_t rows = int64_t(q.n_new) * p.group;
+        return rows >= p.min_rows && rows < p.max_rows;
+    }
+
+    static __device__ int64_t cost(const AttnParams &p, int s)
+    {
+        if (s >= p.b.n_seqs)
+            return 0;
+        const SeqInfo q = seq_info(p.b, s, blockIdx.x == 0 ? p.status : nullptr);
+        if (!mine(p, q))
+            return 0;
+        int64_t n = 0;
+        const int tiles = row_tiles(q.n_new, p.group, ROWS);
+        for (int r = 0; r < tiles; ++r)
+            n += span_of<ROWS, TOK>(q, r, p.group, p.window, p.sinks).n;
+        return n * p.kv.heads;
+    }
+
+    // Inclusive scan over the block; `sums` holds one entry per warp.
+    template <int THREADS>
+    static __device__ int64_t scan(int64_t v, int64_t *sums, int64_t &total)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        long long x = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d)
+                x += y;
+        }
+        __syncthreads();
+        if (lane == 31)
+            sums[warp] = x;
+        __syncthreads();
+        int64_t before = 0;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp)
+                before += sums[w];
+            total += sums[w];
+        }
+        return before + x;
+    }
+
+    // The share of CTA `cta` of `n_cta`: tiles [x0, x1) and the cursor of the unit that
+    // holds x0.  Returns the share's size (`share`; every CTA but the last has it), or 0
+    // when this CTA has no tiles.
+    template <int THREADS>
+    static __device__ int64_t find(const AttnParams &p, int n_cta, int64_t *sums, Cursor *found,
+                                   int64_t &x0, int64_t &x1)
+    {
+        const int tid = threadIdx.x;
+        int64_t total = 0;
+        for (int base = 0; base < p.b.n_seqs; base += THREADS) {
+            int64_t t;
+            scan<THREADS>(cost(p, base + tid), sums, t);
+            total += t;
+        }
+        const int64_t share = (total + n_cta - 1) / n_cta;
+        x0 = share * blockIdx.x;
+        x1 = min(x0 + share, total);
+        if (x0 >= x1)
+            return 0;
+        int64_t before = 0;
+        for (int base = 0; base < p.b.n_seqs; base += THREADS) {
+            int64_t t;
+            const int64_t c = cost(p, base + tid);
+            const int64_t upto = before + scan<THREADS>(c, sums, t);
+            if (upto > x0 && upto - c <= x0) {
+                Cursor u;
+                u.s = base + tid;
+                u.q = seq_info(p.b, u.s, nullptr);
+                u.at = upto - c;
+                u.r = 0;
+                while (true) {
+                    u.span = span_of<ROWS, TOK>(u.q, u.r, p.group, p.window, p.sinks);
+                    const int64_t w = int64_t(u.span.n) * p.kv.heads;
+                    if (u.at + w > x0)
+                        break;
+                    u.at += w;
+                    ++u.r;
+                }
+                u.h = int((x0 - u.at) / u.span.n);
+                u.at += int64_t(u.h) * u.span.n;
+                *found = u;
+            }
+            before += t;
+            if (before > x0)
+                break;
+        }
+        __syncthreads();
+        return share;
+    }
+
+    // The unit after `u` (the caller knows that there is one).
+    static __device__ void next(const AttnParams &p, Cursor &u)
+    {
+        u.at += u.span.n;
+        if (++u.h < p.kv.heads)
+            return;
+        u.h = 0;
+        ++u.r;
+        if (u.r >= row_tiles(u.q.n_new, p.group, ROWS)) {
+            u.r = 0;
+            do {
+                ++u.s;
+                u.q = seq_info(p.b, u.s, nullptr);
+            } while (!mine(p, u.q) && u.s + 1 < p.b.n_seqs);
+        }
+        u.span = span_of<ROWS, TOK>(u.q, u.r, p.group, p.window, p.sinks);
+    }
+};
+
+// One row computed on its own, key by key, with no product for a key it does not see:
+// for a row whose tile gave a result that is not finite.  There the keys other rows of
+// the tile see may hold an infinity or a NaN, which a zero weight does not take out of
+// the tile's product; here they are never multiplied.  `q` is the row's query, `pos` its
+// position; a whole warp, lane l holds elements d = l, l + 32, ...; returns them in o.
+template <int DIM, int FMT>
+__device__ void careful_row(const AttnParams &p, const SeqInfo &s, int seq, int head, int pos,
+                            const uint16_t *q, float o[DIM / 32])
+{
+    constexpr int N = DIM / 32;
+    const int lane = threadIdx.x & 31;
+    float qf[N], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        qf[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(q)[lane + 32 * e]);
+        o[e] = 0.f;
+    }
+    for (int j = 0; j <= pos; ++j) {
+        if (!sees(pos, j, p.window, p.sinks))
+            continue;
+        const int jp = page_of(p.kv, j);
+        const int page = p.b.pages[int64_t(seq) * p.b.ld_pages + jp];
+        const bool there = page >= 0 && page < p.kv.n_pages;
+        const int cell = j - jp * p.kv.page_size;
+        const int64_t at = there ? page * p.kv.page_stride + cell * p.kv.cell_stride + head * p.kv.head_stride : 0;
+        const int64_t sat = there ? page * p.kv.s_page + cell * p.kv.s_cell + head * p.kv.s_head : 0;
+        float kf[N], vf[N], dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int d = lane + 32 * e;
+            float a, b;
+            if (FMT == kKvBf16) {
+                a = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.kv.k + at)[d]);
+                b = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.kv.v + at)[d]);
+            } else if (FMT == kKvInt8) {
+                a = float(reinterpret_cast<const int8_t *>(p.kv.k + at)[d]) * p.kv.k_scale[sat];
+                b = float(reinterpret_cast<const int8_t *>(p.kv.v + at)[d]) * p.kv.v_scale[sat];
+            } else {
+                a = float(reinterpret_cast<const __nv_fp8_e4m3 *>(p.kv.k + at)[d]) * p.kv.k_scale[sat];
+                b = float(reinterpret_cast<const __nv_fp8_e4m3 *>(p.kv.v + at)[d]) * p.kv.v_scale[sat];
+            }
+            kf[e] = there ? a : 0.f;
+            vf[e] = there ? b : 0.f;
+            dot = fmaf(qf[e], kf[e], dot);
+        }
+        const float sc = warp_sum(dot) * p.scale;
+        const float mn = fmaxf(m, sc), ref = mn == -INFINITY ? 0.f : mn;
+        const float a = expf(m - ref), w = sc == INFINITY ? __int_as_float(0x7fffffff) : expf(sc - ref);
+        m = mn;
+        l = l * a + w;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            o[e] = o[e] * a + w * vf[e];
+    }
+    const float inv = l > 0.f ? 1.f / l : l;            // no key: 0; a NaN stays one
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        o[e] = l == 0.f ? 0.f : o[e] * inv;
+}
+
+}  // namespace lora

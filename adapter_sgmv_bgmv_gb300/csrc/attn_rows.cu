@@ -1,0 +1,558 @@
+// Attention of a few new tokens over the paged cache: decode batches and short chunks.
+//
+//   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q.k_j - m),  m = the running maximum
+//
+// over the keys j a row sees.  Every key and value is read from DRAM once per 16 query
+// rows (the group that shares a key head, and a few tokens), so at one new token the
+// bytes of the cache bound it: 16 rows are one m16n8k16 tensor-core tile (bf16 in, fp32
+// sums), whose arithmetic is a few percent of the time the bytes take.
+//
+// Layout.  All (sequence, key head, 16 rows) units are cut into tiles of kWarps * BT
+// keys and the tiles split evenly over the CTAs (attn.cuh).  Each warp has its own BT
+// keys of a tile, its own ring of ST stages in shared memory filled by 16-byte
+// cp.async (any page size, any strides: each row of a stage has its own address), and
+// its own running maximum, sum and output; the warps meet only at the end of a unit.
+// A unit that is spread over CTAs leaves its parts in scratch and the CTA that arrives
+// last adds them in the order of the CTAs, so the result does not depend on the order of
+// arrival.
+//
+// 8-bit keys and values become bf16 in registers between ldmatrix and the product (every
+// code is exact in bf16).  A key's scale multiplies its column of scores, a value's scale
+// its weight.  The second product takes each weight as two bf16 terms (the rounded weight
+// and what the rounding left), about 16 significant bits: the tensor cores have the time,
+// and one bf16 term was measured to add up to a bf16 step to an output.
+#include <cuda_runtime.h>
+
+#include "attn.cuh"
+#include "tc.cuh"
+
+namespace lora {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 16;
+
+template <int DIM, int FMT>
+struct Shape {
+    static constexpr int ES = FMT == kKvBf16 ? 2 : 1;
+    static constexpr int RB = DIM * ES;                    // bytes of a key row
+    static constexpr int BT = FMT == kKvBf16 && DIM == 128 ? 16 : 32;
+    static constexpr int ST = 3;
+    static constexpr int TOK = kWarps * BT;
+    static constexpr int SCALES = FMT == kKvBf16 ? 0 : BT * 8;
+    static constexpr int STAGE = 2 * BT * RB + SCALES;
+    static constexpr int RING = kWarps * ST * STAGE;
+    static constexpr int MERGE = kWarps * kRows * DIM * 4;
+    static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + kWarps * kRows * 8 + 1024;
+};
+
+// Byte offset of 16-byte chunk c of row r: rows of RB bytes, chunks exchanged so that
+// eight rows' same chunk lie in different banks.
+template <int RB>
+__device__ __forceinline__ uint32_t cell_at(uint32_t r, uint32_t c)
+{
+    if (RB >= 128)
+        return r * RB + ((c ^ (r & 7u)) << 4);
+    return r * RB + ((c ^ ((r >> 1) & 3u)) << 4);          // 64-byte rows: two share 128 bytes
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t r[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t r[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+
+__device__ __forceinline__ void mma(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t bf2(float lo, float hi)
+{
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+
+// Four codes (bytes b0..b3) to the bf16 pairs (b0, b2) and (b1, b3).
+template <int FMT>
+__device__ __forceinline__ void widen(uint32_t r, uint32_t &even, uint32_t &odd)
+{
+    if (FMT == kKvInt8) {
+        // 128 + the low seven bits, less 128 or (sign bit) 256: exact in bf16
+        const uint32_t o = r >> 8;
+        const uint32_t e1 = (r & 0x007f007fu) | 0x43004300u, e0 = (r & 0x00800080u) | 0x43004300u;
+        const uint32_t o1 = (o & 0x007f007fu) | 0x43004300u, o0 = (o & 0x00800080u) | 0x43004300u;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(even) : "r"(e1), "r"(e0));
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(o1), "r"(o0));
+    } else {
+        const uint32_t s = __byte_perm(r, 0, 0x3120);      // b0 b2 b1 b3
+        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(s & 0xffffu), __NV_E4M3);
+        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(s >> 16), __NV_E4M3);
+        const float2 fa = __half22float2(__half2(a)), fb = __half22float2(__half2(b));
+        even = bf2(fa.x, fa.y);
+        odd = bf2(fb.x, fb.y);
+    }
+}
+
+
+template <int DIM, int FMT>
+__global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant__ AttnParams p)
+{
+    using S = Shape<DIM, FMT>;
+    using Cut = Split<kRows, S::TOK>;
+    constexpr int BT = S::BT, ST = S::ST, RB = S::RB;
+    constexpr int NT = BT / 8;                             // 8-key tiles of scores
+    constexpr int KS = DIM / 16;                           // k-steps of q.k
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    __shared__ int64_t sums[kWarps];
+    __shared__ Cursor found;
+    __shared__ int last_flag;
+    __shared__ float row_sum[kRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, g = lane >> 2;
+    const KvView &kv = p.kv;
+    const BatchView &b = p.b;
+
+    grid_dep_wait();
+    grid_dep_launch();
+
+    int64_t x0, x1;
+    const int64_t share = Cut::template find<kThreads>(p, gridDim.x, sums, &found, x0, x1);
+    if (share == 0)
+        return;
+    Cursor u = found;
+    const uint32_t ring = smem_u32(smem) + warp * ST * S::STAGE;
+    float2 *ml = reinterpret_cast<float2 *>(smem + (S::RING > S::MERGE ? S::RING : S::MERGE));
+    const float sl = p.scale * 1.4426950408889634f;        // scores in powers of two
+
+    for (int64_t x = x0; x < x1;) {
+        const int t0 = int(x - u.at), t1 = int(min(x1 - u.at, int64_t(u.span.n)));
+        const int n_rows = min(kRows, u.q.n_new * p.group - u.r * kRows);
+        const int base = u.q.len - u.q.n_new;
+        const uint8_t *kp = kv.k + u.h * kv.head_stride, *vp = kv.v + u.h * kv.head_stride;
+        const int32_t *pages = b.pages + int64_t(u.s) * b.ld_pages;
+
+        // this thread's rows g and g + 8: position, query (as the products want it)
+        int pos[2];
+        uint32_t qf[KS][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = g + 8 * i, rho = u.r * kRows + row;
+            const bool on = row < n_rows;
+            pos[i] = on ? base + rho / p.group : -1;
+            const uint16_t *src = p.q + int64_t(u.q.start + rho / p.group) * p.ldq +
+                                  (u.h * p.group + rho % p.group) * DIM;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                if (FMT == kKvBf16) {
+                    qf[k][i] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 2 * c) : 0u;
+                    qf[k][i + 2] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 8 + 2 * c) : 0u;
+                } else {
+                    // the codes of d = 4c .. 4c + 3 arrive as pairs (0, 2) and (1, 3)
+                    const uint2 w = on ? *reinterpret_cast<const uint2 *>(src + 16 * k + 4 * c) : make_uint2(0, 0);
+                    qf[k][i] = __byte_perm(w.x, w.y, 0x5410);
+                    qf[k][i + 2] = __byte_perm(w.x, w.y, 0x7632);
+                }
+            }
+        }
+
+        float o[DIM / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < DIM / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[i][e] = 0.f;
+
+        // first position of this warp's keys in tile t, and the end of the keys to read
+        auto keys = [&](int t, int &j0, int &j1) {
+            if (t < u.span.n_sink) {
+                j0 = t * S::TOK + warp * BT;
+                j1 = u.span.sink;
+            } else {
+                j0 = u.span.lo + (t - u.span.n_sink) * S::TOK + warp * BT;
+                j1 = u.span.hi;
+            }
+        };
+        auto page_at = [&](int t) -> int {                 // page id of this lane's key of tile t
+            int j0, j1;
+            keys(t, j0, j1);
+            const int j = j0 + lane;
+            if (t >= t1 || lane >= BT || j >= j1)
+                return -1;
+            const int page = pages[page_of(kv, j)];
+            if (page < 0 || page >= kv.n_pages) {
+                raise_status(p.status, kDevBadPage);
+                return -1;
+            }
+            return page;
+        };
+        auto issue = [&](int t, int page) {                // copies of tile t into its stage
+            if (t < t1) {
+                int j0, j1;
+                keys(t, j0, j1);
+                const int cell = j0 + lane - page_of(kv, j0 + lane) * kv.page_size;
+                const int64_t at = page < 0 ? -1 : page * kv.page_stride + cell * kv.cell_stride;
+                const uint32_t st = ring + uint32_t(t % ST) * S::STAGE;
+                constexpr int CH = RB / 16, RPI = 32 / CH; // chunks a row, rows an instruction
+#pragma unroll
+                for (int i = 0; i < BT / RPI; ++i) {
+                    const int r = i * RPI + lane / CH, ch = lane % CH;
+                    const int64_t a = __shfl_sync(0xffffffffu, (long long)at, r);
+                    const uint32_t n = a < 0 ? 0u : 16u;
+                    const int64_t off = a < 0 ? 0 : a + ch * 16;
+                    tc::cp_async16(st + cell_at<RB>(r, ch), kp + off, n);
+                    tc::cp_async16(st + BT * RB + cell_at<RB>(r, ch), vp + off, n);
+                }
+                if (FMT != kKvBf16 && lane < BT) {
+                    const int64_t sa = page < 0 ? 0 : page * kv.s_page + cell * kv.s_cell + u.h * kv.s_head;
+                    const uint32_t n = page < 0 ? 0u : 4u;
+                    const uint32_t d = st + 2 * BT * RB + lane * 4;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(kv.k_scale + sa), "r"(n) : "memory");
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d + BT * 4), "l"(kv.v_scale + sa), "r"(n) : "memory");
+                }
+            }
+            tc::cp_async_commit();
+        };
+
+        int pid[ST];
+#pragma unroll
+        for (int i = 0; i < ST; ++i)
+            pid[i] = page_at(t0 + i);
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i)
+            issue(t0 + i, pid[i]);
+        int page_next = pid[ST - 1];
+
+        for (int t = t0; t < t1; ++t) {
+            tc::cp_async_wait<ST - 2>();
+            __syncwarp();
+            int j0, j1;
+            keys(t, j0, j1);
+            const uint32_t st = ring + uint32_t(t % ST) * S::STAGE;
+            if (j0 < j1) {
+                // scores of 16 rows x BT keys
+                float s[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[n][e] = 0.f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint32_t row = n * 8 + (lane & 7);
+                    if (FMT == kKvBf16) {
+#pragma unroll
+                        for (int k = 0; k < KS; k += 2) {  // four 8 x 8 blocks: two k-steps
+                            uint32_t f[4];
+                            ldsm4(st + cell_at<RB>(row, 2 * k + (lane >> 3)), f);
+                            mma(s[n], qf[k], f[0], f[1]);
+                            mma(s[n], qf[k + 1], f[2], f[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < KS; k += 4) {  // four k-steps
+                            uint32_t f[4];
+                            ldsm4(st + cell_at<RB>(row, k + (lane >> 3)), f);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t lo, hi;
+                                widen<FMT>(f[e], lo, hi);
+                                mma(s[n], qf[k + e], lo, hi);
+                            }
+                        }
+                    }
+                }
+                // scale, mask, running maximum
+                const float *sc = reinterpret_cast<const float *>(smem + (st - smem_u32(smem)) + 2 * BT * RB);
+                float mx[2] = {m[0], m[1]};
+                const int je = min(j0 + BT, j1);
+                const bool all = je - 1 <= u.span.p0 && je - j0 == BT &&
+                                 (p.window == 0 || t < u.span.n_sink || j0 > base + (u.r * kRows + n_rows - 1) / p.group - p.window);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float ks[2] = {sl, sl};
+                    if (FMT != kKvBf16) {
+                        const float2 t2 = *reinterpret_cast<const float2 *>(sc + n * 8 + 2 * c);
+                        ks[0] *= t2.x;
+                        ks[1] *= t2.y;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v = s[n][e] * ks[e & 1];
+                        if (!all) {
+                            const int j = j0 + n * 8 + 2 * c + (e & 1);
+                            if (j >= j1 || !sees(pos[e >> 1], j, p.window, p.sinks))
+                                v = -INFINITY;
+                        }
+                        s[n][e] = v;
+                        mx[e >> 1] = fmaxf(mx[e >> 1], v);
+                    }
+                }
+                float ref[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+                    ref[i] = mx[i] == -INFINITY ? 0.f : mx[i];
+                    const float a = exp2f(m[i] - ref[i]);
+                    m[i] = mx[i];
+                    l[i] *= a;
+#pragma unroll
+                    for (int d = 0; d < DIM / 8; ++d) {
+                        o[d][2 * i] *= a;
+                        o[d][2 * i + 1] *= a;
+                    }
+                }
+                // weights, as the left operand of the second product
+                uint32_t w[BT / 16][4], wl[BT / 16][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float vs[2] = {1.f, 1.f};
+                    if (FMT != kKvBf16) {
+                        const float2 t2 = *reinterpret_cast<const float2 *>(sc + BT + n * 8 + 2 * c);
+                        vs[0] = t2.x;
+                        vs[1] = t2.y;
+                    }
+                    float e[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float v = exp2f(s[n][i] - ref[i >> 1]);
+                        l[i >> 1] += v;
+                        // a key that is not seen has weight 0 whatever its scale is
+                        e[i] = FMT == kKvBf16 ? v : s[n][i] == -INFINITY ? 0.f : v * vs[i & 1];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t hi = bf2(e[2 * i], e[2 * i + 1]);
+                        w[n / 2][(n & 1) * 2 + i] = hi;
+                        wl[n / 2][(n & 1) * 2 + i] = bf2(e[2 * i] - __uint_as_float(hi << 16),
+                                                         e[2 * i + 1] - __uint_as_float(hi & 0xffff0000u));
+                    }
+                }
+                // o += w v
+                const uint32_t sv = st + BT * RB;
+#pragma unroll
+                for (int kk = 0; kk < BT / 16; ++kk) {
+                    const uint32_t row = kk * 16 + (lane & 15);
+                    if (FMT == kKvBf16) {
+#pragma unroll
+                        for (int d = 0; d < DIM / 16; ++d) {
+                            uint32_t f[4];
+                            ldsm4t(sv + cell_at<RB>(row, 2 * d + (lane >> 4)), f);
+                            mma(o[2 * d], w[kk], f[0], f[1]);
+                            mma(o[2 * d + 1], w[kk], f[2], f[3]);
+                            mma(o[2 * d], wl[kk], f[0], f[1]);
+                            mma(o[2 * d + 1], wl[kk], f[2], f[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int d = 0; d < DIM / 16; d += 2) {   // 16-element chunks d, d + 1
+                            uint32_t f[4], e0, o0, e1, o1;
+                            ldsm4t(sv + cell_at<RB>(row, d + (lane >> 4)), f);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                widen<FMT>(f[2 * e], e0, o0);
+                                widen<FMT>(f[2 * e + 1], e1, o1);
+                                mma(o[2 * (d + e)], w[kk], e0, e1);
+                                mma(o[2 * (d + e) + 1], w[kk], o0, o1);
+                                mma(o[2 * (d + e)], wl[kk], e0, e1);
+                                mma(o[2 * (d + e) + 1], wl[kk], o0, o1);
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            const int ahead = page_at(t + ST);
+            issue(t + ST - 1, page_next);
+            page_next = ahead;
+        }
+        tc::cp_async_wait<0>();
+
+        // The warps' results meet.  Element d of the output tile held as o[i][e]:
+        // bf16 pools: 8i + 2c + (e & 1); 8-bit pools: tiles come in even / odd pairs of
+        // one 16-wide chunk, 16 (i / 2) + 4c + 2 (e & 1) + (i & 1).
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        }
+        __syncthreads();                                   // every warp is done with its ring
+        float *mo = reinterpret_cast<float *>(smem);       // [warp][row][DIM]
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = g + 8 * i;
+            if (row < n_rows) {
+                float *dst = mo + (warp * kRows + row) * DIM;
+                if (c == 0)
+                    ml[warp * kRows + row] = make_float2(m[i], l[i]);
+#pragma unroll
+                for (int d = 0; d < DIM / 8; ++d) {
+                    if (FMT == kKvBf16) {
+                        *reinterpret_cast<float2 *>(dst + 8 * d + 2 * c) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
+                    } else if ((d & 1) == 0) {
+                        *reinterpret_cast<float4 *>(dst + 8 * d + 4 * c) =
+                            make_float4(o[d][2 * i], o[d + 1][2 * i], o[d][2 * i + 1], o[d + 1][2 * i + 1]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == u.span.n;
+        const int64_t first = u.at / share, final_ = (u.at + u.span.n - 1) / share;
+        constexpr int V4 = DIM / 4;
+        float *po = p.part_o;
+        float2 *pm = p.part_ml;
+        const int slot = int(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0);
+        for (int e = threadIdx.x; e < n_rows * V4; e += kThreads) {
+            const int row = e / V4, d = (e % V4) * 4;
+            float mm = -INFINITY, ll = 0.f;
+            float2 wml[kWarps];
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                wml[i] = ml[i * kRows + row];
+                mm = fmaxf(mm, wml[i].x);
+            }
+            const float ref = mm == -INFINITY ? 0.f : mm;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float a = exp2f(wml[i].x - ref);
+                ll += wml[i].y * a;
+                const float4 v = *reinterpret_cast<const float4 *>(mo + (i * kRows + row) * DIM + d);
+                acc.x += a * v.x;
+                acc.y += a * v.y;
+                acc.z += a * v.z;
+                acc.w += a * v.w;
+            }
+            if (!whole) {
+                *reinterpret_cast<float4 *>(po + (int64_t(slot) * kRows + row) * DIM + d) = acc;
+                if (d == 0)
+                    pm[int64_t(slot) * kRows + row] = make_float2(mm, ll);
+            } else {
+                *reinterpret_cast<float4 *>(mo + row * DIM + d) = acc;   // read by this thread only
+                if (d == 0)
+                    row_sum[row] = ll;
+            }
+        }
+        bool finish = whole;
+        if (!whole) {
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0)
+                last_flag = atomicAdd(&p.arrived[first], 1) == int(final_ - first);
+            __syncthreads();
+            finish = last_flag != 0;
+            if (finish) {
+                __threadfence();
+                if (threadIdx.x == 0)
+                    p.arrived[first] = 0;
+                for (int e = threadIdx.x; e < n_rows * V4; e += kThreads) {
+                    const int row = e / V4, d = (e % V4) * 4;
+                    float mm = -INFINITY, ll = 0.f;
+                    for (int64_t i = first; i <= final_; ++i)
+                        mm = fmaxf(mm, __ldcg(&pm[(i * 2 + (i == first)) * kRows + row]).x);
+                    const float ref = mm == -INFINITY ? 0.f : mm;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int64_t i = first; i <= final_; ++i) {
+                        const int64_t at = (i * 2 + (i == first)) * kRows + row;
+                        const float2 w = __ldcg(&pm[at]);
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(po + at * DIM + d));
+                        const float a = exp2f(w.x - ref);
+                        ll += w.y * a;
+                        acc.x += a * v.x;
+                        acc.y += a * v.y;
+                        acc.z += a * v.z;
+                        acc.w += a * v.w;
+                    }
+                    *reinterpret_cast<float4 *>(mo + row * DIM + d) = acc;
+                    if (d == 0)
+                        row_sum[row] = ll;
+                }
+            }
+        }
+        if (finish) {
+            __syncthreads();
+            // one warp a row: the quotient, and the check that it is finite
+            for (int row = warp; row < n_rows; row += kWarps) {
+                const int rho = u.r * kRows + row, tok = rho / p.group;
+                const float ll = row_sum[row];
+                float f[DIM / 32];
+                bool ok = true;
+#pragma unroll
+                for (int e = 0; e < DIM / 32; ++e) {
+                    f[e] = ll == 0.f ? 0.f : mo[row * DIM + lane + 32 * e] / ll;
+                    ok = ok && fabsf(f[e]) < INFINITY;
+                }
+                const int64_t col = (u.h * p.group + rho % p.group) * DIM;
+                if (!__all_sync(0xffffffffu, ok))
+                    careful_row<DIM, FMT>(p, u.q, u.s, u.h, base + tok,
+                                          p.q + int64_t(u.q.start + tok) * p.ldq + col, f);
+                uint16_t *dst = p.out + int64_t(u.q.start + tok) * p.ldo + col;
+#pragma unroll
+                for (int e = 0; e < DIM / 32; ++e)
+                    reinterpret_cast<__nv_bfloat16 *>(dst)[lane + 32 * e] = __float2bfloat16_rn(f[e]);
+            }
+        }
+        __syncthreads();                                   // the ring and `found` are free again
+        x = u.at + t1;
+        if (x < x1)
+            Cut::next(p, u);
+    }
+}
+
+template <int DIM, int FMT>
+cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream)
+{
+    static bool configured = false;
+    if (!configured) {
+        cudaError_t e = cudaFuncSetAttribute(k_attn_rows<DIM, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Shape<DIM, FMT>::SMEM);
+        if (e != cudaSuccess)
+            return e;
+        configured = true;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(2 * sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Shape<DIM, FMT>::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_attn_rows<DIM, FMT>, p);
+}
+
+}  // namespace
+
+AttnScratch attn_rows_scratch(int sms)
+{
+    const size_t slots = size_t(sms) * 2 * 2;
+    return {slots * kRows * 128 * sizeof(float), slots * kRows * sizeof(float2), size_t(sms) * 2 * sizeof(int)};
+}
+
+cudaError_t launch_attn_rows(const AttnParams &p, int sms, cudaStream_t stream)
+{
+    const bool wide = p.kv.dim == 128;
+    switch (p.kv.format) {
+    case kKvBf16: return wide ? launch<128, kKvBf16>(p, sms, stream) : launch<64, kKvBf16>(p, sms, stream);
+    case kKvInt8: return wide ? launch<128, kKvInt8>(p, sms, stream) : launch<64, kKvInt8>(p, sms, stream);
+    default: return wide ? launch<128, kKvFp8>(p, sms, stream) : launch<64, kKvFp8>(p, sms, stream);
+    }
+}
+
+}  // namespace lora

@@ -1,0 +1,231 @@
+// Writing new keys and values into the pages of the cache, and reading cached ones
+// back as bf16 rows.
+//
+// One vector is the dim elements of one (row, head): dim / 8 lanes take 8 elements
+// (16 bytes of bf16) each.  A CTA serves one row: its warps find the row's sequence
+// and cell once, then go over the 2 * heads vectors (keys, then values).
+//
+// 8-bit formats, per vector: scale = max |x| / T (T = 127 for int8, 448 for e4m3; one
+// fp32 division, rounded to nearest), code = x / scale rounded to nearest even and
+// limited to +-T.  x / scale is a true division: the code is the nearest one, not one
+// off at a tie as with a rounded reciprocal.  A vector that holds an infinity or a
+// NaN gets a NaN scale and zero codes, so it reads back as NaN; a zero vector gets
+// scale 0.
+//
+// Bound: DRAM at prefill sizes (the vectors are read and written once), and one
+// launch plus three dependent loads (starts and lens, page id, data) for a decode batch.
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "kv.h"
+#include "ptx.cuh"
+
+#include "kv.cuh"
+
+namespace lora {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Row `row`'s place in the cache, found by a whole warp: byte offset of the page's
+// cell in the pools (without the head) and element offset in the scales.
+struct Place {
+    bool live;                // the row belongs to a sequence of the batch
+    bool stored;              // ... and has a position and a valid page
+    int64_t at, s_at;
+};
+
+__device__ __forceinline__ Place find_row(const KvView &kv, const BatchView &b, int row,
+                                          unsigned *status)
+{
+    const int lane = threadIdx.x & 31;
+    Place pl{false, false, 0, 0};
+    // A decode batch has one row per sequence: row r is sequence r.  Otherwise a
+    // 32-way search for the last sequence that starts at or before the row.
+    int s = row;
+    bool hit = s < b.n_seqs && b.starts[s] == row && b.starts[s + 1] == row + 1;
+    if (!hit) {
+        int lo = 0, n = b.n_seqs;                    // starts[lo] <= row, answer in [lo, lo + n)
+        while (n > 1) {
+            const int step = (n + 31) / 32;
+            const int i = lo + lane * step;
+            const bool le = lane * step < n && b.starts[i] <= row;
+            const unsigned m = __ballot_sync(0xffffffffu, le);
+            const int last = m ? 31 - __clz(m) : 0;
+            n = min(step, n - last * step);
+            lo += last * step;
+        }
+        s = lo;
+    }
+    const SeqInfo q = seq_info(b, s, status);
+    if (row < q.start || row >= q.start + q.n_new)
+        return pl;
+    pl.live = true;
+    const int pos = q.len - q.n_new + (row - q.start);
+    if (pos < 0)
+        return pl;
+    const int j = page_of(kv, pos);
+    const int page = b.pages[int64_t(s) * b.ld_pages + j];
+    if (page < 0 || page >= kv.n_pages) {
+        raise_status(status, kDevBadPage);
+        return pl;
+    }
+    const int cell = pos - j * kv.page_size;
+    pl.stored = true;
+    pl.at = page * kv.page_stride + cell * kv.cell_stride;
+    pl.s_at = page * kv.s_page + cell * kv.s_cell;
+    return pl;
+}
+
+template <int DIM, int FMT>
+__global__ void __launch_bounds__(kThreads) k_kv_write(const __grid_constant__ KvRowsParams p)
+{
+    constexpr int kLanes = DIM / 8;                  // lanes per vector
+    constexpr int kPer = kThreads / kLanes;          // vectors per pass of the CTA
+    constexpr int kUnroll = 4;
+    const int row = blockIdx.x, sub = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
+    const KvView &kv = p.kv;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int nvec = 2 * kv.heads;
+    // the row's vectors are on their way while its place is looked up
+    for (int v0 = blockIdx.y * kPer * kUnroll; v0 < nvec; v0 += gridDim.y * kPer * kUnroll) {
+        uint4 x[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int vec = v0 + u * kPer + sub;
+            x[u] = uint4{0, 0, 0, 0};
+            if (vec < nvec) {
+                const bool is_v = vec >= kv.heads;
+                const uint16_t *src = is_v ? p.v + int64_t(row) * p.ldv : p.k + int64_t(row) * p.ldk;
+                x[u] = *reinterpret_cast<const uint4 *>(src + (is_v ? vec - kv.heads : vec) * DIM + l * 8);
+            }
+        }
+        const Place pl = find_row(kv, p.b, row, p.status);
+        if (!pl.stored)
+            return;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int vec = v0 + u * kPer + sub;
+            const bool on = vec < nvec;
+            const bool is_v = vec >= kv.heads;
+            const int head = on ? (is_v ? vec - kv.heads : vec) : 0;
+            uint8_t *dst = (is_v ? kv.v : kv.k) + pl.at + head * kv.head_stride;
+            if (FMT == kKvBf16) {
+                if (on)
+                    *reinterpret_cast<uint4 *>(dst + l * 16) = x[u];
+            } else {
+                float f[8];
+                unpack8(x[u], f);
+                float scale;
+                const uint2 code = encode8<FMT, kLanes>(f, scale);
+                if (on) {
+                    *reinterpret_cast<uint2 *>(dst + l * 8) = code;
+                    if (l == 0)
+                        (is_v ? kv.v_scale : kv.k_scale)[pl.s_at + head * kv.s_head] = scale;
+                }
+            }
+        }
+    }
+}
+
+template <int DIM, int FMT>
+__global__ void __launch_bounds__(kThreads) k_kv_read(const __grid_constant__ KvRowsParams p)
+{
+    constexpr int kLanes = DIM / 8;
+    constexpr int kPer = kThreads / kLanes;
+    constexpr int kUnroll = 4;
+    const int row = blockIdx.x, sub = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
+    const KvView &kv = p.kv;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int nvec = 2 * kv.heads;
+    const Place pl = find_row(kv, p.b, row, p.status);
+    if (!pl.live)
+        return;
+    for (int v0 = blockIdx.y * kPer * kUnroll; v0 < nvec; v0 += gridDim.y * kPer * kUnroll) {
+        uint4 x[kUnroll];
+        float scale[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int vec = v0 + u * kPer + sub;
+            x[u] = uint4{0, 0, 0, 0};
+            scale[u] = 0.f;
+            if (vec < nvec && pl.stored) {
+                const bool is_v = vec >= kv.heads;
+                const int head = is_v ? vec - kv.heads : vec;
+                const uint8_t *src = (is_v ? kv.v : kv.k) + pl.at + head * kv.head_stride;
+                if (FMT == kKvBf16) {
+                    x[u] = *reinterpret_cast<const uint4 *>(src + l * 16);
+                } else {
+                    const uint2 c = *reinterpret_cast<const uint2 *>(src + l * 8);
+                    x[u].x = c.x;
+                    x[u].y = c.y;
+                    scale[u] = (is_v ? kv.v_scale : kv.k_scale)[pl.s_at + head * kv.s_head];
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int vec = v0 + u * kPer + sub;
+            if (vec >= nvec)
+                continue;
+            const bool is_v = vec >= kv.heads;
+            uint16_t *dst = is_v ? p.v + int64_t(row) * p.ldv : p.k + int64_t(row) * p.ldk;
+            uint4 y = x[u];
+            if (FMT != kKvBf16 && pl.stored) {
+                float f[8];
+                decode8<FMT>(make_uint2(x[u].x, x[u].y), f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    f[e] *= scale[u];
+                y = pack8(f);
+            }
+            *reinterpret_cast<uint4 *>(dst + (is_v ? vec - kv.heads : vec) * DIM + l * 8) = y;
+        }
+    }
+}
+
+template <typename F>
+cudaError_t launch(F kernel, const KvRowsParams &p, cudaStream_t stream)
+{
+    // one CTA per row; rows of many vectors are split when the batch alone would not
+    // fill the SMs
+    const int per = kThreads / (p.kv.dim / 8) * 4;
+    const int parts = (2 * p.kv.heads + per - 1) / per;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(p.b.n_rows), unsigned(p.b.n_rows < 1024 ? parts : 1));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write(const KvRowsParams &p, cudaStream_t stream)
+{
+    const bool wide = p.kv.dim == 128;
+    switch (p.kv.format) {
+    case kKvBf16: return wide ? launch(k_kv_write<128, kKvBf16>, p, stream) : launch(k_kv_write<64, kKvBf16>, p, stream);
+    case kKvInt8: return wide ? launch(k_kv_write<128, kKvInt8>, p, stream) : launch(k_kv_write<64, kKvInt8>, p, stream);
+    default: return wide ? launch(k_kv_write<128, kKvFp8>, p, stream) : launch(k_kv_write<64, kKvFp8>, p, stream);
+    }
+}
+
+cudaError_t launch_kv_read(const KvRowsParams &p, cudaStream_t stream)
+{
+    const bool wide = p.kv.dim == 128;
+    switch (p.kv.format) {
+    case kKvBf16: return wide ? launch(k_kv_read<128, kKvBf16>, p, stream) : launch(k_kv_read<64, kKvBf16>, p, stream);
+    case kKvInt8: return wide ? launch(k_kv_read<128, kKvInt8>, p, stream) : launch(k_kv_read<64, kKvInt8>, p, stream);
+    default: return wide ? launch(k_kv_read<128, kKvFp8>, p, stream) : launch(k_kv_read<64, kKvFp8>, p, stream);
+    }
+}
+
+}  // namespace lora

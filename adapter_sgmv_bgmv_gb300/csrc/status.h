@@ -13,7 +13,9 @@ enum DeviceStatus : unsigned {
     kDevTimeoutMma = 2,    // a tensor-core commit did not arrive in time
     kDevTimeoutPipe = 3,   // a producer/consumer pipeline slot was not released
     kDevBadShape = 4,      // a kernel found a size it cannot handle (skipped)
-    kDevBadId = 5          // a device-resident adapter id the table cannot serve (row skipped)
+    kDevBadId = 5,         // a device-resident adapter id the table cannot serve (row skipped)
+    kDevBadBatch = 6,      // a sequence's rows or length out of range (sequence skipped)
+    kDevBadPage = 7        // a page id outside the cache's pools (its positions skipped)
 };
 
 }  // namespace lora

@@ -426,12 +426,95 @@ int lora_profile_end(lora_ctx *ctx, double *ms, int64_t *launches);
  * trap, no fault: the kernel ends normally. */
 int lora_selftest_timeout(lora_ctx *ctx, int64_t limit_us, void *stream);
 
+/* ------------------------------------------------------------ key/value cache
+ *
+ * A serving step's keys and values live in pages next to the adapters' (S-LoRA page,
+ * Unified Paging: one pool of pages holds both).  A cache is a pair of pools of
+ * n_pages pages of page_size cells; a cell holds n_heads vectors of head_dim elements,
+ * the keys (or values) of one token.  Element (page, cell, head, d) of the key pool is
+ *     k_pool + page * page_stride + cell * cell_stride + head * head_stride + d
+ * (strides in elements; the value pool has the same ones), so pools may be split or
+ * joint, cells or heads first, and pages of a unified adapter pool can be cells.
+ *
+ * Formats: LORA_KV_BF16; LORA_KV_INT8 and LORA_KV_FP8 (e4m3), 8-bit codes with one fp32
+ * scale for each (page, cell, head) in k_scale / v_scale, with strides of their own.  A
+ * cached vector stands for scale * code.  Writing x takes scale = max |x| / T (T = 127 or
+ * 448, one fp32 division) and code = x / scale to the nearest, ties to even; a vector
+ * with an infinity or a NaN gets a NaN scale and zero codes, and reads back as NaN.
+ *
+ * head_dim is 64 or 128.  Pool pointers and page, cell and head strides are multiples
+ * of 16 bytes.  The pools and scales stay caller-owned device memory and must outlive
+ * the cache; distinct (page, cell, head) must not overlap. */
+enum { LORA_KV_BF16 = 0, LORA_KV_INT8 = 1, LORA_KV_FP8 = 2 };
+typedef struct lora_kv lora_kv;
+typedef struct {
+    void *k_pool, *v_pool;
+    float *k_scale, *v_scale;      /* 8-bit formats, else ignored */
+    int64_t n_pages;
+    int page_size, n_heads, head_dim, format;
+    int64_t page_stride, cell_stride, head_stride;                    /* elements */
+    int64_t scale_page_stride, scale_cell_stride, scale_head_stride;  /* elements */
+} lora_kv_desc;
+
+/* The sequences of a call, in device memory (never read on the host, so a captured
+ * graph's replays see the values of the moment): rows [starts[s], starts[s + 1]) of the
+ * call's k / v / q / out belong to sequence s, in order, and are its last tokens; lens[s]
+ * is its length with them.  Row i of n_new is at position p = lens[s] - n_new + i, which
+ * is cell p % page_size of page pages[s * ld_pages + p / page_size].  A row with p < 0
+ * (a released slot of a fixed batch: length 0) has no position.  Rows past starts[n_seqs]
+ * belong to no sequence and are left alone.  max_new bounds every sequence's n_new.
+ *
+ * A sequence whose rows or length are out of range (starts not ascending or past n,
+ * n_new > max_new, length negative or beyond n_cols * page_size) is skipped and the
+ * next lora_sync_status returns LORA_E_INVAL; a page id the cache does not have makes
+ * it return LORA_E_PAGE, and that position is neither written nor read (it reads as
+ * zeros, and the attention's result for the sequence is of no use). */
+typedef struct {
+    const int32_t *starts;         /* [n_seqs + 1] */
+    const int32_t *lens;           /* [n_seqs] */
+    const int32_t *pages;          /* [n_seqs][ld_pages], n_cols of them used */
+    int64_t n_seqs, n_cols, ld_pages, max_new;
+} lora_kv_batch;
+
+/* Register a cache with a context.  The first one of a context allocates its attention
+ * scratch; no later call allocates.  LORA_E_UNSUPPORTED: head_dim; LORA_E_CAPACITY: 2^31
+ * pages or more, page_size above 2^20. */
+int lora_kv_create(lora_ctx *ctx, const lora_kv_desc *desc, lora_kv **out);
+int lora_kv_destroy(lora_kv *kv);
+
+/* Store the n rows of k and v ([n][n_heads * head_dim] bf16, row strides ldk / ldv) in
+ * their cells; rows without a position are skipped. */
+int lora_kv_write(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch, int64_t n,
+                  const void *k, int64_t ldk, const void *v, int64_t ldv, void *stream);
+
+/* The inverse: the cells of the rows' positions as bf16 rows (scale * code, rounded
+ * once); rows without a position become zeros.  With n_new = lens it reads whole
+ * sequences back. */
+int lora_kv_read(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch, int64_t n,
+                 void *k, int64_t ldk, void *v, int64_t ldv, void *stream);
+
+/* Attention of the batch's new tokens over the cache, which already holds them:
+ *     out_i = sum_j w_ij v_j / sum_j w_ij,   w_ij = exp(scale * q_i . k_j)
+ * over the positions j that row i (position p) sees: j <= p and, when window > 0,
+ * p - window < j or j < sinks (a sliding window and the first `sinks` tokens).  q and
+ * out are [n][n_heads * head_dim] bf16 with row strides ldq / ldo; n_heads is a
+ * multiple of the cache's heads, and query head h reads key head
+ * h / (n_heads / cache heads).  A row without a position gets zeros.  Positions a row
+ * does not see never reach its result, whatever they hold.  out may not overlap q.
+ * Scores, weights' sums and outputs are kept in fp32.  For the product with v, weights
+ * are taken as two bf16 terms (about 16 bits) for sequences of at most 16 rows
+ * (n_new * query heads per key head), and rounded to bf16 for longer ones. */
+int lora_attention(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch, int64_t n,
+                   const void *q, int64_t ldq, int n_heads, float scale, int window,
+                   int sinks, void *out, int64_t ldo, void *stream);
+
 /* Kernels launched by this context since it was created. */
 int64_t lora_launch_count(const lora_ctx *ctx);
 
 /* Which kernel the last call launched: 0 none, 1 row-gather, 2 tensor-core tile,
  * 3 both (delta calls), 4 merge / unmerge, 8 page-in, 16 base projection GEMM (with
- * the bits of the shrink kernels lora_base_fused launched before it); and how many
+ * the bits of the shrink kernels lora_base_fused launched before it), 32 cache write /
+ * read, 64 attention of few rows, 128 attention of many rows; and how many
  * kernels it launched. */
 int lora_last_path(const lora_ctx *ctx, int *n_launches);
 
