@@ -42,19 +42,21 @@ __device__ __forceinline__ int row_tiles(int n_new, int group, int rows)
     return int((int64_t(n_new) * group + rows - 1) / rows);
 }
 
-// The even split.  All units' tiles, one after another (sequence, then row tile, then key
-// head, then tile), are cut into equal shares, one per CTA; a CTA finds its own share
-// from the lengths in device memory, so no plan is made ahead and nothing is read on the
-// host.  Only sequences with min_rows <= rows < max_rows (rows = new tokens * group)
-// take part: the rest are another kernel's.
+// The even split.  All units, one after another (sequence, then row tile, then key head),
+// are laid on a line: a unit is as long as its tiles and OV more, for what a unit costs
+// besides them.  The line is cut into equal pieces, one per worker; a worker finds its own
+// piece from the lengths in device memory, so no plan is made ahead and nothing is read on
+// the host.  A piece [x0, x1) holds the tiles [x0 - at - OV, x1 - at - OV) of the unit at
+// `at`, as far as it has them.  Only sequences with min_rows <= rows < max_rows (rows =
+// new tokens * group) take part: the rest are another kernel's.
 struct Cursor {
-    int64_t at;               // the unit's first tile among all tiles
+    int64_t at;               // where the unit starts on the line
     int s, r, h;              // the unit
     SeqInfo q;
     Span span;
 };
 
-template <int ROWS, int TOK>
+template <int ROWS, int TOK, int OV>
 struct Split {
     static __device__ __forceinline__ bool mine(const AttnParams &p, const SeqInfo &q)
     {
@@ -62,6 +64,7 @@ struct Split {
         return rows >= p.min_rows && rows < p.max_rows;
     }
 
+    // Sequence s's length on the line.
     static __device__ int64_t cost(const AttnParams &p, int s)
     {
         if (s >= p.b.n_seqs)
@@ -72,7 +75,7 @@ struct Split {
         int64_t n = 0;
         const int tiles = row_tiles(q.n_new, p.group, ROWS);
         for (int r = 0; r < tiles; ++r)
-            n += span_of<ROWS, TOK>(q, r, p.group, p.window, p.sinks).n;
+            n += span_of<ROWS, TOK>(q, r, p.group, p.window, p.sinks).n + OV;
         return n * p.kv.heads;
     }
 
@@ -103,60 +106,66 @@ struct Split {
         return before + x;
     }
 
-    // The share of CTA `cta` of `n_cta`: tiles [x0, x1) and the cursor of the unit that
-    // holds x0.  Returns the share's size (`share`; every CTA but the last has it), or 0
-    // when this CTA has no tiles.
-    template <int THREADS>
-    static __device__ int64_t find(const AttnParams &p, int n_cta, int64_t *sums, Cursor *found,
-                                   int64_t &x0, int64_t &x1)
+    // The pieces of this CTA's N workers: worker i of CTA c has [(c * N + i) * piece, + piece)
+    // cut at `total`; found[i] is the unit that holds its start, where that is before
+    // `total`.  Every thread of the block calls it.
+    template <int THREADS, int N>
+    static __device__ void find(const AttnParams &p, int64_t *sums, Cursor *found, int64_t &piece,
+                                int64_t &total)
     {
         const int tid = threadIdx.x;
-        int64_t total = 0;
-        for (int base = 0; base < p.b.n_seqs; base += THREADS) {
+        const int64_t c0 = cost(p, tid);        // the only pass's, up to THREADS sequences
+        const int64_t upto0 = scan<THREADS>(c0, sums, total);
+        for (int base = THREADS; base < p.b.n_seqs; base += THREADS) {
             int64_t t;
             scan<THREADS>(cost(p, base + tid), sums, t);
             total += t;
         }
-        const int64_t share = (total + n_cta - 1) / n_cta;
-        x0 = share * blockIdx.x;
-        x1 = min(x0 + share, total);
-        if (x0 >= x1)
-            return 0;
+        const int64_t workers = int64_t(gridDim.x) * N;
+        piece = (total + workers - 1) / workers;
+        const int64_t x0 = piece * N * blockIdx.x;
+        if (x0 >= total)
+            return;
         int64_t before = 0;
         for (int base = 0; base < p.b.n_seqs; base += THREADS) {
-            int64_t t;
-            const int64_t c = cost(p, base + tid);
-            const int64_t upto = before + scan<THREADS>(c, sums, t);
-            if (upto > x0 && upto - c <= x0) {
-                Cursor u;
-                u.s = base + tid;
-                u.q = seq_info(p.b, u.s, nullptr);
-                u.at = upto - c;
-                u.r = 0;
-                while (true) {
-                    u.span = span_of<ROWS, TOK>(u.q, u.r, p.group, p.window, p.sinks);
-                    const int64_t w = int64_t(u.span.n) * p.kv.heads;
-                    if (u.at + w > x0)
-                        break;
-                    u.at += w;
-                    ++u.r;
+            int64_t t = 0, c = c0, upto = upto0;
+            if (p.b.n_seqs > THREADS) {
+                c = base ? cost(p, base + tid) : c0;
+                upto = before + scan<THREADS>(c, sums, t);
+            }
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) {
+                const int64_t x = x0 + i * piece;
+                if (upto > x && upto - c <= x) {
+                    Cursor u;
+                    u.s = base + tid;
+                    u.q = seq_info(p.b, u.s, nullptr);
+                    u.at = upto - c;
+                    u.r = 0;
+                    while (true) {
+                        u.span = span_of<ROWS, TOK>(u.q, u.r, p.group, p.window, p.sinks);
+                        const int64_t w = int64_t(u.span.n + OV) * p.kv.heads;
+                        if (u.at + w > x)
+                            break;
+                        u.at += w;
+                        ++u.r;
+                    }
+                    u.h = int((x - u.at) / (u.span.n + OV));
+                    u.at += int64_t(u.h) * (u.span.n + OV);
+                    found[i] = u;
                 }
-                u.h = int((x0 - u.at) / u.span.n);
-                u.at += int64_t(u.h) * u.span.n;
-                *found = u;
             }
             before += t;
-            if (before > x0)
+            if (before >= x0 + N * piece)
                 break;
         }
         __syncthreads();
-        return share;
     }
 
     // The unit after `u` (the caller knows that there is one).
     static __device__ void next(const AttnParams &p, Cursor &u)
     {
-        u.at += u.span.n;
+        u.at += u.span.n + OV;
         if (++u.h < p.kv.heads)
             return;
         u.h = 0;
@@ -172,11 +181,30 @@ struct Split {
     }
 };
 
+// Where row `row` of unit u is: its token among the call's rows and the first column of
+// its query head.
+template <int ROWS, int DIM>
+__device__ __forceinline__ void row_place(const AttnParams &p, const Cursor &u, int row, int64_t &token,
+                                          int64_t &col, int &pos)
+{
+    const int rho = u.r * ROWS + row, t = rho / p.group;
+    token = u.q.start + t;
+    col = int64_t(u.h * p.group + rho - t * p.group) * DIM;
+    pos = u.q.len - u.q.n_new + t;
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // One row computed on its own, key by key, with no product for a key it does not see:
 // for a row whose tile gave a result that is not finite.  There the keys other rows of
 // the tile see may hold an infinity or a NaN, which a zero weight does not take out of
 // the tile's product; here they are never multiplied.  `q` is the row's query, `pos` its
-// position; a whole warp, lane l holds elements d = l, l + 32, ...; returns them in o.
+// position; a whole warp, lane l holds the DIM / 32 elements from l * DIM / 32; returns them in o.
 template <int DIM, int FMT>
 __device__ void careful_row(const AttnParams &p, const SeqInfo &s, int seq, int head, int pos,
                             const uint16_t *q, float o[DIM / 32])
@@ -186,7 +214,7 @@ __device__ void careful_row(const AttnParams &p, const SeqInfo &s, int seq, int 
     float qf[N], m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-        qf[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(q)[lane + 32 * e]);
+        qf[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(q)[lane * N + e]);
         o[e] = 0.f;
     }
     for (int j = 0; j <= pos; ++j) {
@@ -201,7 +229,7 @@ __device__ void careful_row(const AttnParams &p, const SeqInfo &s, int seq, int 
         float kf[N], vf[N], dot = 0.f;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            const int d = lane + 32 * e;
+            const int d = lane * N + e;
             float a, b;
             if (FMT == kKvBf16) {
                 a = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.kv.k + at)[d]);
@@ -230,6 +258,38 @@ __device__ void careful_row(const AttnParams &p, const SeqInfo &s, int seq, int 
 #pragma unroll
     for (int e = 0; e < N; ++e)
         o[e] = l == 0.f ? 0.f : o[e] * inv;
+}
+
+// The end of one row, by a whole warp: its sums o (lane l has the DIM / 32 elements from
+// l * DIM / 32) over the sum of its weights l, as bf16; by careful_row where that is not
+// finite.
+template <int ROWS, int DIM, int FMT>
+__device__ __forceinline__ void finish_row(const AttnParams &p, const Cursor &u, int row,
+                                           const float o[DIM / 32], float l)
+{
+    constexpr int N = DIM / 32;
+    const int lane = threadIdx.x & 31;
+    int64_t token, col;
+    int pos;
+    row_place<ROWS, DIM>(p, u, row, token, col, pos);
+    float f[N];
+    bool ok = true;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        f[e] = l == 0.f ? 0.f : o[e] / l;
+        ok = ok && fabsf(f[e]) < INFINITY;
+    }
+    if (!__all_sync(0xffffffffu, ok))
+        careful_row<DIM, FMT>(p, u.q, u.s, u.h, pos, p.q + token * p.ldq + col, f);
+    uint16_t *dst = p.out + token * p.ldo + col + lane * N;
+    __nv_bfloat162 w[N / 2];
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e)
+        w[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+    if (N == 4)
+        *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<uint2 *>(w);
+    else
+        *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<uint32_t *>(w);
 }
 
 }  // namespace lora

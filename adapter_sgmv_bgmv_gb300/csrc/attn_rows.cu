@@ -7,14 +7,14 @@
 // bytes of the cache bound it: 16 rows are one m16n8k16 tensor-core tile (bf16 in, fp32
 // sums), whose arithmetic is a few percent of the time the bytes take.
 //
-// Layout.  All (sequence, key head, 16 rows) units are cut into tiles of kWarps * BT
-// keys and the tiles split evenly over the CTAs (attn.cuh).  Each warp has its own BT
-// keys of a tile, its own ring of ST stages in shared memory filled by 16-byte
-// cp.async (any page size, any strides: each row of a stage has its own address), and
-// its own running maximum, sum and output; the warps meet only at the end of a unit.
-// A unit that is spread over CTAs leaves its parts in scratch and the CTA that arrives
-// last adds them in the order of the CTAs, so the result does not depend on the order of
-// arrival.
+// Layout.  All (sequence, key head, 16 rows) units are cut into tiles of BT keys and laid
+// on a line that is split evenly over the warps of the grid (attn.cuh).  A warp goes
+// through its piece alone: its own ring of ST stages in shared memory, filled by 16-byte
+// cp.async (any page size, any strides: each row of a stage has its own address), its own
+// running maximum, sum and output.  A unit inside one piece goes straight to the output;
+// the parts of one that crosses pieces are joined when the CTA's warps are done: first
+// within the CTA in shared memory, then over CTAs by the one that arrives last, always in
+// the order of the pieces, so the result does not depend on the order of arrival.
 //
 // 8-bit keys and values become bf16 in registers between ldmatrix and the product (every
 // code is exact in bf16).  A key's scale multiplies its column of scores, a value's scale
@@ -33,6 +33,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;
+constexpr int kUnitCost = 3;   // a unit's start and end, in tiles
 
 template <int DIM, int FMT>
 struct Shape {
@@ -40,12 +41,10 @@ struct Shape {
     static constexpr int RB = DIM * ES;                    // bytes of a key row
     static constexpr int BT = FMT == kKvBf16 && DIM == 128 ? 16 : 32;
     static constexpr int ST = 3;
-    static constexpr int TOK = kWarps * BT;
     static constexpr int SCALES = FMT == kKvBf16 ? 0 : BT * 8;
     static constexpr int STAGE = 2 * BT * RB + SCALES;
-    static constexpr int RING = kWarps * ST * STAGE;
-    static constexpr int MERGE = kWarps * kRows * DIM * 4;
-    static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + kWarps * kRows * 8 + 1024;
+    static constexpr int SMEM = kWarps * ST * STAGE + 128;
+    static_assert(ST * STAGE >= kRows * DIM * 4, "a warp's partial takes the place of its ring");
 };
 
 // Byte offset of 16-byte chunk c of row r: rows of RB bytes, chunks exchanged so that
@@ -106,20 +105,72 @@ __device__ __forceinline__ void widen(uint32_t r, uint32_t &even, uint32_t &odd)
 }
 
 
+// The order of partial results on the line: for each warp the unit it found begun and saw
+// the end of (its head), then the unit its piece ended in (its tail).
+struct Part {
+    bool there, begins;       // begins: holds the unit's first tile
+    int m_rows;
+    Cursor u;
+};
+
+// Adds `n` partials (the i-th's row at o(i), its maximum and sum ml(i)) of one row in order;
+// a whole warp, lane l the DIM / 32 elements from l * DIM / 32.
+template <int DIM, typename O, typename ML>
+__device__ __forceinline__ void join(int n, O &&o, ML &&ml, float acc[DIM / 32], float &m, float &l)
+{
+    constexpr int N = DIM / 32;
+    const int lane = threadIdx.x & 31;
+    m = -INFINITY;
+    l = 0.f;
+    for (int i = lane; i < n; i += 32)
+        m = fmaxf(m, ml(i).x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        acc[e] = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float2 t = ml(i);
+        const float a = exp2_fast(t.x - ref);
+        float v[N];
+        o(i, v);
+        l += t.y * a;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            acc[e] = fmaf(a, v[e], acc[e]);
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void load_vec(float v[N], const float *src)
+{
+    if (N == 4) {
+        const float4 t = __ldcg(reinterpret_cast<const float4 *>(src));
+        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+    } else {
+        const float2 t = __ldcg(reinterpret_cast<const float2 *>(src));
+        v[0] = t.x, v[1] = t.y;
+    }
+}
+
 template <int DIM, int FMT>
 __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant__ AttnParams p)
 {
     using S = Shape<DIM, FMT>;
-    using Cut = Split<kRows, S::TOK>;
-    constexpr int BT = S::BT, ST = S::ST, RB = S::RB;
+    using Cut = Split<kRows, S::BT, kUnitCost>;
+    constexpr int BT = S::BT, ST = S::ST, RB = S::RB, N = DIM / 32;
     constexpr int NT = BT / 8;                             // 8-key tiles of scores
     constexpr int KS = DIM / 16;                           // k-steps of q.k
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     __shared__ int64_t sums[kWarps];
-    __shared__ Cursor found;
+    __shared__ Cursor found[kWarps];
+    __shared__ Part parts[2 * kWarps];
+    __shared__ float2 tail_ml[kWarps][kRows];
     __shared__ int last_flag;
-    __shared__ float row_sum[kRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, g = lane >> 2;
     const KvView &kv = p.kv;
     const BatchView &b = p.b;
@@ -127,60 +178,46 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
     grid_dep_wait();
     grid_dep_launch();
 
-    int64_t x0, x1;
-    const int64_t share = Cut::template find<kThreads>(p, gridDim.x, sums, &found, x0, x1);
-    if (share == 0)
+    int64_t piece, total;
+    Cut::template find<kThreads, kWarps>(p, sums, found, piece, total);
+    const int64_t share = piece * kWarps;
+    if (share * blockIdx.x >= total)
         return;
-    Cursor u = found;
-    const uint32_t ring = smem_u32(smem) + warp * ST * S::STAGE;
-    float2 *ml = reinterpret_cast<float2 *>(smem + (S::RING > S::MERGE ? S::RING : S::MERGE));
+    const int worker = int(blockIdx.x) * kWarps + warp;
+    int64_t x = worker * piece;
+    const int64_t x1 = min(x + piece, total);
+    uint8_t *mine = smem + warp * ST * S::STAGE;
+    const uint32_t ring = smem_u32(mine);
     const float sl = p.scale * 1.4426950408889634f;        // scores in powers of two
+    if (lane < 2)
+        parts[2 * warp + lane].there = false;
+    __syncwarp();
 
-    for (int64_t x = x0; x < x1;) {
-        const int t0 = int(x - u.at), t1 = int(min(x1 - u.at, int64_t(u.span.n)));
+    Cursor u;
+    if (x < x1)
+        u = found[warp];
+    while (x < x1) {
+        const int64_t first = u.at + kUnitCost, end = first + u.span.n;
+        const int t0 = int(max(x - first, int64_t(0)));
+        const int t1 = int(max(min(x1, end) - first, int64_t(0)));
+        x = end;
+        if (t1 <= t0) {                                    // only the unit's own cost is here
+            if (x < x1)
+                Cut::next(p, u);
+            continue;
+        }
         const int n_rows = min(kRows, u.q.n_new * p.group - u.r * kRows);
         const int base = u.q.len - u.q.n_new;
         const uint8_t *kp = kv.k + u.h * kv.head_stride, *vp = kv.v + u.h * kv.head_stride;
         const int32_t *pages = b.pages + int64_t(u.s) * b.ld_pages;
 
-        // this thread's rows g and g + 8: position, query (as the products want it)
-        int pos[2];
-        uint32_t qf[KS][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = g + 8 * i, rho = u.r * kRows + row;
-            const bool on = row < n_rows;
-            pos[i] = on ? base + rho / p.group : -1;
-            const uint16_t *src = p.q + int64_t(u.q.start + rho / p.group) * p.ldq +
-                                  (u.h * p.group + rho % p.group) * DIM;
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                if (FMT == kKvBf16) {
-                    qf[k][i] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 2 * c) : 0u;
-                    qf[k][i + 2] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 8 + 2 * c) : 0u;
-                } else {
-                    // the codes of d = 4c .. 4c + 3 arrive as pairs (0, 2) and (1, 3)
-                    const uint2 w = on ? *reinterpret_cast<const uint2 *>(src + 16 * k + 4 * c) : make_uint2(0, 0);
-                    qf[k][i] = __byte_perm(w.x, w.y, 0x5410);
-                    qf[k][i + 2] = __byte_perm(w.x, w.y, 0x7632);
-                }
-            }
-        }
-
-        float o[DIM / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < DIM / 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[i][e] = 0.f;
-
-        // first position of this warp's keys in tile t, and the end of the keys to read
+        // first position of tile t's keys, and the end of the keys to read
         auto keys = [&](int t, int &j0, int &j1) {
             if (t < u.span.n_sink) {
-                j0 = t * S::TOK + warp * BT;
+                j0 = t * BT;
                 j1 = u.span.sink;
             } else {
-                j0 = u.span.lo + (t - u.span.n_sink) * S::TOK + warp * BT;
+                j0 = u.span.lo + (t - u.span.n_sink) * BT;
                 j1 = u.span.hi;
             }
         };
@@ -229,10 +266,43 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
 #pragma unroll
         for (int i = 0; i < ST; ++i)
             pid[i] = page_at(t0 + i);
+
+        // this thread's rows g and g + 8: position, query (as the products want it)
+        int pos[2];
+        uint32_t qf[KS][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = g + 8 * i;
+            const bool on = row < n_rows;
+            int64_t token, col;
+            row_place<kRows, DIM>(p, u, on ? row : 0, token, col, pos[i]);
+            if (!on)
+                pos[i] = -1;
+            const uint16_t *src = p.q + token * p.ldq + col;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                if (FMT == kKvBf16) {
+                    qf[k][i] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 2 * c) : 0u;
+                    qf[k][i + 2] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 8 + 2 * c) : 0u;
+                } else {
+                    // the codes of d = 4c .. 4c + 3 arrive as pairs (0, 2) and (1, 3)
+                    const uint2 w = on ? *reinterpret_cast<const uint2 *>(src + 16 * k + 4 * c) : make_uint2(0, 0);
+                    qf[k][i] = __byte_perm(w.x, w.y, 0x5410);
+                    qf[k][i + 2] = __byte_perm(w.x, w.y, 0x7632);
+                }
+            }
+        }
 #pragma unroll
         for (int i = 0; i < ST - 1; ++i)
             issue(t0 + i, pid[i]);
         int page_next = pid[ST - 1];
+
+        float o[DIM / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < DIM / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[i][e] = 0.f;
 
         for (int t = t0; t < t1; ++t) {
             tc::cp_async_wait<ST - 2>();
@@ -274,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
                     }
                 }
                 // scale, mask, running maximum
-                const float *sc = reinterpret_cast<const float *>(smem + (st - smem_u32(smem)) + 2 * BT * RB);
+                const float *sc = reinterpret_cast<const float *>(mine + (t % ST) * S::STAGE + 2 * BT * RB);
                 float mx[2] = {m[0], m[1]};
                 const int je = min(j0 + BT, j1);
                 const bool all = je - 1 <= u.span.p0 && je - j0 == BT &&
@@ -305,13 +375,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
                     mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
                     mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
                     ref[i] = mx[i] == -INFINITY ? 0.f : mx[i];
-                    const float a = exp2f(m[i] - ref[i]);
-                    m[i] = mx[i];
-                    l[i] *= a;
+                }
+                // most tiles of a long sequence leave every maximum as it was
+                if (__any_sync(0xffffffffu, mx[0] != m[0] || mx[1] != m[1])) {
 #pragma unroll
-                    for (int d = 0; d < DIM / 8; ++d) {
-                        o[d][2 * i] *= a;
-                        o[d][2 * i + 1] *= a;
+                    for (int i = 0; i < 2; ++i) {
+                        const float a = exp2_fast(m[i] - ref[i]);
+                        m[i] = mx[i];
+                        l[i] *= a;
+#pragma unroll
+                        for (int d = 0; d < DIM / 8; ++d) {
+                            o[d][2 * i] *= a;
+                            o[d][2 * i + 1] *= a;
+                        }
                     }
                 }
                 // weights, as the left operand of the second product
@@ -327,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
                     float e[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float v = exp2f(s[n][i] - ref[i >> 1]);
+                        const float v = exp2_fast(s[n][i] - ref[i >> 1]);
                         l[i >> 1] += v;
                         // a key that is not seen has weight 0 whatever its scale is
                         e[i] = FMT == kKvBf16 ? v : s[n][i] == -INFINITY ? 0.f : v * vs[i & 1];
@@ -379,137 +455,141 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
             page_next = ahead;
         }
         tc::cp_async_wait<0>();
-
-        // The warps' results meet.  Element d of the output tile held as o[i][e]:
-        // bf16 pools: 8i + 2c + (e & 1); 8-bit pools: tiles come in even / odd pairs of
-        // one 16-wide chunk, 16 (i / 2) + 4c + 2 (e & 1) + (i & 1).
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
         }
-        __syncthreads();                                   // every warp is done with its ring
-        float *mo = reinterpret_cast<float *>(smem);       // [warp][row][DIM]
+
+        // Where the rows go: the unit's end, or a partial.  Element d of the output held as
+        // o[i][e]: bf16 pools, 8i + 2c + (e & 1); 8-bit pools, tiles come in even / odd
+        // pairs of one 16-wide chunk, 16 (i / 2) + 4c + 2 (e & 1) + (i & 1).
+        const bool begins = t0 == 0, ends = t1 == u.span.n;
+        const bool head = ends && !begins;
+        float *dst = head ? p.part.warp_o + int64_t(worker) * kRows * DIM : reinterpret_cast<float *>(mine);
+        float2 *dml = head ? p.part.warp_ml + int64_t(worker) * kRows : tail_ml[warp];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int row = g + 8 * i;
             if (row < n_rows) {
-                float *dst = mo + (warp * kRows + row) * DIM;
                 if (c == 0)
-                    ml[warp * kRows + row] = make_float2(m[i], l[i]);
+                    dml[row] = make_float2(m[i], l[i]);
 #pragma unroll
                 for (int d = 0; d < DIM / 8; ++d) {
                     if (FMT == kKvBf16) {
-                        *reinterpret_cast<float2 *>(dst + 8 * d + 2 * c) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
+                        *reinterpret_cast<float2 *>(dst + row * DIM + 8 * d + 2 * c) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
                     } else if ((d & 1) == 0) {
-                        *reinterpret_cast<float4 *>(dst + 8 * d + 4 * c) =
+                        *reinterpret_cast<float4 *>(dst + row * DIM + 8 * d + 4 * c) =
                             make_float4(o[d][2 * i], o[d + 1][2 * i], o[d][2 * i + 1], o[d + 1][2 * i + 1]);
                     }
                 }
             }
         }
-        __syncthreads();
-        const bool whole = t0 == 0 && t1 == u.span.n;
-        const int64_t first = u.at / share, final_ = (u.at + u.span.n - 1) / share;
-        constexpr int V4 = DIM / 4;
-        float *po = p.part_o;
-        float2 *pm = p.part_ml;
-        const int slot = int(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0);
-        for (int e = threadIdx.x; e < n_rows * V4; e += kThreads) {
-            const int row = e / V4, d = (e % V4) * 4;
-            float mm = -INFINITY, ll = 0.f;
-            float2 wml[kWarps];
+        __syncwarp();
+        if (begins && ends) {
+            for (int row = 0; row < n_rows; ++row) {
+                float f[N];
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                wml[i] = ml[i * kRows + row];
-                mm = fmaxf(mm, wml[i].x);
+                for (int e = 0; e < N; ++e)
+                    f[e] = dst[row * DIM + lane * N + e];
+                finish_row<kRows, DIM, FMT>(p, u, row, f, dml[row].y);
             }
-            const float ref = mm == -INFINITY ? 0.f : mm;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                const float a = exp2f(wml[i].x - ref);
-                ll += wml[i].y * a;
-                const float4 v = *reinterpret_cast<const float4 *>(mo + (i * kRows + row) * DIM + d);
-                acc.x += a * v.x;
-                acc.y += a * v.y;
-                acc.z += a * v.z;
-                acc.w += a * v.w;
-            }
-            if (!whole) {
-                *reinterpret_cast<float4 *>(po + (int64_t(slot) * kRows + row) * DIM + d) = acc;
-                if (d == 0)
-                    pm[int64_t(slot) * kRows + row] = make_float2(mm, ll);
-            } else {
-                *reinterpret_cast<float4 *>(mo + row * DIM + d) = acc;   // read by this thread only
-                if (d == 0)
-                    row_sum[row] = ll;
-            }
+            __syncwarp();                                  // the ring is free again
+        } else if (lane == 0) {
+            Part &pt = parts[2 * warp + (head ? 0 : 1)];
+            pt.there = true;
+            pt.begins = begins;
+            pt.m_rows = n_rows;
+            pt.u = u;
         }
-        bool finish = whole;
-        if (!whole) {
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0)
-                last_flag = atomicAdd(&p.arrived[first], 1) == int(final_ - first);
-            __syncthreads();
-            finish = last_flag != 0;
-            if (finish) {
-                __threadfence();
-                if (threadIdx.x == 0)
-                    p.arrived[first] = 0;
-                for (int e = threadIdx.x; e < n_rows * V4; e += kThreads) {
-                    const int row = e / V4, d = (e % V4) * 4;
-                    float mm = -INFINITY, ll = 0.f;
-                    for (int64_t i = first; i <= final_; ++i)
-                        mm = fmaxf(mm, __ldcg(&pm[(i * 2 + (i == first)) * kRows + row]).x);
-                    const float ref = mm == -INFINITY ? 0.f : mm;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int64_t i = first; i <= final_; ++i) {
-                        const int64_t at = (i * 2 + (i == first)) * kRows + row;
-                        const float2 w = __ldcg(&pm[at]);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(po + at * DIM + d));
-                        const float a = exp2f(w.x - ref);
-                        ll += w.y * a;
-                        acc.x += a * v.x;
-                        acc.y += a * v.y;
-                        acc.z += a * v.z;
-                        acc.w += a * v.w;
-                    }
-                    *reinterpret_cast<float4 *>(mo + row * DIM + d) = acc;
-                    if (d == 0)
-                        row_sum[row] = ll;
-                }
-            }
-        }
-        if (finish) {
-            __syncthreads();
-            // one warp a row: the quotient, and the check that it is finite
-            for (int row = warp; row < n_rows; row += kWarps) {
-                const int rho = u.r * kRows + row, tok = rho / p.group;
-                const float ll = row_sum[row];
-                float f[DIM / 32];
-                bool ok = true;
-#pragma unroll
-                for (int e = 0; e < DIM / 32; ++e) {
-                    f[e] = ll == 0.f ? 0.f : mo[row * DIM + lane + 32 * e] / ll;
-                    ok = ok && fabsf(f[e]) < INFINITY;
-                }
-                const int64_t col = (u.h * p.group + rho % p.group) * DIM;
-                if (!__all_sync(0xffffffffu, ok))
-                    careful_row<DIM, FMT>(p, u.q, u.s, u.h, base + tok,
-                                          p.q + int64_t(u.q.start + tok) * p.ldq + col, f);
-                uint16_t *dst = p.out + int64_t(u.q.start + tok) * p.ldo + col;
-#pragma unroll
-                for (int e = 0; e < DIM / 32; ++e)
-                    reinterpret_cast<__nv_bfloat16 *>(dst)[lane + 32 * e] = __float2bfloat16_rn(f[e]);
-            }
-        }
-        __syncthreads();                                   // the ring and `found` are free again
-        x = u.at + t1;
         if (x < x1)
             Cut::next(p, u);
+    }
+
+    // Units that crossed the warps of this CTA: runs of `parts` with the same unit.  Each
+    // run is one warp's; those that reach beyond the CTA become its partials.
+    __threadfence_block();
+    __syncthreads();
+    int cross[2] = {-1, -1};                               // parts of the runs that came in / go on
+    int run = 0;
+    for (int i = 0; i < 2 * kWarps;) {
+        if (!parts[i].there) {
+            ++i;
+            continue;
+        }
+        const int64_t at = parts[i].u.at;
+        int idx[2 * kWarps], n = 0, j = i;
+        for (; j < 2 * kWarps; ++j) {
+            if (!parts[j].there)
+                continue;
+            if (parts[j].u.at != at)
+                break;
+            idx[n++] = j;
+        }
+        const bool begins = parts[i].begins, ends = (idx[n - 1] & 1) == 0;
+        if (!begins)
+            cross[0] = i;
+        else if (!ends)
+            cross[1] = i;
+        if (run++ % kWarps == warp) {
+            for (int row = 0; row < parts[i].m_rows; ++row) {
+                float acc[N], m, l;
+                auto ml = [&](int k) {
+                    const int w = idx[k] >> 1;
+                    return (idx[k] & 1) ? tail_ml[w][row] : __ldcg(&p.part.warp_ml[(int64_t(blockIdx.x) * kWarps + w) * kRows + row]);
+                };
+                auto o = [&](int k, float *v) {
+                    const int w = idx[k] >> 1;
+                    if (idx[k] & 1) {
+                        const float *src = reinterpret_cast<const float *>(smem + w * ST * S::STAGE) + row * DIM + lane * N;
+#pragma unroll
+                        for (int e = 0; e < N; ++e)
+                            v[e] = src[e];
+                    } else {
+                        load_vec<N>(v, p.part.warp_o + ((int64_t(blockIdx.x) * kWarps + w) * kRows + row) * DIM + lane * N);
+                    }
+                };
+                join<DIM>(n, o, ml, acc, m, l);
+                if (begins && ends) {
+                    finish_row<kRows, DIM, FMT>(p, parts[i].u, row, acc, l);
+                } else {
+                    const int64_t at2 = (int64_t(blockIdx.x) * 2 + begins) * kRows + row;
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        p.part.cta_o[at2 * DIM + lane * N + e] = acc[e];
+                    if (lane == 0)
+                        p.part.cta_ml[at2] = make_float2(m, l);
+                }
+            }
+        }
+        i = j;
+    }
+    // Units that cross CTAs: the last to arrive adds the CTAs' partials, all its warps.
+    for (int k = 0; k < 2; ++k) {
+        if (cross[k] < 0)
+            continue;
+        const Part &pt = parts[cross[k]];
+        const int64_t first = (pt.u.at + kUnitCost) / share, final_ = (pt.u.at + kUnitCost + pt.u.span.n - 1) / share;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            last_flag = atomicAdd(&p.part.arrived[first], 1) == int(final_ - first);
+            if (last_flag)
+                p.part.arrived[first] = 0;
+        }
+        __syncthreads();
+        if (!last_flag)
+            continue;
+        __threadfence();
+        for (int row = warp; row < pt.m_rows; row += kWarps) {
+            float acc[N], m, l;
+            auto at = [&](int i) { return ((first + i) * 2 + (i == 0)) * kRows + row; };
+            join<DIM>(int(final_ - first) + 1,
+                      [&](int i, float *v) { load_vec<N>(v, p.part.cta_o + at(i) * DIM + lane * N); },
+                      [&](int i) { return __ldcg(&p.part.cta_ml[at(i)]); }, acc, m, l);
+            finish_row<kRows, DIM, FMT>(p, pt.u, row, acc, l);
+        }
     }
 }
 
@@ -539,10 +619,25 @@ cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream)
 
 }  // namespace
 
-AttnScratch attn_rows_scratch(int sms)
+size_t attn_rows_scratch(uint8_t *base, int sms, AttnScratch *s)
 {
-    const size_t slots = size_t(sms) * 2 * 2;
-    return {slots * kRows * 128 * sizeof(float), slots * kRows * sizeof(float2), size_t(sms) * 2 * sizeof(int)};
+    const size_t ctas = size_t(sms) * 2, warps = ctas * kWarps;
+    const size_t row = 128 * sizeof(float);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        uint8_t *p = base + at;
+        at += (bytes + 255) & ~size_t(255);
+        return p;
+    };
+    AttnScratch t;
+    t.cta_o = reinterpret_cast<float *>(take(ctas * 2 * kRows * row));
+    t.cta_ml = reinterpret_cast<float2 *>(take(ctas * 2 * kRows * sizeof(float2)));
+    t.warp_o = reinterpret_cast<float *>(take(warps * kRows * row));
+    t.warp_ml = reinterpret_cast<float2 *>(take(warps * kRows * sizeof(float2)));
+    t.arrived = reinterpret_cast<int *>(take(ctas * sizeof(int)));
+    if (s)
+        *s = t;
+    return at;
 }
 
 cudaError_t launch_attn_rows(const AttnParams &p, int sms, cudaStream_t stream)

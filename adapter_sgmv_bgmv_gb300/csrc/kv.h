@@ -51,6 +51,19 @@ struct KvRowsParams {
 cudaError_t launch_kv_write(const KvRowsParams &p, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvRowsParams &p, cudaStream_t stream);
 
+// Partial results of units split over workers, in device memory.  A partial is each of a
+// unit's rows' unnormalised output [dim] (fp32) and its running maximum and sum of
+// weights.  `arrived` has one counter per CTA, zero between calls.
+struct AttnScratch {
+    float *cta_o;             // two partials per CTA
+    float2 *cta_ml;
+    float *warp_o;            // one per warp
+    float2 *warp_ml;
+    int *arrived;
+};
+// Lays the few-rows kernel's partials out in `base`; returns the bytes they take.
+size_t attn_rows_scratch(uint8_t *base, int sms, AttnScratch *s);
+
 struct AttnParams {
     KvView kv;
     BatchView b;
@@ -64,20 +77,9 @@ struct AttnParams {
     int window;               // 0: none
     int sinks;
     int64_t min_rows, max_rows;   // sequences this launch serves: min <= new * group < max
-    // Partial results of units split over CTAs: two slots per CTA of `rows` rows, each
-    // row's unnormalised output [dim], and its running maximum and sum; one arrival
-    // counter per CTA, zero between calls.
-    float *part_o;
-    float2 *part_ml;
-    int *arrived;
+    AttnScratch part;
     unsigned *status;
 };
-// Bytes of the three partial-result arrays, one after another, of the largest grid of
-// each kernel, on a device of `sms` SMs.
-struct AttnScratch {
-    size_t o_bytes, ml_bytes, count_bytes;
-};
-AttnScratch attn_rows_scratch(int sms);
 cudaError_t launch_attn_rows(const AttnParams &p, int sms, cudaStream_t stream);
 
 #ifdef __CUDACC__

@@ -15,8 +15,7 @@ using namespace lora;
 struct lora_kv {
     lora_ctx *ctx = nullptr;           // not owned
     KvView view{};
-    uint8_t *scratch = nullptr;        // the context's
-    AttnScratch part{};
+    AttnScratch few{};                 // in the context's scratch
 };
 
 namespace {
@@ -146,8 +145,10 @@ int lora_kv_create(lora_ctx *ctx, const lora_kv_desc *d, lora_kv **out)
     if (ctx_device(ctx) >= 0) {
         int rc = ctx_begin(ctx, nullptr);
         if (rc == LORA_OK) {
-            kv->part = attn_rows_scratch(ctx_sms(ctx));
-            rc = ctx_attn_scratch(ctx, kv->part.o_bytes + kv->part.ml_bytes + kv->part.count_bytes, &kv->scratch);
+            uint8_t *base = nullptr;
+            rc = ctx_attn_scratch(ctx, attn_rows_scratch(nullptr, ctx_sms(ctx), nullptr), &base);
+            if (rc == LORA_OK)
+                attn_rows_scratch(base, ctx_sms(ctx), &kv->few);
         }
         if (rc != LORA_OK) {
             delete kv;
@@ -210,9 +211,7 @@ int lora_attention(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *b, int
     p.sinks = int(std::min<int64_t>(sinks, kMaxPosition));
     p.min_rows = 1;
     p.max_rows = int64_t(1) << 40;
-    p.part_o = reinterpret_cast<float *>(kv->scratch);
-    p.part_ml = reinterpret_cast<float2 *>(kv->scratch + kv->part.o_bytes);
-    p.arrived = reinterpret_cast<int *>(kv->scratch + kv->part.o_bytes + kv->part.ml_bytes);
+    p.part = kv->few;
     p.status = ctx_status(ctx);
     const cudaError_t e = launch_attn_rows(p, ctx_sms(ctx), stream);
     if (e != cudaSuccess)
