@@ -206,7 +206,7 @@ __device__ __forceinline__ float exp2_fast(float x)
 // the tile's product; here they are never multiplied.  `q` is the row's query, `pos` its
 // position; a whole warp, lane l holds the DIM / 32 elements from l * DIM / 32; returns them in o.
 template <int DIM, int FMT>
-__device__ void careful_row(const AttnParams &p, const SeqInfo &s, int seq, int head, int pos,
+__device__ __noinline__ void careful_row(const AttnParams &p, const SeqInfo &s, int seq, int head, int pos,
                             const uint16_t *q, float o[DIM / 32])
 {
     constexpr int N = DIM / 32;
@@ -258,6 +258,49 @@ __device__ void careful_row(const AttnParams &p, const SeqInfo &s, int seq, int 
 #pragma unroll
     for (int e = 0; e < N; ++e)
         o[e] = l == 0.f ? 0.f : o[e] * inv;
+}
+
+// Adds `n` partials (the i-th's row at o(i), its maximum and sum ml(i)) of one row in order;
+// a whole warp, lane l the DIM / 32 elements from l * DIM / 32.
+template <int DIM, typename O, typename ML>
+__device__ __forceinline__ void join(int n, O &&o, ML &&ml, float acc[DIM / 32], float &m, float &l)
+{
+    constexpr int N = DIM / 32;
+    const int lane = threadIdx.x & 31;
+    m = -INFINITY;
+    l = 0.f;
+    for (int i = lane; i < n; i += 32)
+        m = fmaxf(m, ml(i).x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        acc[e] = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float2 t = ml(i);
+        const float a = exp2_fast(t.x - ref);
+        float v[N];
+        o(i, v);
+        l += t.y * a;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            acc[e] = fmaf(a, v[e], acc[e]);
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void load_vec(float v[N], const float *src)
+{
+    if (N == 4) {
+        const float4 t = __ldcg(reinterpret_cast<const float4 *>(src));
+        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+    } else {
+        const float2 t = __ldcg(reinterpret_cast<const float2 *>(src));
+        v[0] = t.x, v[1] = t.y;
+    }
 }
 
 // The end of one row, by a whole warp: its sums o (lane l has the DIM / 32 elements from

@@ -113,49 +113,6 @@ struct Part {
     Cursor u;
 };
 
-// Adds `n` partials (the i-th's row at o(i), its maximum and sum ml(i)) of one row in order;
-// a whole warp, lane l the DIM / 32 elements from l * DIM / 32.
-template <int DIM, typename O, typename ML>
-__device__ __forceinline__ void join(int n, O &&o, ML &&ml, float acc[DIM / 32], float &m, float &l)
-{
-    constexpr int N = DIM / 32;
-    const int lane = threadIdx.x & 31;
-    m = -INFINITY;
-    l = 0.f;
-    for (int i = lane; i < n; i += 32)
-        m = fmaxf(m, ml(i).x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-        acc[e] = 0.f;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-        const float2 t = ml(i);
-        const float a = exp2_fast(t.x - ref);
-        float v[N];
-        o(i, v);
-        l += t.y * a;
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            acc[e] = fmaf(a, v[e], acc[e]);
-    }
-}
-
-template <int N>
-__device__ __forceinline__ void load_vec(float v[N], const float *src)
-{
-    if (N == 4) {
-        const float4 t = __ldcg(reinterpret_cast<const float4 *>(src));
-        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-    } else {
-        const float2 t = __ldcg(reinterpret_cast<const float2 *>(src));
-        v[0] = t.x, v[1] = t.y;
-    }
-}
-
 template <int DIM, int FMT>
 __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant__ AttnParams p)
 {
@@ -175,14 +132,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
     const KvView &kv = p.kv;
     const BatchView &b = p.b;
 
-    grid_dep_wait();
-    grid_dep_launch();
+    if (!p.behind) {
+        grid_dep_wait();
+        grid_dep_launch();
+    }
 
     int64_t piece, total;
     Cut::template find<kThreads, kWarps>(p, sums, found, piece, total);
     const int64_t share = piece * kWarps;
-    if (share * blockIdx.x >= total)
+    if (share * blockIdx.x >= total) {
+        if (p.behind)
+            grid_dep_wait();
         return;
+    }
     const int worker = int(blockIdx.x) * kWarps + warp;
     int64_t x = worker * piece;
     const int64_t x1 = min(x + piece, total);
@@ -591,6 +553,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
             finish_row<kRows, DIM, FMT>(p, pt.u, row, acc, l);
         }
     }
+    // whoever comes next may take this kernel's end for the whole call's
+    if (p.behind)
+        grid_dep_wait();
 }
 
 template <int DIM, int FMT>

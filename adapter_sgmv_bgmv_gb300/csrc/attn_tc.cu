@@ -1,0 +1,898 @@
+// Attention of many new tokens over the paged cache: prefill, and chunks of a prompt.
+//
+// The same sums as in attn_rows.cu, with the products on the tensor cores at full width.
+// A unit is 256 query rows (two tiles A and B of 128) of one (sequence, key head); it goes
+// through its keys in tiles of 128.  Per key tile and row tile, two products of
+// 128 x 128 x dim: S = Q K^T, then O += W V with W = exp2(S - reference).  Two products of
+// 128^3 take 1024 cycles of the tensor cores an SM has, and W takes 128 exponentials a row:
+// both row tiles share every key tile, and while one is at its weights the tensor cores
+// work for the other.
+//
+//   warps 0-3, 4-7   weights of tile A / B: one thread a row, S read from TMEM, W written
+//                    back over it as bf16 (the left operand of the second product).  The
+//                    reference is the running maximum, but it is moved (and O rescaled in
+//                    TMEM) only when the maximum passes it by 2^8: weights stay below 2^8,
+//                    and the sums are divided out at the end all the same.
+//   warps 8-11       loads: cells of the pages to 128-byte-swizzled tiles, each row with its
+//                    own address (any page size, any strides); bf16 by cp.async, 8-bit codes
+//                    through registers, where they become bf16 (exact).
+//   warp 12          one thread issues the products.
+//
+// TMEM (512 columns): S of A and B (128 each, W in their first half), O of A and B (dim).
+// The products of one thread run in the order of their issue, so the next S may be issued
+// behind the second product that reads the weights it will overwrite.
+// Shared memory (dim 128): Q 64 KB, a ring of four 32 KB tiles (keys, values by turns).
+//
+// The units lie on a line that is split evenly over one CTA per SM (attn.cuh), each CTA
+// going through its piece without a break: the loads of the next unit run while the
+// last one ends.  A unit cut by the ends of pieces leaves its parts in scratch, and the CTA
+// that arrives last joins them in the order of the CTAs.
+#include <cuda_runtime.h>
+
+#include <climits>
+
+#include "attn.cuh"
+#include "tc.cuh"
+
+namespace lora {
+
+namespace {
+
+constexpr int kThreads = 512;        // warps 13-15 only take part in the block's barriers
+constexpr int kM = 128;              // rows of a row tile
+constexpr int kRows = 2 * kM;
+constexpr int kKeys = 128;           // keys of a key tile
+constexpr int kUnitCost = 2;         // a unit's start and end, in key tiles
+constexpr int kScaleSlots = 4;
+constexpr int kMoreRegs = 152, kLoadRegs = 112, kFewRegs = 96;   // of 512 x 128 at launch
+
+template <int DIM>
+struct TcShape {
+    static constexpr int HALVES = DIM / 64;
+    static constexpr uint32_t HALF = 128 * 128;              // 128 rows x 64 elements
+    static constexpr uint32_t TILE = HALVES * HALF;
+    static constexpr int STAGES = DIM == 128 ? 4 : 6;
+    static constexpr uint32_t RING = 2 * TILE;               // after the two Q tiles
+    static constexpr uint32_t SCALES = RING + STAGES * TILE; // [slot][k, v][128] floats
+    static constexpr uint32_t BARS = SCALES + kScaleSlots * 2 * kKeys * 4;
+    static constexpr uint32_t BYTES = BARS + 256;
+    static constexpr uint32_t SMEM = BYTES + 1024;
+};
+
+// Barriers, 8 bytes each from BARS.
+enum Bar : uint32_t {
+    kFull = 0, kEmpty = 8, kQFull = 16, kQEmpty = 18, kSFull = 20, kWReady = 22, kPvDone = 24
+};
+
+__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMoreRegs)); }
+template <int R>
+__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(acc) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t r[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t r[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+        "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Bounded wait of a role: after one that ran out (here or in another warp) every wait of
+// the block gives up at once, and the roles go through their loops without the work.
+__device__ __forceinline__ bool await(uint32_t bar, uint32_t parity, volatile int *dead, unsigned *status, unsigned code)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!*dead) {
+        if (mbar_try_wait(bar, parity))
+            return true;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            raise_status(status, code);
+            *dead = 1;
+        }
+    }
+    return false;
+}
+
+// A warp's way along its CTA's piece: the unit, and the key tiles [t0, t1) of it that are
+// here.  It lies in shared memory: one lane moves it, all read it.
+template <typename Cut>
+struct Walk {
+    Cursor u;
+    int64_t x, x1;
+    int t, t0, t1;
+    bool more;                // t is a tile; false past the end
+
+    __device__ __forceinline__ void start(const AttnParams &p, const Cursor &c, int64_t from, int64_t to)
+    {
+        u = c;
+        x = from;
+        x1 = to;
+        more = true;
+        enter(p);
+    }
+    // The next unit (from x on) that has tiles here.
+    __device__ __forceinline__ void enter(const AttnParams &p)
+    {
+        while (true) {
+            const int64_t first = u.at + kUnitCost, end = first + u.span.n;
+            t0 = t = int(max(x - first, int64_t(0)));
+            t1 = int(max(min(x1, end) - first, int64_t(0)));
+            x = end;
+            if (t1 > t0)
+                return;
+            if (x >= x1) {
+                more = false;
+                return;
+            }
+            Cut::next(p, u);
+        }
+    }
+    __device__ __forceinline__ void step(const AttnParams &p)
+    {
+        if (++t < t1)
+            return;
+        if (x >= x1) {
+            more = false;
+            return;
+        }
+        Cut::next(p, u);
+        enter(p);
+    }
+    // First key of tile `i` and the end of the keys to read.
+    __device__ __forceinline__ void keys(int i, int &j0, int &j1) const
+    {
+        if (i < u.span.n_sink) {
+            j0 = i * kKeys;
+            j1 = u.span.sink;
+        } else {
+            j0 = u.span.lo + (i - u.span.n_sink) * kKeys;
+            j1 = u.span.hi;
+        }
+    }
+};
+
+// One row tile of a unit: its rows, and the positions of its first and last token.
+struct Side {
+    int rows, p_first, p_last;
+};
+
+__device__ __forceinline__ Side side_of(const AttnParams &p, const Cursor &u, int tile)
+{
+    Side s;
+    const int rho = u.r * kRows + tile * kM, all = u.q.n_new * p.group;
+    s.rows = max(0, min(kM, all - rho));
+    const int base = u.q.len - u.q.n_new;
+    s.p_first = base + rho / p.group;
+    s.p_last = base + (rho + max(s.rows, 1) - 1) / p.group;
+    return s;
+}
+
+// Whether any row of the tile sees a key of [j0, j0 + kKeys): the products of the others are
+// left out.
+template <typename W>
+__device__ __forceinline__ bool busy(const AttnParams &p, const W &w, const Side &s, int i)
+{
+    if (s.rows == 0)
+        return false;
+    int j0, j1;
+    w.keys(i, j0, j1);
+    if (j0 > s.p_last)
+        return false;
+    return i < w.u.span.n_sink || p.window == 0 || j0 + kKeys - 1 > s.p_first - p.window || j0 < p.sinks;
+}
+
+// Four codes (bytes 0..3) to bf16, in order.
+template <int FMT>
+__device__ __forceinline__ uint2 widen4(uint32_t r)
+{
+    uint2 y;
+    if (FMT == kKvInt8) {
+        // 128 + the low seven bits, less 128 or (sign bit) 256: exact in bf16
+        const uint32_t a = __byte_perm(r, 0, 0x4140), b = __byte_perm(r, 0, 0x4342);
+        const uint32_t a1 = (a & 0x007f007fu) | 0x43004300u, a0 = (a & 0x00800080u) | 0x43004300u;
+        const uint32_t b1 = (b & 0x007f007fu) | 0x43004300u, b0 = (b & 0x00800080u) | 0x43004300u;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y.x) : "r"(a1), "r"(a0));
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y.y) : "r"(b1), "r"(b0));
+    } else {
+        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(r & 0xffffu), __NV_E4M3);
+        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(r >> 16), __NV_E4M3);
+        const float2 fa = __half22float2(__half2(a)), fb = __half22float2(__half2(b));
+        y.x = pack2(fa.x, fa.y);
+        y.y = pack2(fb.x, fb.y);
+    }
+    return y;
+}
+
+template <int DIM, int FMT>
+__global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__ AttnParams p)
+{
+    using S = TcShape<DIM>;
+    using Cut = Split<kRows, kKeys, kUnitCost>;
+    constexpr int ST = S::STAGES, N = DIM / 32;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), sm = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (sm - raw);
+    __shared__ int64_t sums[kThreads / 32];
+    __shared__ Cursor found[1];
+    __shared__ Walk<Cut> walks[kThreads / 32];             // each warp's, out of its registers
+    __shared__ Cursor units[4];                            // the load warps' unit whose queries come next
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead_flag, last_flag;
+    volatile int *dead = &dead_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const KvView &kv = p.kv;
+    auto bar = [&](uint32_t i) { return sm + S::BARS + 8 * i; };
+
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(bar(kFull + i), 4);          // the load warps
+            mbar_init(bar(kEmpty + i), 1);         // a commit
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kQFull + i), 4);
+            mbar_init(bar(kQEmpty + i), 1);
+            mbar_init(bar(kSFull + i), 1);
+            mbar_init(bar(kWReady + i), 4);        // the warps of one row tile
+            mbar_init(bar(kPvDone + i), 1);
+        }
+        fence_mbar_init();
+        dead_flag = 0;
+    }
+    if (warp == 12)
+        tc::tmem_alloc(smem_u32(&tmem_slot), 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+
+    grid_dep_wait();
+    grid_dep_launch();
+
+    int64_t piece, total;
+    Cut::template find<kThreads, 1>(p, sums, found, piece, total);
+    const int64_t x0 = piece * blockIdx.x, x1 = min(x0 + piece, total);
+    const bool any = x0 < x1;
+    bool ok = true;
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ weights
+        setmaxnreg_inc();
+        const int T = warp >> 2, row = tid & 127;
+        const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lanes + T * 128u, tO = tmem + lanes + 256u + T * uint32_t(DIM);
+        const float sl = p.scale * 1.4426950408889634f;
+        const bool scaled = FMT != kKvBf16 || sl <= 0.f;   // scores scaled before the maximum
+        uint32_t n_s = 0;                                  // S tiles taken so far
+        int tile_no = 0;                                   // key tiles of the CTA so far
+        Walk<Cut> &w = walks[warp];
+        const Cursor &u = w.u;
+        if (lane == 0) {
+            w.more = any;
+            if (any)
+                w.start(p, found[0], x0, x1);
+        }
+        __syncwarp();
+        while (w.more) {
+            const int t0 = w.t0, t1 = w.t1;
+            const Side sd = side_of(p, u, T);
+            int64_t token, col;
+            int pos;
+            const bool on = row < sd.rows;
+            row_place<kRows, DIM>(p, u, on ? T * kM + row : 0, token, col, pos);
+            if (!on)
+                pos = -1;
+            float ref = -INFINITY, l = 0.f;
+            bool begun = false;
+            for (int t = t0; t < t1; ++t, ++tile_no) {
+                if (!busy(p, w, sd, t))
+                    continue;
+                ok = __all_sync(0xffffffffu, await(bar(kSFull + T), n_s & 1, dead, p.status, kDevTimeoutMma)) && ok;
+                if (!ok)
+                    continue;
+                tc::fence_after_sync();
+                const float *ks = reinterpret_cast<const float *>(smem + S::SCALES) + (tile_no % kScaleSlots) * 2 * kKeys;
+                int j0, j1;
+                w.keys(t, j0, j1);
+                const bool sink = t < u.span.n_sink;
+                const bool masked = j0 + kKeys - 1 > sd.p_first || (sink && j1 - j0 < kKeys) ||
+                                    (p.window && !sink && j0 <= sd.p_last - p.window);
+                const int hi = (sink ? min(pos, j1 - 1) : pos) - j0;            // last key seen
+                const int lo = p.window && !sink ? pos - p.window - j0 : -1;   // last hidden behind the window
+                const int sk = p.sinks - j0;
+                auto hidden = [&](int i) { return i > hi || (i <= lo && i >= sk); };
+                // first over S: the maximum
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                {
+                    uint32_t r[2][32];
+                    tc::tmem_ld32_nowait(tS, r[0]);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        if (h < 3)
+                            tc::tmem_ld32_nowait(tS + 32 * (h + 1), r[(h + 1) & 1]);
+                        float *s = reinterpret_cast<float *>(r[h & 1]);
+                        if (FMT != kKvBf16) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 k4 = *reinterpret_cast<const float4 *>(ks + 32 * h + i);
+                                s[i] *= k4.x;
+                                s[i + 1] *= k4.y;
+                                s[i + 2] *= k4.z;
+                                s[i + 3] *= k4.w;
+                            }
+                        } else if (scaled) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                s[i] *= sl;
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (hidden(32 * h + i))
+                                    s[i] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                mx[e] = fmaxf(mx[e], fmaxf(s[i + e], s[i + e + 4]));
+                        tc::tmem_wait_ld();
+                    }
+                }
+                const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const float top = scaled ? most : most * sl;
+                const bool move = top > ref + 8.f;         // the first tile's always does
+                if (__any_sync(0xffffffffu, move)) {
+                    const float a = move ? exp2_fast(ref - top) : 1.f;
+                    if (move)
+                        ref = top;
+                    l *= a;
+                    if (begun) {                           // the products so far, at rest
+                        ok = __all_sync(0xffffffffu, await(bar(kPvDone + T), (n_s - 1) & 1, dead, p.status, kDevTimeoutMma)) && ok;
+                        tc::fence_after_sync();
+                        if (ok) {
+#pragma unroll 1
+                            for (int i = 0; i < DIM / 32; ++i) {
+                                uint32_t v[32];
+                                tc::tmem_ld32_nowait(tO + 32 * i, v);
+                                tc::tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
+                                tmem_st32(tO + 32 * i, v);
+                            }
+                        }
+                    }
+                }
+                // then the weights, each 32 over the S they came from
+                const float m = ref == -INFINITY ? 0.f : ref;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                {
+                    uint32_t r[2][32];
+                    tc::tmem_ld32_nowait(tS, r[0]);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        if (h < 3)
+                            tc::tmem_ld32_nowait(tS + 32 * (h + 1), r[(h + 1) & 1]);
+                        const float *s = reinterpret_cast<const float *>(r[h & 1]);
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            float kf[4] = {sl, sl, sl, sl}, vf[4], e4[4];
+                            if (FMT != kKvBf16) {
+                                const float4 k4 = *reinterpret_cast<const float4 *>(ks + 32 * h + i);
+                                const float4 v4 = *reinterpret_cast<const float4 *>(ks + kKeys + 32 * h + i);
+                                kf[0] = k4.x, kf[1] = k4.y, kf[2] = k4.z, kf[3] = k4.w;
+                                vf[0] = v4.x, vf[1] = v4.y, vf[2] = v4.z, vf[3] = v4.w;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float x = fmaf(s[i + e], kf[e], -m);
+                                if (masked && hidden(32 * h + i + e))
+                                    x = -INFINITY;
+                                const float q = exp2_fast(x);
+                                sum[e] += q;
+                                // a key that is not seen has weight 0 whatever its scale is
+                                e4[e] = FMT == kKvBf16 ? q : masked && x == -INFINITY ? 0.f : q * vf[e];
+                            }
+                            pk[i / 2] = pack2(e4[0], e4[1]);
+                            pk[i / 2 + 1] = pack2(e4[2], e4[3]);
+                        }
+                        tc::tmem_wait_ld();
+                        tmem_st16(tS + 16 * h, pk);
+                    }
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(kWReady + T));
+                begun = true;
+                ++n_s;
+            }
+            // the part's end
+            if (begun) {
+                ok = __all_sync(0xffffffffu, await(bar(kPvDone + T), (n_s - 1) & 1, dead, p.status, kDevTimeoutMma)) && ok;
+                tc::fence_after_sync();
+            }
+            const bool begins = t0 == 0, ends = t1 == u.span.n;
+            if (begins && ends) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                bool fine = true;
+                uint16_t *dst = p.out + token * p.ldo + col;
+#pragma unroll
+                for (int i = 0; i < DIM / 32; ++i) {
+                    uint32_t v[32];
+                    if (begun && ok) {
+                        tc::tmem_ld32_nowait(tO + 32 * i, v);
+                        tc::tmem_wait_ld();
+                    }
+                    uint4 y[4];
+                    uint32_t *yw = reinterpret_cast<uint32_t *>(y);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float a = begun && l != 0.f ? __uint_as_float(v[e]) * inv : 0.f;
+                        const float b = begun && l != 0.f ? __uint_as_float(v[e + 1]) * inv : 0.f;
+                        fine = fine && fabsf(a) < INFINITY && fabsf(b) < INFINITY;
+                        yw[e / 2] = pack2(a, b);
+                    }
+                    if (on && ok)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<uint4 *>(dst + 32 * i + 8 * e) = y[e];
+                }
+                unsigned bad = __ballot_sync(0xffffffffu, on && ok && !fine);
+                while (bad) {                              // rows to be done on their own
+                    const int src = __ffs(bad) - 1;
+                    bad &= bad - 1;
+                    float o[N] = {};
+                    finish_row<kRows, DIM, FMT>(p, u, T * kM + (warp & 3) * 32 + src, o, __int_as_float(0x7fffffff));
+                }
+            } else {
+                const int64_t at = ((int64_t(blockIdx.x) * 2 + begins) * kRows + T * kM + row);
+                if (on)
+                    p.part.cta_ml[at] = make_float2(ref, l);
+#pragma unroll
+                for (int i = 0; i < DIM / 32; ++i) {
+                    uint32_t v[32];
+                    if (begun && ok) {
+                        tc::tmem_ld32_nowait(tO + 32 * i, v);
+                        tc::tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = 0;
+                    }
+                    if (on)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4 *>(p.part.cta_o + at * DIM + 32 * i + e) =
+                                make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                }
+                const int64_t first = (u.at + kUnitCost) / piece, final_ = (u.at + kUnitCost + u.span.n - 1) / piece;
+                __threadfence();
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (tid == 0) {
+                    last_flag = atomicAdd(&p.part.arrived[first], 1) == int(final_ - first);
+                    if (last_flag)
+                        p.part.arrived[first] = 0;
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (last_flag) {
+                    __threadfence();
+                    const int n_rows = min(kRows, u.q.n_new * p.group - u.r * kRows);
+                    for (int rr = warp; rr < n_rows; rr += 8) {
+                        float acc[N], m, ll;
+                        auto where = [&](int i) { return ((first + i) * 2 + (i == 0)) * kRows + rr; };
+                        join<DIM>(int(final_ - first) + 1,
+                                  [&](int i, float *v) { load_vec<N>(v, p.part.cta_o + where(i) * DIM + lane * N); },
+                                  [&](int i) { return __ldcg(&p.part.cta_ml[where(i)]); }, acc, m, ll);
+                        if (ok)
+                            finish_row<kRows, DIM, FMT>(p, u, rr, acc, ll);
+                    }
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");   // last_flag is free again
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                w.t = t1 - 1;
+                w.step(p);
+            }
+            __syncwarp();
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------------------ loads
+        setmaxnreg_dec<kLoadRegs>();
+        const int lw = warp - 8;                           // this warp's 32 keys (or rows) of a tile
+        const int32_t *table = p.b.pages;
+        Walk<Cut> &w = walks[warp];
+        if (lane == 0) {
+            w.more = any;
+            if (any)
+                w.start(p, found[0], x0, x1);
+        }
+        __syncwarp();
+        auto step = [&]() {
+            __syncwarp();
+            if (lane == 0)
+                w.step(p);
+            __syncwarp();
+        };
+        uint32_t entry = 0;                                // ring entries so far: keys 2j, values 2j + 1
+        int part = 0, tile_no = 0;
+        uint32_t pending = 0;                              // barrier of the copies under way
+
+        auto page_id = [&](const Walk<Cut> &k) -> int {
+            int j0, j1;
+            k.keys(k.t, j0, j1);
+            const int j = j0 + lw * 32 + lane;
+            return j < j1 ? table[int64_t(k.u.s) * p.b.ld_pages + page_of(kv, j)] : INT_MIN;
+        };
+        auto place = [&](const Walk<Cut> &k, int page, int64_t &at, int64_t &s_at) {
+            at = -1;
+            s_at = 0;
+            if (page == INT_MIN)
+                return;
+            if (page < 0 || page >= kv.n_pages) {
+                raise_status(p.status, kDevBadPage);
+                return;
+            }
+            int j0, j1;
+            k.keys(k.t, j0, j1);
+            const int j = j0 + lw * 32 + lane;
+            const int cell = j - page_of(kv, j) * kv.page_size;
+            at = page * kv.page_stride + cell * kv.cell_stride + k.u.h * kv.head_stride;
+            s_at = page * kv.s_page + cell * kv.s_cell + k.u.h * kv.s_head;
+        };
+        // The copies before the last commit are in shared memory: hand them over.
+        auto settle = [&](bool all) {
+            if (all)
+                tc::cp_async_wait<0>();
+            else
+                tc::cp_async_wait<1>();
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (pending && lane == 0)
+                mbar_arrive(pending);
+        };
+        auto stage = [&](uint32_t e) { return sm + S::RING + (e % ST) * S::TILE; };
+        auto wait_empty = [&](uint32_t e) {
+            if (e >= uint32_t(ST))
+                ok = await(bar(kEmpty + e % ST), (e / ST - 1) & 1, dead, p.status, kDevTimeoutPipe) && ok;
+            ok = __all_sync(0xffffffffu, ok);
+        };
+        constexpr int CH = DIM / 8, RPI = 32 / CH;         // 16-byte chunks of a bf16 row, rows an instruction
+        auto copy_rows = [&](uint32_t dst, const uint8_t *src, int64_t at) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int rr = i * RPI + lane / CH, ch = lane % CH, row = lw * 32 + rr;
+                const int64_t a = __shfl_sync(0xffffffffu, (long long)at, rr);
+                tc::cp_async16(dst + (ch / 8) * S::HALF + tc::sw128(row, ch % 8), src + (a < 0 ? 0 : a + ch * 16), a < 0 ? 0u : 16u);
+            }
+        };
+        auto load_q = [&](const Cursor &u) {
+            for (int T = 0; T < 2; ++T) {
+                if (part > 0)
+                    ok = await(bar(kQEmpty + T), (part - 1) & 1, dead, p.status, kDevTimeoutPipe) && ok;
+                ok = __all_sync(0xffffffffu, ok);
+                const int row = T * kM + lw * 32 + lane;
+                int64_t at = -1;
+                if (u.r * kRows + row < u.q.n_new * p.group) {
+                    int64_t token, col;
+                    int pos;
+                    row_place<kRows, DIM>(p, u, row, token, col, pos);
+                    at = (token * p.ldq + col) * 2;
+                }
+                if (ok)
+                    copy_rows(sm + T * S::TILE, reinterpret_cast<const uint8_t *>(p.q), at);
+                tc::cp_async_commit();
+                settle(false);
+                pending = bar(kQFull + T);
+            }
+            ++part;
+        };
+
+        int page = w.more ? page_id(w) : INT_MIN;
+        Cursor &unit = units[lw];
+        if (FMT == kKvBf16) {
+            while (w.more) {
+                const bool fresh = w.t == w.t0;
+                int64_t at, s_at;
+                place(w, page, at, s_at);
+                if (fresh && lane == 0)
+                    unit = w.u;
+                step();
+                page = w.more ? page_id(w) : INT_MIN;      // on its way during this tile
+                for (int side = 0; side < 2; ++side) {
+                    wait_empty(entry);
+                    if (ok)
+                        copy_rows(stage(entry), side ? kv.v : kv.k, at);
+                    tc::cp_async_commit();
+                    settle(false);
+                    pending = bar(kFull + entry % ST);
+                    ++entry;
+                    if (side == 0 && fresh)
+                        load_q(unit);
+                }
+            }
+            settle(true);
+        } else {
+            constexpr int C8 = DIM / 16, R8 = 32 / C8;     // 16-byte chunks of a row of codes
+            auto fetch = [&](uint4 x[C8], const uint8_t *src, int64_t at) {
+#pragma unroll
+                for (int i = 0; i < C8; ++i) {
+                    const int64_t a = __shfl_sync(0xffffffffu, (long long)at, i * R8 + lane / C8);
+                    x[i] = a < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(src + a + (lane % C8) * 16);
+                }
+            };
+            auto store = [&](uint32_t dst, const uint4 x[C8]) {
+#pragma unroll
+                for (int i = 0; i < C8; ++i) {
+                    const int row = lw * 32 + i * R8 + lane / C8, ch = 2 * (lane % C8);
+                    const uint2 a = widen4<FMT>(x[i].x), b = widen4<FMT>(x[i].y), c = widen4<FMT>(x[i].z), d = widen4<FMT>(x[i].w);
+                    uint8_t *base = smem + (dst - sm) + (ch / 8) * S::HALF;
+                    *reinterpret_cast<uint4 *>(base + tc::sw128(row, ch % 8)) = make_uint4(a.x, a.y, b.x, b.y);
+                    *reinterpret_cast<uint4 *>(base + tc::sw128(row, ch % 8 + 1)) = make_uint4(c.x, c.y, d.x, d.y);
+                }
+            };
+            auto hand_over = [&](uint32_t b) {
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(b);
+            };
+            const float sl = p.scale * 1.4426950408889634f;
+            uint4 kx[C8], vx[C8];
+            float ks = 0.f, vs = 0.f;
+            int64_t at = -1, s_at = 0;
+            auto scales = [&]() {
+                ks = at < 0 ? 0.f : kv.k_scale[s_at] * sl;
+                vs = at < 0 ? 0.f : kv.v_scale[s_at];
+            };
+            if (w.more) {
+                place(w, page, at, s_at);
+                fetch(kx, kv.k, at);
+                scales();
+            }
+            while (w.more) {
+                const bool fresh = w.t == w.t0;
+                fetch(vx, kv.v, at);
+                if (fresh && lane == 0)
+                    unit = w.u;
+                step();
+                page = w.more ? page_id(w) : INT_MIN;
+                wait_empty(entry);
+                if (ok) {
+                    store(stage(entry), kx);
+                    float *sc = reinterpret_cast<float *>(smem + S::SCALES) + (tile_no % kScaleSlots) * 2 * kKeys + lw * 32 + lane;
+                    sc[0] = ks;
+                    sc[kKeys] = vs;
+                }
+                hand_over(bar(kFull + entry % ST));
+                ++entry;
+                if (fresh) {
+                    pending = 0;
+                    load_q(unit);
+                    settle(true);
+                }
+                if (w.more) {
+                    place(w, page, at, s_at);
+                    fetch(kx, kv.k, at);
+                    scales();
+                }
+                wait_empty(entry);
+                if (ok)
+                    store(stage(entry), vx);
+                hand_over(bar(kFull + entry % ST));
+                ++entry;
+                ++tile_no;
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ products
+        setmaxnreg_dec<kFewRegs>();
+        if (warp == 12 && lane == 0 && any) {
+            constexpr uint32_t iqk = tc::idesc_bf16(kM, kKeys, 0, 0), ipv = tc::idesc_bf16(kM, DIM, 0, 1);
+            Walk<Cut> &w = walks[warp];
+            w.start(p, found[0], x0, x1);
+            uint32_t tile = 0, n_w[2] = {0, 0};
+            int part = 0;
+            bool first_pv[2] = {true, true};
+            auto scores = [&](int T, bool act, bool last) {   // S of tile `tile`
+                if (act) {
+                    ok = ok && await(bar(kFull + (2 * tile) % ST), (2 * tile / ST) & 1, dead, p.status, kDevTimeoutLoad);
+                    ok = ok && await(bar(kQFull + T), part & 1, dead, p.status, kDevTimeoutLoad);
+                    if (ok) {
+                        tc::fence_after_sync();
+                        const uint32_t q = sm + T * S::TILE, k = sm + S::RING + ((2 * tile) % ST) * S::TILE;
+#pragma unroll
+                        for (int i = 0; i < DIM / 16; ++i)
+                            tc::mma_bf16(tmem + T * 128u,
+                                         tc::smem_desc_sw128(q + (i / 4) * S::HALF + 32u * (i % 4), 16u, 1024u),
+                                         tc::smem_desc_sw128(k + (i / 4) * S::HALF + 32u * (i % 4), 16u, 1024u), iqk, i > 0);
+                        tc::mma_commit(bar(kSFull + T));
+                    }
+                }
+                if (last && ok)
+                    tc::mma_commit(bar(kQEmpty + T));
+            };
+            auto sums_ = [&](int T, bool act) {               // O += W V of tile `tile`
+                if (!act)
+                    return;
+                ok = ok && await(bar(kWReady + T), n_w[T] & 1, dead, p.status, kDevTimeoutPipe);
+                ok = ok && await(bar(kFull + (2 * tile + 1) % ST), ((2 * tile + 1) / ST) & 1, dead, p.status, kDevTimeoutLoad);
+                ++n_w[T];
+                if (ok) {
+                    tc::fence_after_sync();
+                    const uint32_t v = sm + S::RING + ((2 * tile + 1) % ST) * S::TILE;
+#pragma unroll
+                    for (int i = 0; i < kKeys / 16; ++i)
+                        mma_tmem_a(tmem + 256u + T * uint32_t(DIM), tmem + T * 128u + 8 * i,
+                                   tc::smem_desc_sw128(v + 2048u * i, S::HALF, 1024u), ipv, !(first_pv[T] && i == 0));
+                    tc::mma_commit(bar(kPvDone + T));
+                }
+                first_pv[T] = false;
+            };
+            Side sd[2] = {side_of(p, w.u, 0), side_of(p, w.u, 1)};
+            bool act[2];
+            for (int T = 0; T < 2 && w.more; ++T) {
+                act[T] = busy(p, w, sd[T], w.t);
+                scores(T, act[T], w.t + 1 == w.t1);
+            }
+            if (w.more && ok)
+                tc::mma_commit(bar(kEmpty + 0));
+            while (w.more) {
+                const bool unit_end = w.t + 1 == w.t1;
+                w.step(p);
+                bool next[2] = {false, false};
+                if (w.more) {
+                    if (unit_end) {
+                        sd[0] = side_of(p, w.u, 0);
+                        sd[1] = side_of(p, w.u, 1);
+                    }
+                    next[0] = busy(p, w, sd[0], w.t);
+                    next[1] = busy(p, w, sd[1], w.t);
+                }
+                const bool last = w.t + 1 == w.t1;
+                if (unit_end) {
+                    // the next unit's queries may still be on their way: both tiles' ends first
+                    sums_(0, act[0]);
+                    sums_(1, act[1]);
+                    if (ok)
+                        tc::mma_commit(bar(kEmpty + (2 * tile + 1) % ST));
+                    first_pv[0] = first_pv[1] = true;
+                    ++part;
+                    ++tile;
+                    if (w.more) {
+                        scores(0, next[0], last);
+                        scores(1, next[1], last);
+                    }
+                } else {
+                    sums_(0, act[0]);
+                    ++tile;
+                    scores(0, next[0], last);
+                    --tile;
+                    sums_(1, act[1]);
+                    if (ok)
+                        tc::mma_commit(bar(kEmpty + (2 * tile + 1) % ST));
+                    ++tile;
+                    scores(1, next[1], last);
+                }
+                if (w.more && ok)
+                    tc::mma_commit(bar(kEmpty + (2 * tile) % ST));
+                act[0] = next[0];
+                act[1] = next[1];
+            }
+        }
+    }
+    // Every product has ended: the weights' warps waited for each tile's last, and a role
+    // that gave up is waited for here.
+    tc::fence_before_sync();
+    __syncthreads();
+    if (dead_flag && warp == 12) {
+        if (lane == 0) {
+            tc::mma_commit(bar(kSFull));
+            const uint64_t t = globaltimer_ns();
+            while (globaltimer_ns() - t < 1000000ull) {
+            }
+        }
+        __syncwarp();
+    }
+    if (warp == 12) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int DIM, int FMT>
+cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream)
+{
+    static bool configured = false;
+    if (!configured) {
+        cudaError_t e = cudaFuncSetAttribute(k_attn_tc<DIM, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             TcShape<DIM>::SMEM);
+        if (e != cudaSuccess)
+            return e;
+        configured = true;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = TcShape<DIM>::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_attn_tc<DIM, FMT>, p);
+}
+
+}  // namespace
+
+size_t attn_tc_scratch(uint8_t *base, int sms, AttnScratch *s)
+{
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        uint8_t *p = base + at;
+        at += (bytes + 255) & ~size_t(255);
+        return p;
+    };
+    AttnScratch t{};
+    t.cta_o = reinterpret_cast<float *>(take(size_t(sms) * 2 * kRows * 128 * sizeof(float)));
+    t.cta_ml = reinterpret_cast<float2 *>(take(size_t(sms) * 2 * kRows * sizeof(float2)));
+    t.arrived = reinterpret_cast<int *>(take(size_t(sms) * sizeof(int)));
+    if (s)
+        *s = t;
+    return at;
+}
+
+cudaError_t launch_attn_tc(const AttnParams &p, int sms, cudaStream_t stream)
+{
+    const bool wide = p.kv.dim == 128;
+    switch (p.kv.format) {
+    case kKvBf16: return wide ? launch<128, kKvBf16>(p, sms, stream) : launch<64, kKvBf16>(p, sms, stream);
+    case kKvInt8: return wide ? launch<128, kKvInt8>(p, sms, stream) : launch<64, kKvInt8>(p, sms, stream);
+    default: return wide ? launch<128, kKvFp8>(p, sms, stream) : launch<64, kKvFp8>(p, sms, stream);
+    }
+}
+
+}  // namespace lora

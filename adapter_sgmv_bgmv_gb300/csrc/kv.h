@@ -61,8 +61,9 @@ struct AttnScratch {
     float2 *warp_ml;
     int *arrived;
 };
-// Lays the few-rows kernel's partials out in `base`; returns the bytes they take.
+// Lay the partials of the few-rows / many-rows kernel out in `base`; return their bytes.
 size_t attn_rows_scratch(uint8_t *base, int sms, AttnScratch *s);
+size_t attn_tc_scratch(uint8_t *base, int sms, AttnScratch *s);
 
 struct AttnParams {
     KvView kv;
@@ -79,8 +80,11 @@ struct AttnParams {
     int64_t min_rows, max_rows;   // sequences this launch serves: min <= new * group < max
     AttnScratch part;
     unsigned *status;
+    int behind;               // launched right behind the call's other kernel, which waited
+                              // for the stream: start at once, wait for it before the end
 };
 cudaError_t launch_attn_rows(const AttnParams &p, int sms, cudaStream_t stream);
+cudaError_t launch_attn_tc(const AttnParams &p, int sms, cudaStream_t stream);
 
 #ifdef __CUDACC__
 struct SeqInfo {

@@ -15,7 +15,7 @@ using namespace lora;
 struct lora_kv {
     lora_ctx *ctx = nullptr;           // not owned
     KvView view{};
-    AttnScratch few{};                 // in the context's scratch
+    AttnScratch few{}, many{};         // in the context's scratch
 };
 
 namespace {
@@ -25,6 +25,10 @@ namespace {
 constexpr int64_t kMaxPosition = int64_t(1) << 30;
 
 bool aligned(const void *p, uintptr_t a) { return p && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Rows (new tokens times query heads per key head) up to which a sequence's attention
+// goes to the few-rows kernel.
+constexpr int kFewRows = 32;
 
 int log2_exact(int v)
 {
@@ -146,9 +150,12 @@ int lora_kv_create(lora_ctx *ctx, const lora_kv_desc *d, lora_kv **out)
         int rc = ctx_begin(ctx, nullptr);
         if (rc == LORA_OK) {
             uint8_t *base = nullptr;
-            rc = ctx_attn_scratch(ctx, attn_rows_scratch(nullptr, ctx_sms(ctx), nullptr), &base);
-            if (rc == LORA_OK)
+            const size_t few = attn_rows_scratch(nullptr, ctx_sms(ctx), nullptr);
+            rc = ctx_attn_scratch(ctx, few + attn_tc_scratch(nullptr, ctx_sms(ctx), nullptr), &base);
+            if (rc == LORA_OK) {
                 attn_rows_scratch(base, ctx_sms(ctx), &kv->few);
+                attn_tc_scratch(base + few, ctx_sms(ctx), &kv->many);
+            }
         }
         if (rc != LORA_OK) {
             delete kv;
@@ -209,11 +216,26 @@ int lora_attention(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *b, int
     p.scale = scale;
     p.window = int(std::min<int64_t>(window, kMaxPosition));
     p.sinks = int(std::min<int64_t>(sinks, kMaxPosition));
-    p.min_rows = 1;
-    p.max_rows = int64_t(1) << 40;
-    p.part = kv->few;
     p.status = ctx_status(ctx);
-    const cudaError_t e = launch_attn_rows(p, ctx_sms(ctx), stream);
+    // Sequences of few rows (decoding, a few tokens at once) and of many go to a kernel
+    // each; which of them the batch has is known on the device only, so both are launched
+    // unless max_new leaves out the second.
+    const bool many = int64_t(p.b.max_new) * p.group > kFewRows;
+    cudaError_t e = cudaSuccess;
+    if (many) {
+        p.min_rows = kFewRows + 1;
+        p.max_rows = int64_t(1) << 40;
+        p.part = kv->many;
+        e = launch_attn_tc(p, ctx_sms(ctx), stream);
+        if (e != cudaSuccess)
+            return ctx_cuda_fail(ctx, e);
+        ctx_launched(ctx, stream, 128);
+    }
+    p.min_rows = 1;
+    p.max_rows = kFewRows + 1;
+    p.part = kv->few;
+    p.behind = many;
+    e = launch_attn_rows(p, ctx_sms(ctx), stream);
     if (e != cudaSuccess)
         return ctx_cuda_fail(ctx, e);
     ctx_launched(ctx, stream, 64);
