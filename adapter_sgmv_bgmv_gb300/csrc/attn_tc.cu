@@ -38,13 +38,19 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 512;        // warps 13-15 only take part in the block's barriers
+constexpr int kThreads = 512;
 constexpr int kM = 128;              // rows of a row tile
 constexpr int kRows = 2 * kM;
 constexpr int kKeys = 128;           // keys of a key tile
 constexpr int kUnitCost = 2;         // a unit's start and end, in key tiles
 constexpr int kScaleSlots = 4;
-constexpr int kMoreRegs = 152, kLoadRegs = 112, kFewRegs = 96;   // of 512 x 128 at launch
+// Registers, of 512 x 128 at launch: the warps of the loads and of the products (three of
+// which are there for their registers alone) give some to the weights.
+template <int FMT>
+struct Regs {
+    static constexpr int more = FMT == kKvBf16 ? 184 : 176, load = FMT == kKvBf16 ? 80 : 96, few = 64;
+    static_assert(2 * more + load + few == 512, "the registers of the block");
+};
 
 template <int DIM>
 struct TcShape {
@@ -64,7 +70,8 @@ enum Bar : uint32_t {
     kFull = 0, kEmpty = 8, kQFull = 16, kQEmpty = 18, kSFull = 20, kWReady = 22, kPvDone = 24
 };
 
-__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMoreRegs)); }
+template <int R>
+__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
 __device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
@@ -77,20 +84,6 @@ __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b_de
         ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(acc) : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t r[32])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-        ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
 __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t r[16])
 {
     asm volatile(
@@ -100,6 +93,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t r[16])
         "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
         "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16_raw(uint32_t a, uint32_t r[16])
+{
+    float v[16];
+    tc::tmem_ld16(a, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        r[i] = __float_as_uint(v[i]);
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -173,17 +175,6 @@ struct Walk {
         Cut::next(p, u);
         enter(p);
     }
-    // First key of tile `i` and the end of the keys to read.
-    __device__ __forceinline__ void keys(int i, int &j0, int &j1) const
-    {
-        if (i < u.span.n_sink) {
-            j0 = i * kKeys;
-            j1 = u.span.sink;
-        } else {
-            j0 = u.span.lo + (i - u.span.n_sink) * kKeys;
-            j1 = u.span.hi;
-        }
-    }
 };
 
 // One row tile of a unit: its rows, and the positions of its first and last token.
@@ -202,18 +193,25 @@ __device__ __forceinline__ Side side_of(const AttnParams &p, const Cursor &u, in
     return s;
 }
 
-// Whether any row of the tile sees a key of [j0, j0 + kKeys): the products of the others are
-// left out.
-template <typename W>
-__device__ __forceinline__ bool busy(const AttnParams &p, const W &w, const Side &s, int i)
+// The key tiles in which any row of a row tile sees a key: those before `behind` and from
+// `from` on, short of `to`.  The products of the others are left out.
+struct Active {
+    int from, to, behind;
+    __device__ __forceinline__ bool operator()(int t) const { return t < to && (t >= from || t < behind); }
+};
+
+__device__ __forceinline__ Active active(const AttnParams &p, const Cursor &u, const Side &s)
 {
-    if (s.rows == 0)
-        return false;
-    int j0, j1;
-    w.keys(i, j0, j1);
-    if (j0 > s.p_last)
-        return false;
-    return i < w.u.span.n_sink || p.window == 0 || j0 + kKeys - 1 > s.p_first - p.window || j0 < p.sinks;
+    const Span &k = u.span;
+    Active a{0, 0, 0};
+    if (s.rows == 0 || s.p_last < 0)
+        return a;
+    a.to = k.n_sink + (s.p_last >= k.lo ? (s.p_last - k.lo) / kKeys + 1 : 0);
+    if (p.window) {
+        a.from = k.n_sink + max(0, s.p_first - p.window + 1 - k.lo) / kKeys;
+        a.behind = k.n_sink + (p.sinks > k.lo ? (p.sinks - k.lo + kKeys - 1) / kKeys : 0);
+    }
+    return a;
 }
 
 // Four codes (bytes 0..3) to bf16, in order.
@@ -238,6 +236,94 @@ __device__ __forceinline__ uint2 widen4(uint32_t r)
     return y;
 }
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)),
+          "l"(*reinterpret_cast<uint64_t *>(&c)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+
+// s[i] *= k[i], k in shared memory (the same for every row).
+__device__ __forceinline__ void scale_row(float s[128], const float *k)
+{
+#pragma unroll
+    for (int i = 0; i < 128; i += 4) {
+        const float4 k4 = *reinterpret_cast<const float4 *>(k + i);
+        const float2 a = mul2(make_float2(s[i], s[i + 1]), make_float2(k4.x, k4.y));
+        const float2 b = mul2(make_float2(s[i + 2], s[i + 3]), make_float2(k4.z, k4.w));
+        s[i] = a.x, s[i + 1] = a.y, s[i + 2] = b.x, s[i + 3] = b.y;
+    }
+}
+
+__device__ __forceinline__ float maximum(const float s[128])
+{
+    float mx[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        mx[e] = s[e];
+#pragma unroll
+    for (int i = 8; i < 120; i += 16)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            mx[e] = fmaxf(mx[e], fmaxf(s[i + e], s[i + 8 + e]));
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        mx[e] = fmaxf(mx[e], s[120 + e]);
+    return fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+}
+
+// The weights exp2(s * f - m) of this thread's row, written as bf16 (times the values'
+// scales vs) over the columns of S they came from; returns their sum.
+template <int FMT>
+__device__ __forceinline__ float weights(uint32_t r[128], uint32_t tS, const float *vs, float f, float m)
+{
+    const float *s = reinterpret_cast<const float *>(r);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    const float2 ff = make_float2(f, f), less = make_float2(-m, -m);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const float *x = s + 32 * h + i;
+            float2 a = fma2(make_float2(x[0], x[1]), ff, less), b = fma2(make_float2(x[2], x[3]), ff, less);
+            a.x = exp2_fast(a.x), a.y = exp2_fast(a.y), b.x = exp2_fast(b.x), b.y = exp2_fast(b.y);
+            sum[0] = add2(sum[0], a);
+            sum[1] = add2(sum[1], b);
+            if (FMT != kKvBf16) {
+                const float4 v4 = *reinterpret_cast<const float4 *>(vs + 32 * h + i);
+                a = mul2(a, make_float2(v4.x, v4.y));
+                b = mul2(b, make_float2(v4.z, v4.w));
+            }
+            pk[i / 2] = pack2(a.x, a.y);
+            pk[i / 2 + 1] = pack2(b.x, b.y);
+        }
+        tmem_st16(tS + 16 * h, pk);
+    }
+    return (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+}
+
 template <int DIM, int FMT>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__ AttnParams p)
 {
@@ -250,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     __shared__ int64_t sums[kThreads / 32];
     __shared__ Cursor found[1];
     __shared__ Walk<Cut> walks[kThreads / 32];             // each warp's, out of its registers
+    __shared__ uint32_t poison[kScaleSlots * 4];           // per slot: keys whose value's scale is not finite
     __shared__ Cursor units[4];                            // the load warps' unit whose queries come next
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_flag, last_flag;
@@ -291,12 +378,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
 
     if (warp < 8) {
         // ------------------------------------------------------------ weights
-        setmaxnreg_inc();
+        setmaxnreg_inc<Regs<FMT>::more>();
         const int T = warp >> 2, row = tid & 127;
         const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + T * 128u, tO = tmem + lanes + 256u + T * uint32_t(DIM);
         const float sl = p.scale * 1.4426950408889634f;
-        const bool scaled = FMT != kKvBf16 || sl <= 0.f;   // scores scaled before the maximum
         uint32_t n_s = 0;                                  // S tiles taken so far
         int tile_no = 0;                                   // key tiles of the CTA so far
         Walk<Cut> &w = walks[warp];
@@ -310,72 +396,68 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         while (w.more) {
             const int t0 = w.t0, t1 = w.t1;
             const Side sd = side_of(p, u, T);
-            int64_t token, col;
-            int pos;
-            const bool on = row < sd.rows;
-            row_place<kRows, DIM>(p, u, on ? T * kM + row : 0, token, col, pos);
-            if (!on)
-                pos = -1;
+            const Active act = active(p, u, sd);
+            const int n_sink = u.span.n_sink, lo = u.span.lo, sink_end = u.span.sink;
+            int pos = -1;
+            if (row < sd.rows)
+                pos = u.q.len - u.q.n_new + (u.r * kRows + T * kM + row) / p.group;
             float ref = -INFINITY, l = 0.f;
             bool begun = false;
+#pragma unroll 1
             for (int t = t0; t < t1; ++t, ++tile_no) {
-                if (!busy(p, w, sd, t))
+                if (!act(t))
                     continue;
+                const bool sink = t < n_sink;
+                const int j0 = sink ? t * kKeys : lo + (t - n_sink) * kKeys;
+                const bool masked = j0 + kKeys - 1 > sd.p_first || (sink && j0 + kKeys > sink_end) ||
+                                    (p.window && !sink && j0 <= sd.p_last - p.window);
+                const float *ks = reinterpret_cast<const float *>(smem + S::SCALES) + (tile_no % kScaleSlots) * 2 * kKeys;
                 ok = __all_sync(0xffffffffu, await(bar(kSFull + T), n_s & 1, dead, p.status, kDevTimeoutMma)) && ok;
                 if (!ok)
                     continue;
                 tc::fence_after_sync();
-                const float *ks = reinterpret_cast<const float *>(smem + S::SCALES) + (tile_no % kScaleSlots) * 2 * kKeys;
-                int j0, j1;
-                w.keys(t, j0, j1);
-                const bool sink = t < u.span.n_sink;
-                const bool masked = j0 + kKeys - 1 > sd.p_first || (sink && j1 - j0 < kKeys) ||
-                                    (p.window && !sink && j0 <= sd.p_last - p.window);
-                const int hi = (sink ? min(pos, j1 - 1) : pos) - j0;            // last key seen
-                const int lo = p.window && !sink ? pos - p.window - j0 : -1;   // last hidden behind the window
-                const int sk = p.sinks - j0;
-                auto hidden = [&](int i) { return i > hi || (i <= lo && i >= sk); };
-                // first over S: the maximum
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                {
-                    uint32_t r[2][32];
-                    tc::tmem_ld32_nowait(tS, r[0]);
-                    tc::tmem_wait_ld();
+                const uint32_t *odd = poison + (tile_no % kScaleSlots) * 4;
+                const bool rework = masked || (FMT == kKvBf16 ? sl <= 0.f : (odd[0] | odd[1] | odd[2] | odd[3]) != 0);
+                if (rework) {
+                    // the few tiles at an edge of what the rows see: scores scaled and hidden
+                    // in place, so that the pass below has one form
+                    const int hi = (sink ? min(pos, sink_end - 1) : pos) - j0;     // last key seen
+                    const int behind = p.window && !sink ? pos - p.window - j0 : -1;
+                    const int kept = p.sinks - j0;
+#pragma unroll 1
+                    for (int i = 0; i < 128; i += 16) {
+                        uint32_t v[16];
+                        tmem_ld16_raw(tS + i, v);
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        if (h < 3)
-                            tc::tmem_ld32_nowait(tS + 32 * (h + 1), r[(h + 1) & 1]);
-                        float *s = reinterpret_cast<float *>(r[h & 1]);
-                        if (FMT != kKvBf16) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 k4 = *reinterpret_cast<const float4 *>(ks + 32 * h + i);
-                                s[i] *= k4.x;
-                                s[i + 1] *= k4.y;
-                                s[i + 2] *= k4.z;
-                                s[i + 3] *= k4.w;
+                        for (int e = 0; e < 16; ++e) {
+                            const int k = i + e;
+                            float x = __uint_as_float(v[e]);
+                            if (FMT != kKvBf16) {
+                                x *= ks[k];
+                                // a value's scale that is not finite makes the row's sum a NaN
+                                if (odd[k >> 5] >> (k & 31) & 1)
+                                    x = __int_as_float(0x7fffffff);
+                            } else if (sl <= 0.f) {
+                                x *= sl;
                             }
-                        } else if (scaled) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                s[i] *= sl;
+                            if (k > hi || (k <= behind && k >= kept))
+                                x = -INFINITY;
+                            v[e] = __float_as_uint(x);
                         }
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (hidden(32 * h + i))
-                                    s[i] = -INFINITY;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                mx[e] = fmaxf(mx[e], fmaxf(s[i + e], s[i + e + 4]));
-                        tc::tmem_wait_ld();
+                        tmem_st16(tS + i, v);
                     }
+                    tmem_wait_st();
                 }
-                const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                const float top = scaled ? most : most * sl;
+                uint32_t r[128];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tc::tmem_ld32_nowait(tS + 32 * i, r + 32 * i);
+                tc::tmem_wait_ld();
+                float *s = reinterpret_cast<float *>(r);
+                if (FMT != kKvBf16 && !rework)
+                    scale_row(s, ks);
+                const float f = FMT == kKvBf16 && sl > 0.f ? sl : 1.f;
+                const float top = maximum(s) * f;
                 const bool move = top > ref + 8.f;         // the first tile's always does
                 if (__any_sync(0xffffffffu, move)) {
                     const float a = move ? exp2_fast(ref - top) : 1.f;
@@ -385,60 +467,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     if (begun) {                           // the products so far, at rest
                         ok = __all_sync(0xffffffffu, await(bar(kPvDone + T), (n_s - 1) & 1, dead, p.status, kDevTimeoutMma)) && ok;
                         tc::fence_after_sync();
-                        if (ok) {
 #pragma unroll 1
-                            for (int i = 0; i < DIM / 32; ++i) {
-                                uint32_t v[32];
-                                tc::tmem_ld32_nowait(tO + 32 * i, v);
-                                tc::tmem_wait_ld();
+                        for (int i = 0; i < DIM / 16 && ok; ++i) {
+                            uint32_t v[16];
+                            tmem_ld16_raw(tO + 16 * i, v);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
-                                tmem_st32(tO + 32 * i, v);
-                            }
+                            for (int e = 0; e < 16; ++e)
+                                v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
+                            tmem_st16(tO + 16 * i, v);
                         }
                     }
                 }
-                // then the weights, each 32 over the S they came from
-                const float m = ref == -INFINITY ? 0.f : ref;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                {
-                    uint32_t r[2][32];
-                    tc::tmem_ld32_nowait(tS, r[0]);
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        if (h < 3)
-                            tc::tmem_ld32_nowait(tS + 32 * (h + 1), r[(h + 1) & 1]);
-                        const float *s = reinterpret_cast<const float *>(r[h & 1]);
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            float kf[4] = {sl, sl, sl, sl}, vf[4], e4[4];
-                            if (FMT != kKvBf16) {
-                                const float4 k4 = *reinterpret_cast<const float4 *>(ks + 32 * h + i);
-                                const float4 v4 = *reinterpret_cast<const float4 *>(ks + kKeys + 32 * h + i);
-                                kf[0] = k4.x, kf[1] = k4.y, kf[2] = k4.z, kf[3] = k4.w;
-                                vf[0] = v4.x, vf[1] = v4.y, vf[2] = v4.z, vf[3] = v4.w;
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float x = fmaf(s[i + e], kf[e], -m);
-                                if (masked && hidden(32 * h + i + e))
-                                    x = -INFINITY;
-                                const float q = exp2_fast(x);
-                                sum[e] += q;
-                                // a key that is not seen has weight 0 whatever its scale is
-                                e4[e] = FMT == kKvBf16 ? q : masked && x == -INFINITY ? 0.f : q * vf[e];
-                            }
-                            pk[i / 2] = pack2(e4[0], e4[1]);
-                            pk[i / 2 + 1] = pack2(e4[2], e4[3]);
-                        }
-                        tc::tmem_wait_ld();
-                        tmem_st16(tS + 16 * h, pk);
-                    }
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += weights<FMT>(r, tS, ks + kKeys, f, ref == -INFINITY ? 0.f : ref);
                 tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
@@ -452,8 +492,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 ok = __all_sync(0xffffffffu, await(bar(kPvDone + T), (n_s - 1) & 1, dead, p.status, kDevTimeoutMma)) && ok;
                 tc::fence_after_sync();
             }
-            const bool begins = t0 == 0, ends = t1 == u.span.n;
+            const bool begins = t0 == 0, ends = t1 == u.span.n, on = row < sd.rows;
             if (begins && ends) {
+                int64_t token, col;
+                row_place<kRows, DIM>(p, u, on ? T * kM + row : 0, token, col, pos);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 bool fine = true;
                 uint16_t *dst = p.out + token * p.ldo + col;
@@ -540,9 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         }
     } else if (warp < 12) {
         // ------------------------------------------------------------ loads
-        setmaxnreg_dec<kLoadRegs>();
+        setmaxnreg_dec<Regs<FMT>::load>();
         const int lw = warp - 8;                           // this warp's 32 keys (or rows) of a tile
-        const int32_t *table = p.b.pages;
         Walk<Cut> &w = walks[warp];
         if (lane == 0) {
             w.more = any;
@@ -550,23 +591,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 w.start(p, found[0], x0, x1);
         }
         __syncwarp();
-        auto step = [&]() {
-            __syncwarp();
-            if (lane == 0)
-                w.step(p);
-            __syncwarp();
+        Cursor &unit = units[lw];
+        // this warp's tile: its unit's table row, pools at its head, and the keys
+        const int32_t *table = nullptr;
+        const uint8_t *kp = nullptr, *vp = nullptr;
+        int64_t s_head = 0;
+        int t = 0, t1 = 0, n_sink = 0, lo = 0, hi = 0, sink_end = 0;
+        bool more = false, fresh = false;
+        auto enter = [&]() {
+            more = w.more;
+            if (!more)
+                return;
+            const Cursor &u = w.u;
+            table = p.b.pages + int64_t(u.s) * p.b.ld_pages;
+            kp = kv.k + u.h * kv.head_stride;
+            vp = kv.v + u.h * kv.head_stride;
+            s_head = u.h * kv.s_head;
+            t = w.t0, t1 = w.t1, n_sink = u.span.n_sink, lo = u.span.lo, hi = u.span.hi, sink_end = u.span.sink;
+            fresh = true;
         };
-        uint32_t entry = 0;                                // ring entries so far: keys 2j, values 2j + 1
+        auto step = [&]() {
+            fresh = false;
+            if (++t < t1)
+                return;
+            __syncwarp();
+            if (lane == 0) {
+                w.t = t1 - 1;
+                w.step(p);
+            }
+            __syncwarp();
+            enter();
+        };
+        uint32_t entry = 0, slot = 0, phase = 1;           // ring entries: keys 2j, values 2j + 1
         int part = 0, tile_no = 0;
         uint32_t pending = 0;                              // barrier of the copies under way
 
-        auto page_id = [&](const Walk<Cut> &k) -> int {
-            int j0, j1;
-            k.keys(k.t, j0, j1);
-            const int j = j0 + lw * 32 + lane;
-            return j < j1 ? table[int64_t(k.u.s) * p.b.ld_pages + page_of(kv, j)] : INT_MIN;
+        auto key_of = [&](int &j) -> bool {                // this lane's key of the tile
+            const bool sink = t < n_sink;
+            j = (sink ? t * kKeys : lo + (t - n_sink) * kKeys) + lw * 32 + lane;
+            return j < (sink ? sink_end : hi);
         };
-        auto place = [&](const Walk<Cut> &k, int page, int64_t &at, int64_t &s_at) {
+        auto page_id = [&]() -> int {
+            int j;
+            return more && key_of(j) ? table[page_of(kv, j)] : INT_MIN;
+        };
+        auto place = [&](int page, int64_t &at, int64_t &s_at) {
             at = -1;
             s_at = 0;
             if (page == INT_MIN)
@@ -575,12 +644,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 raise_status(p.status, kDevBadPage);
                 return;
             }
-            int j0, j1;
-            k.keys(k.t, j0, j1);
-            const int j = j0 + lw * 32 + lane;
+            int j;
+            key_of(j);
             const int cell = j - page_of(kv, j) * kv.page_size;
-            at = page * kv.page_stride + cell * kv.cell_stride + k.u.h * kv.head_stride;
-            s_at = page * kv.s_page + cell * kv.s_cell + k.u.h * kv.s_head;
+            at = page * kv.page_stride + cell * kv.cell_stride;
+            s_at = page * kv.s_page + cell * kv.s_cell + s_head;
         };
         // The copies before the last commit are in shared memory: hand them over.
         auto settle = [&](bool all) {
@@ -593,11 +661,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             if (pending && lane == 0)
                 mbar_arrive(pending);
         };
-        auto stage = [&](uint32_t e) { return sm + S::RING + (e % ST) * S::TILE; };
-        auto wait_empty = [&](uint32_t e) {
-            if (e >= uint32_t(ST))
-                ok = await(bar(kEmpty + e % ST), (e / ST - 1) & 1, dead, p.status, kDevTimeoutPipe) && ok;
+        auto wait_empty = [&]() {
+            if (entry >= uint32_t(ST))
+                ok = await(bar(kEmpty + slot), phase, dead, p.status, kDevTimeoutPipe) && ok;
             ok = __all_sync(0xffffffffu, ok);
+        };
+        auto advance = [&]() {
+            ++entry;
+            if (++slot == uint32_t(ST))
+                slot = 0, phase ^= 1;
         };
         constexpr int CH = DIM / 8, RPI = 32 / CH;         // 16-byte chunks of a bf16 row, rows an instruction
         auto copy_rows = [&](uint32_t dst, const uint8_t *src, int64_t at) {
@@ -630,26 +702,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             ++part;
         };
 
-        int page = w.more ? page_id(w) : INT_MIN;
-        Cursor &unit = units[lw];
+        enter();
+        int page = page_id();
+        int64_t at, s_at;
         if (FMT == kKvBf16) {
-            while (w.more) {
-                const bool fresh = w.t == w.t0;
-                int64_t at, s_at;
-                place(w, page, at, s_at);
+            while (more) {
+                place(page, at, s_at);
+                const uint8_t *src[2] = {kp, vp};
+                const bool queries = fresh;
                 if (fresh && lane == 0)
                     unit = w.u;
+                __syncwarp();
                 step();
-                page = w.more ? page_id(w) : INT_MIN;      // on its way during this tile
+                page = page_id();                          // on its way during this tile
+#pragma unroll
                 for (int side = 0; side < 2; ++side) {
-                    wait_empty(entry);
+                    wait_empty();
                     if (ok)
-                        copy_rows(stage(entry), side ? kv.v : kv.k, at);
+                        copy_rows(sm + S::RING + slot * S::TILE, src[side], at);
                     tc::cp_async_commit();
                     settle(false);
-                    pending = bar(kFull + entry % ST);
-                    ++entry;
-                    if (side == 0 && fresh)
+                    pending = bar(kFull + slot);
+                    advance();
+                    if (side == 0 && queries)
                         load_q(unit);
                 }
             }
@@ -682,144 +757,156 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             const float sl = p.scale * 1.4426950408889634f;
             uint4 kx[C8], vx[C8];
             float ks = 0.f, vs = 0.f;
-            int64_t at = -1, s_at = 0;
             auto scales = [&]() {
                 ks = at < 0 ? 0.f : kv.k_scale[s_at] * sl;
                 vs = at < 0 ? 0.f : kv.v_scale[s_at];
             };
-            if (w.more) {
-                place(w, page, at, s_at);
-                fetch(kx, kv.k, at);
+            if (more) {
+                place(page, at, s_at);
+                fetch(kx, kp, at);
                 scales();
             }
-            while (w.more) {
-                const bool fresh = w.t == w.t0;
-                fetch(vx, kv.v, at);
+            while (more) {
+                const bool queries = fresh;
+                fetch(vx, vp, at);
                 if (fresh && lane == 0)
                     unit = w.u;
+                __syncwarp();
                 step();
-                page = w.more ? page_id(w) : INT_MIN;
-                wait_empty(entry);
+                page = page_id();
+                wait_empty();
                 if (ok) {
-                    store(stage(entry), kx);
+                    store(sm + S::RING + slot * S::TILE, kx);
                     float *sc = reinterpret_cast<float *>(smem + S::SCALES) + (tile_no % kScaleSlots) * 2 * kKeys + lw * 32 + lane;
+                    const bool fine = fabsf(vs) < INFINITY;
                     sc[0] = ks;
-                    sc[kKeys] = vs;
+                    sc[kKeys] = fine ? vs : 0.f;
+                    const unsigned bad = __ballot_sync(0xffffffffu, !fine);
+                    if (lane == 0)
+                        poison[(tile_no % kScaleSlots) * 4 + lw] = bad;
                 }
-                hand_over(bar(kFull + entry % ST));
-                ++entry;
-                if (fresh) {
+                hand_over(bar(kFull + slot));
+                advance();
+                if (queries) {
                     pending = 0;
                     load_q(unit);
                     settle(true);
                 }
-                if (w.more) {
-                    place(w, page, at, s_at);
-                    fetch(kx, kv.k, at);
+                if (more) {
+                    place(page, at, s_at);
+                    fetch(kx, kp, at);
                     scales();
                 }
-                wait_empty(entry);
+                wait_empty();
                 if (ok)
-                    store(stage(entry), vx);
-                hand_over(bar(kFull + entry % ST));
-                ++entry;
+                    store(sm + S::RING + slot * S::TILE, vx);
+                hand_over(bar(kFull + slot));
+                advance();
                 ++tile_no;
             }
         }
     } else {
         // ------------------------------------------------------------ products
-        setmaxnreg_dec<kFewRegs>();
+        setmaxnreg_dec<Regs<FMT>::few>();
         if (warp == 12 && lane == 0 && any) {
             constexpr uint32_t iqk = tc::idesc_bf16(kM, kKeys, 0, 0), ipv = tc::idesc_bf16(kM, DIM, 0, 1);
+            const uint64_t q_desc = tc::smem_desc_sw128(sm, 16u, 1024u), k_desc = tc::smem_desc_sw128(sm + S::RING, 16u, 1024u),
+                           v_desc = tc::smem_desc_sw128(sm + S::RING, S::HALF, 1024u);
+            constexpr uint32_t kTile16 = S::TILE / 16, kHalf16 = S::HALF / 16;   // descriptor units
             Walk<Cut> &w = walks[warp];
             w.start(p, found[0], x0, x1);
-            uint32_t tile = 0, n_w[2] = {0, 0};
+            // ring slots of the keys and values in turn: keys 2j, values 2j + 1
+            uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0, n_w[2] = {0, 0};
+            auto next_slot = [&](uint32_t &slot, uint32_t &phase) {
+                slot += 2;
+                if (slot >= uint32_t(ST))
+                    slot -= ST, phase ^= 1;
+            };
             int part = 0;
             bool first_pv[2] = {true, true};
-            auto scores = [&](int T, bool act, bool last) {   // S of tile `tile`
+            auto scores = [&](int T, bool act, bool last) {
                 if (act) {
-                    ok = ok && await(bar(kFull + (2 * tile) % ST), (2 * tile / ST) & 1, dead, p.status, kDevTimeoutLoad);
+                    ok = ok && await(bar(kFull + k_slot), k_phase, dead, p.status, kDevTimeoutLoad);
                     ok = ok && await(bar(kQFull + T), part & 1, dead, p.status, kDevTimeoutLoad);
                     if (ok) {
                         tc::fence_after_sync();
-                        const uint32_t q = sm + T * S::TILE, k = sm + S::RING + ((2 * tile) % ST) * S::TILE;
+                        const uint64_t q = q_desc + T * kTile16, k = k_desc + k_slot * kTile16;
 #pragma unroll
                         for (int i = 0; i < DIM / 16; ++i)
-                            tc::mma_bf16(tmem + T * 128u,
-                                         tc::smem_desc_sw128(q + (i / 4) * S::HALF + 32u * (i % 4), 16u, 1024u),
-                                         tc::smem_desc_sw128(k + (i / 4) * S::HALF + 32u * (i % 4), 16u, 1024u), iqk, i > 0);
+                            tc::mma_bf16(tmem + T * 128u, q + (i / 4) * kHalf16 + 2 * (i % 4),
+                                         k + (i / 4) * kHalf16 + 2 * (i % 4), iqk, i > 0);
                         tc::mma_commit(bar(kSFull + T));
                     }
                 }
                 if (last && ok)
                     tc::mma_commit(bar(kQEmpty + T));
             };
-            auto sums_ = [&](int T, bool act) {               // O += W V of tile `tile`
+            auto sums_ = [&](int T, bool act) {               // O += W V
                 if (!act)
                     return;
+                ok = ok && await(bar(kFull + v_slot), v_phase, dead, p.status, kDevTimeoutLoad);
                 ok = ok && await(bar(kWReady + T), n_w[T] & 1, dead, p.status, kDevTimeoutPipe);
-                ok = ok && await(bar(kFull + (2 * tile + 1) % ST), ((2 * tile + 1) / ST) & 1, dead, p.status, kDevTimeoutLoad);
                 ++n_w[T];
                 if (ok) {
                     tc::fence_after_sync();
-                    const uint32_t v = sm + S::RING + ((2 * tile + 1) % ST) * S::TILE;
+                    const uint64_t v = v_desc + v_slot * kTile16;
 #pragma unroll
                     for (int i = 0; i < kKeys / 16; ++i)
-                        mma_tmem_a(tmem + 256u + T * uint32_t(DIM), tmem + T * 128u + 8 * i,
-                                   tc::smem_desc_sw128(v + 2048u * i, S::HALF, 1024u), ipv, !(first_pv[T] && i == 0));
+                        mma_tmem_a(tmem + 256u + T * uint32_t(DIM), tmem + T * 128u + 8 * i, v + 128 * i, ipv,
+                                   !(first_pv[T] && i == 0));
                     tc::mma_commit(bar(kPvDone + T));
                 }
                 first_pv[T] = false;
             };
-            Side sd[2] = {side_of(p, w.u, 0), side_of(p, w.u, 1)};
-            bool act[2];
-            for (int T = 0; T < 2 && w.more; ++T) {
-                act[T] = busy(p, w, sd[T], w.t);
-                scores(T, act[T], w.t + 1 == w.t1);
+            // this part's tiles: which of them are A's and B's, and the last
+            Active act[2];
+            int t = 0, t1 = 0;
+            auto enter = [&]() {
+                for (int T = 0; T < 2; ++T)
+                    act[T] = active(p, w.u, side_of(p, w.u, T));
+                t = w.t0;
+                t1 = w.t1;
+            };
+            bool more = w.more;
+            if (more) {
+                enter();
+                scores(0, act[0](t), t + 1 == t1);
+                scores(1, act[1](t), t + 1 == t1);
+                if (ok)
+                    tc::mma_commit(bar(kEmpty + k_slot));
+                next_slot(k_slot, k_phase);
             }
-            if (w.more && ok)
-                tc::mma_commit(bar(kEmpty + 0));
-            while (w.more) {
-                const bool unit_end = w.t + 1 == w.t1;
-                w.step(p);
-                bool next[2] = {false, false};
-                if (w.more) {
-                    if (unit_end) {
-                        sd[0] = side_of(p, w.u, 0);
-                        sd[1] = side_of(p, w.u, 1);
-                    }
-                    next[0] = busy(p, w, sd[0], w.t);
-                    next[1] = busy(p, w, sd[1], w.t);
-                }
-                const bool last = w.t + 1 == w.t1;
-                if (unit_end) {
-                    // the next unit's queries may still be on their way: both tiles' ends first
-                    sums_(0, act[0]);
-                    sums_(1, act[1]);
+            while (more) {
+                if (t + 1 < t1) {
+                    const bool last = t + 2 == t1;
+                    sums_(0, act[0](t));
+                    scores(0, act[0](t + 1), last);
+                    sums_(1, act[1](t));
                     if (ok)
-                        tc::mma_commit(bar(kEmpty + (2 * tile + 1) % ST));
+                        tc::mma_commit(bar(kEmpty + v_slot));
+                    scores(1, act[1](t + 1), last);
+                    ++t;
+                } else {
+                    // the next unit's queries may still be on their way: both tiles' ends first
+                    sums_(0, act[0](t));
+                    sums_(1, act[1](t));
+                    if (ok)
+                        tc::mma_commit(bar(kEmpty + v_slot));
                     first_pv[0] = first_pv[1] = true;
                     ++part;
-                    ++tile;
-                    if (w.more) {
-                        scores(0, next[0], last);
-                        scores(1, next[1], last);
+                    w.t = t1 - 1;
+                    w.step(p);
+                    more = w.more;
+                    if (more) {
+                        enter();
+                        scores(0, act[0](t), t + 1 == t1);
+                        scores(1, act[1](t), t + 1 == t1);
                     }
-                } else {
-                    sums_(0, act[0]);
-                    ++tile;
-                    scores(0, next[0], last);
-                    --tile;
-                    sums_(1, act[1]);
-                    if (ok)
-                        tc::mma_commit(bar(kEmpty + (2 * tile + 1) % ST));
-                    ++tile;
-                    scores(1, next[1], last);
                 }
-                if (w.more && ok)
-                    tc::mma_commit(bar(kEmpty + (2 * tile) % ST));
-                act[0] = next[0];
-                act[1] = next[1];
+                next_slot(v_slot, v_phase);
+                if (more && ok)
+                    tc::mma_commit(bar(kEmpty + k_slot));
+                next_slot(k_slot, k_phase);
             }
         }
     }
