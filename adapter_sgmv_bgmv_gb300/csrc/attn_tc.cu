@@ -48,7 +48,7 @@ constexpr int kScaleSlots = 4;
 // which are there for their registers alone) give some to the weights.
 template <int FMT>
 struct Regs {
-    static constexpr int more = FMT == kKvBf16 ? 184 : 176, load = FMT == kKvBf16 ? 80 : 96, few = 64;
+    static constexpr int more = FMT == kKvBf16 ? 152 : 144, load = FMT == kKvBf16 ? 112 : 128, few = 96;
     static_assert(2 * more + load + few == 512, "the registers of the block");
 };
 
@@ -264,62 +264,93 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     return *reinterpret_cast<float2 *>(&d);
 }
 
-// s[i] *= k[i], k in shared memory (the same for every row).
-__device__ __forceinline__ void scale_row(float s[128], const float *k)
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// The two passes over this thread's row of S (128 columns from tS), 32 columns at a time and
+// in short loops: the warps of a CTA run four different programs, and straight code of a
+// thousand instructions for each was measured to wait for instruction fetches most of
+// the time.  SCALED: times the keys' scales ks (in shared memory, the same for every row).
+
+template <bool SCALED>
+__device__ __forceinline__ float maximum(uint32_t tS, const float *ks)
 {
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    uint32_t r[64];
+    tc::tmem_ld32_nowait(tS, r);
+    tc::tmem_wait_ld();
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int i = 0; i < 128; i += 4) {
-        const float4 k4 = *reinterpret_cast<const float4 *>(k + i);
-        const float2 a = mul2(make_float2(s[i], s[i + 1]), make_float2(k4.x, k4.y));
-        const float2 b = mul2(make_float2(s[i + 2], s[i + 3]), make_float2(k4.z, k4.w));
-        s[i] = a.x, s[i + 1] = a.y, s[i + 2] = b.x, s[i + 3] = b.y;
+        for (int b = 0; b < 2; ++b) {
+            // the other half's columns are on their way during this half's
+            if (b == 0 || h == 0)
+                tc::tmem_ld32_nowait(tS + 64 * h + 32 * b + 32, r + 32 * (1 - b));
+            float *s = reinterpret_cast<float *>(r + 32 * b);
+            if (SCALED) {
+                const float4 *k4 = reinterpret_cast<const float4 *>(ks + 64 * h + 32 * b);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 k = k4[i];
+                    const float2 x = mul2(make_float2(s[4 * i], s[4 * i + 1]), make_float2(k.x, k.y));
+                    const float2 y = mul2(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(k.z, k.w));
+                    mx[0] = max3(mx[0], x.x, x.y);
+                    mx[1] = max3(mx[1], y.x, y.y);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = max3(mx[e], s[i + e], s[i + e + 4]);
+            }
+            tc::tmem_wait_ld();
+        }
     }
+    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
 
-__device__ __forceinline__ float maximum(const float s[128])
+// The weights exp2(s * f - m), written as bf16 (times the values' scales, ks + kKeys) over
+// the columns of S they came from; returns their sum.
+template <int FMT, bool SCALED>
+__device__ __forceinline__ float weights(uint32_t tS, const float *ks, float f, float m)
 {
-    float mx[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        mx[e] = s[e];
-#pragma unroll
-    for (int i = 8; i < 120; i += 16)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            mx[e] = fmaxf(mx[e], fmaxf(s[i + e], s[i + 8 + e]));
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        mx[e] = fmaxf(mx[e], s[120 + e]);
-    return fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-}
-
-// The weights exp2(s * f - m) of this thread's row, written as bf16 (times the values'
-// scales vs) over the columns of S they came from; returns their sum.
-template <int FMT>
-__device__ __forceinline__ float weights(uint32_t r[128], uint32_t tS, const float *vs, float f, float m)
-{
-    const float *s = reinterpret_cast<const float *>(r);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float2 ff = make_float2(f, f), less = make_float2(-m, -m);
+    uint32_t r[64];
+    tc::tmem_ld32_nowait(tS, r);
+    tc::tmem_wait_ld();
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        uint32_t pk[16];
+        for (int b = 0; b < 2; ++b) {
+            if (b == 0 || h == 0)
+                tc::tmem_ld32_nowait(tS + 64 * h + 32 * b + 32, r + 32 * (1 - b));
+            const float *s = reinterpret_cast<const float *>(r + 32 * b);
+            const float4 *k4 = reinterpret_cast<const float4 *>(ks + 64 * h + 32 * b);
+            uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            const float *x = s + 32 * h + i;
-            float2 a = fma2(make_float2(x[0], x[1]), ff, less), b = fma2(make_float2(x[2], x[3]), ff, less);
-            a.x = exp2_fast(a.x), a.y = exp2_fast(a.y), b.x = exp2_fast(b.x), b.y = exp2_fast(b.y);
-            sum[0] = add2(sum[0], a);
-            sum[1] = add2(sum[1], b);
-            if (FMT != kKvBf16) {
-                const float4 v4 = *reinterpret_cast<const float4 *>(vs + 32 * h + i);
-                a = mul2(a, make_float2(v4.x, v4.y));
-                b = mul2(b, make_float2(v4.z, v4.w));
+            for (int i = 0; i < 8; ++i) {
+                float2 k0 = ff, k1 = ff;
+                if (SCALED) {
+                    const float4 k = k4[i];
+                    k0 = make_float2(k.x, k.y), k1 = make_float2(k.z, k.w);
+                }
+                float2 x = fma2(make_float2(s[4 * i], s[4 * i + 1]), k0, less);
+                float2 y = fma2(make_float2(s[4 * i + 2], s[4 * i + 3]), k1, less);
+                x.x = exp2_fast(x.x), x.y = exp2_fast(x.y), y.x = exp2_fast(y.x), y.y = exp2_fast(y.y);
+                sum[0] = add2(sum[0], x);
+                sum[1] = add2(sum[1], y);
+                if (FMT != kKvBf16) {
+                    const float4 v = k4[kKeys / 4 + i];
+                    x = mul2(x, make_float2(v.x, v.y));
+                    y = mul2(y, make_float2(v.z, v.w));
+                }
+                pk[2 * i] = pack2(x.x, x.y);
+                pk[2 * i + 1] = pack2(y.x, y.y);
             }
-            pk[i / 2] = pack2(a.x, a.y);
-            pk[i / 2 + 1] = pack2(b.x, b.y);
+            tc::tmem_wait_ld();
+            tmem_st16(tS + 32 * h + 16 * b, pk);
         }
-        tmem_st16(tS + 16 * h, pk);
     }
     return (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
 }
@@ -448,16 +479,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     }
                     tmem_wait_st();
                 }
-                uint32_t r[128];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tc::tmem_ld32_nowait(tS + 32 * i, r + 32 * i);
-                tc::tmem_wait_ld();
-                float *s = reinterpret_cast<float *>(r);
-                if (FMT != kKvBf16 && !rework)
-                    scale_row(s, ks);
+                const bool plain = FMT == kKvBf16 || rework;   // no scales of the keys to apply
                 const float f = FMT == kKvBf16 && sl > 0.f ? sl : 1.f;
-                const float top = maximum(s) * f;
+                const float top = (plain ? maximum<false>(tS, ks) : maximum<true>(tS, ks)) * f;
                 const bool move = top > ref + 8.f;         // the first tile's always does
                 if (__any_sync(0xffffffffu, move)) {
                     const float a = move ? exp2_fast(ref - top) : 1.f;
@@ -478,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         }
                     }
                 }
-                l += weights<FMT>(r, tS, ks + kKeys, f, ref == -INFINITY ? 0.f : ref);
+                const float m = ref == -INFINITY ? 0.f : ref;
+                l += plain ? weights<FMT, false>(tS, ks, f, m) : weights<FMT, true>(tS, ks, f, m);
                 tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
@@ -673,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         };
         constexpr int CH = DIM / 8, RPI = 32 / CH;         // 16-byte chunks of a bf16 row, rows an instruction
         auto copy_rows = [&](uint32_t dst, const uint8_t *src, int64_t at) {
-#pragma unroll
+#pragma unroll 4
             for (int i = 0; i < CH; ++i) {
                 const int rr = i * RPI + lane / CH, ch = lane % CH, row = lw * 32 + rr;
                 const int64_t a = __shfl_sync(0xffffffffu, (long long)at, rr);
@@ -816,97 +841,107 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             Walk<Cut> &w = walks[warp];
             w.start(p, found[0], x0, x1);
             // ring slots of the keys and values in turn: keys 2j, values 2j + 1
-            uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0, n_w[2] = {0, 0};
+            uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0;
+            uint32_t w_phase = 0, started = 0;             // a bit for each row tile
             auto next_slot = [&](uint32_t &slot, uint32_t &phase) {
                 slot += 2;
                 if (slot >= uint32_t(ST))
                     slot -= ST, phase ^= 1;
             };
             int part = 0;
-            bool first_pv[2] = {true, true};
-            auto scores = [&](int T, bool act, bool last) {
-                if (act) {
-                    ok = ok && await(bar(kFull + k_slot), k_phase, dead, p.status, kDevTimeoutLoad);
-                    ok = ok && await(bar(kQFull + T), part & 1, dead, p.status, kDevTimeoutLoad);
-                    if (ok) {
-                        tc::fence_after_sync();
-                        const uint64_t q = q_desc + T * kTile16, k = k_desc + k_slot * kTile16;
+            // One step for one row tile: O += W V of the tile in v_slot, or S of the tile in
+            // k_slot.  One copy of the code for both and short loops (see the passes above).
+            auto product = [&](bool values, int T) {
+                const uint32_t slot = values ? v_slot : k_slot, phase = values ? v_phase : k_phase;
+                ok = ok && await(bar(kFull + slot), phase, dead, p.status, kDevTimeoutLoad);
+                const uint32_t other = values ? bar(kWReady + T) : bar(kQFull + T), parity = values ? w_phase >> T & 1 : part & 1;
+                ok = ok && await(other, parity, dead, p.status, kDevTimeoutPipe);
+                if (!ok)
+                    return;
+                tc::fence_after_sync();
+                if (values) {
+                    uint64_t v = v_desc + slot * kTile16;
+                    uint32_t a = tmem + T * 128u, acc = started >> T & 1;
+                    const uint32_t d = tmem + 256u + T * uint32_t(DIM);
+#pragma unroll 2
+                    for (int i = 0; i < kKeys / 16; ++i) {
+                        mma_tmem_a(d, a, v, ipv, acc);
+                        a += 8;
+                        v += 128;
+                        acc = 1;
+                    }
+                } else {
+                    uint64_t q = q_desc + T * kTile16, k = k_desc + slot * kTile16;
+                    uint32_t acc = 0;
+#pragma unroll 1
+                    for (int h = 0; h < DIM / 64; ++h) {
 #pragma unroll
-                        for (int i = 0; i < DIM / 16; ++i)
-                            tc::mma_bf16(tmem + T * 128u, q + (i / 4) * kHalf16 + 2 * (i % 4),
-                                         k + (i / 4) * kHalf16 + 2 * (i % 4), iqk, i > 0);
-                        tc::mma_commit(bar(kSFull + T));
+                        for (int i = 0; i < 4; ++i) {
+                            tc::mma_bf16(tmem + T * 128u, q + 2 * i, k + 2 * i, iqk, acc);
+                            acc = 1;
+                        }
+                        q += kHalf16;
+                        k += kHalf16;
                     }
                 }
-                if (last && ok)
-                    tc::mma_commit(bar(kQEmpty + T));
-            };
-            auto sums_ = [&](int T, bool act) {               // O += W V
-                if (!act)
-                    return;
-                ok = ok && await(bar(kFull + v_slot), v_phase, dead, p.status, kDevTimeoutLoad);
-                ok = ok && await(bar(kWReady + T), n_w[T] & 1, dead, p.status, kDevTimeoutPipe);
-                ++n_w[T];
-                if (ok) {
-                    tc::fence_after_sync();
-                    const uint64_t v = v_desc + v_slot * kTile16;
-#pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i)
-                        mma_tmem_a(tmem + 256u + T * uint32_t(DIM), tmem + T * 128u + 8 * i, v + 128 * i, ipv,
-                                   !(first_pv[T] && i == 0));
-                    tc::mma_commit(bar(kPvDone + T));
-                }
-                first_pv[T] = false;
+                tc::mma_commit(values ? bar(kPvDone + T) : bar(kSFull + T));
             };
             // this part's tiles: which of them are A's and B's, and the last
-            Active act[2];
+            Active act_a, act_b;
             int t = 0, t1 = 0;
             auto enter = [&]() {
-                for (int T = 0; T < 2; ++T)
-                    act[T] = active(p, w.u, side_of(p, w.u, T));
+                act_a = active(p, w.u, side_of(p, w.u, 0));
+                act_b = active(p, w.u, side_of(p, w.u, 1));
                 t = w.t0;
                 t1 = w.t1;
             };
-            bool more = w.more;
-            if (more) {
+            // The order of the steps: the values of tile i for A, the scores of tile i + 1 for
+            // A, then the same for B; at the end of a unit the values for both come first, as
+            // the next one's queries may still be on their way.
+            bool more = w.more, have = false;              // have: tile t's scores are out
+            if (more)
                 enter();
-                scores(0, act[0](t), t + 1 == t1);
-                scores(1, act[1](t), t + 1 == t1);
-                if (ok)
-                    tc::mma_commit(bar(kEmpty + k_slot));
-                next_slot(k_slot, k_phase);
-            }
             while (more) {
-                if (t + 1 < t1) {
-                    const bool last = t + 2 == t1;
-                    sums_(0, act[0](t));
-                    scores(0, act[0](t + 1), last);
-                    sums_(1, act[1](t));
-                    if (ok)
-                        tc::mma_commit(bar(kEmpty + v_slot));
-                    scores(1, act[1](t + 1), last);
-                    ++t;
-                } else {
-                    // the next unit's queries may still be on their way: both tiles' ends first
-                    sums_(0, act[0](t));
-                    sums_(1, act[1](t));
-                    if (ok)
-                        tc::mma_commit(bar(kEmpty + v_slot));
-                    first_pv[0] = first_pv[1] = true;
-                    ++part;
-                    w.t = t1 - 1;
-                    w.step(p);
-                    more = w.more;
-                    if (more) {
-                        enter();
-                        scores(0, act[0](t), t + 1 == t1);
-                        scores(1, act[1](t), t + 1 == t1);
+                const bool turn = have && t + 1 == t1;     // the last tile of its part
+                const bool now_a = have && act_a(t), now_b = have && act_b(t);
+#pragma unroll 1
+                for (int step = 0; step < 4; ++step) {
+                    const bool values = turn ? step < 2 : (step & 1) == 0;
+                    const int T = turn ? step & 1 : step >> 1;
+                    if (step == 2 && turn) {
+                        started = 0;
+                        ++part;
+                        w.t = t1 - 1;
+                        w.step(p);
+                        more = w.more;
+                        if (more)
+                            enter();
+                    }
+                    if (values) {
+                        if (T ? now_b : now_a) {
+                            product(true, T);
+                            w_phase ^= 1u << T;
+                            started |= 1u << T;
+                        }
+                        if (T == 1 && have && ok)
+                            tc::mma_commit(bar(kEmpty + v_slot));
+                    } else if (more) {
+                        const int i = turn || !have ? t : t + 1;
+                        if (T ? act_b(i) : act_a(i))
+                            product(false, T);
+                        if (ok && i + 1 == t1)
+                            tc::mma_commit(bar(kQEmpty + T));
+                        if (ok && T == 1)
+                            tc::mma_commit(bar(kEmpty + k_slot));
                     }
                 }
-                next_slot(v_slot, v_phase);
-                if (more && ok)
-                    tc::mma_commit(bar(kEmpty + k_slot));
+                if (have) {
+                    next_slot(v_slot, v_phase);
+                    if (!turn)
+                        ++t;
+                }
                 next_slot(k_slot, k_phase);
+                have = true;
             }
         }
     }
