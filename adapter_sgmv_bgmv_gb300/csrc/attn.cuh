@@ -49,10 +49,12 @@ __device__ __forceinline__ int row_tiles(int n_new, int group, int rows)
 // the host.  A piece [x0, x1) holds the tiles [x0 - at - OV, x1 - at - OV) of the unit at
 // `at`, as far as it has them.  Only sequences with min_rows <= rows < max_rows (rows =
 // new tokens * group) take part: the rest are another kernel's.
-struct Cursor {
-    int64_t at;               // where the unit starts on the line
-    int s, r, h;              // the unit
+struct Unit {
+    int s, r, h;              // sequence, row tile, key head
     SeqInfo q;
+};
+struct Cursor : Unit {
+    int64_t at;               // where the unit starts on the line
     Span span;
 };
 
@@ -184,7 +186,7 @@ struct Split {
 // Where row `row` of unit u is: its token among the call's rows and the first column of
 // its query head.
 template <int ROWS, int DIM>
-__device__ __forceinline__ void row_place(const AttnParams &p, const Cursor &u, int row, int64_t &token,
+__device__ __forceinline__ void row_place(const AttnParams &p, const Unit &u, int row, int64_t &token,
                                           int64_t &col, int &pos)
 {
     const int rho = u.r * ROWS + row, t = rho / p.group;
@@ -307,7 +309,7 @@ __device__ __forceinline__ void load_vec(float v[N], const float *src)
 // l * DIM / 32) over the sum of its weights l, as bf16; by careful_row where that is not
 // finite.
 template <int ROWS, int DIM, int FMT>
-__device__ __forceinline__ void finish_row(const AttnParams &p, const Cursor &u, int row,
+__device__ __noinline__ void finish_row(const AttnParams &p, const Unit &u, int row,
                                            const float o[DIM / 32], float l)
 {
     constexpr int N = DIM / 32;

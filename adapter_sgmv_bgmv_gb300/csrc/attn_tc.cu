@@ -17,6 +17,9 @@
 //                    own address (any page size, any strides); bf16 by cp.async, 8-bit codes
 //                    through registers, where they become bf16 (exact).
 //   warp 12          one thread issues the products.
+//   warp 13          one thread goes along the CTA's piece ahead of the others and leaves
+//                    them what they need of each unit (the only copy of that code: see below
+//                    on code size).
 //
 // TMEM (512 columns): S of A and B (128 each, W in their first half), O of A and B (dim).
 // The products of one thread run in the order of their issue, so the next S may be issued
@@ -48,7 +51,7 @@ constexpr int kScaleSlots = 4;
 // which are there for their registers alone) give some to the weights.
 template <int FMT>
 struct Regs {
-    static constexpr int more = FMT == kKvBf16 ? 152 : 144, load = FMT == kKvBf16 ? 112 : 128, few = 96;
+    static constexpr int more = 152, load = 120, few = 88;
     static_assert(2 * more + load + few == 512, "the registers of the block");
 };
 
@@ -61,13 +64,14 @@ struct TcShape {
     static constexpr uint32_t RING = 2 * TILE;               // after the two Q tiles
     static constexpr uint32_t SCALES = RING + STAGES * TILE; // [slot][k, v][128] floats
     static constexpr uint32_t BARS = SCALES + kScaleSlots * 2 * kKeys * 4;
-    static constexpr uint32_t BYTES = BARS + 256;
+    static constexpr uint32_t BYTES = BARS + 512;
     static constexpr uint32_t SMEM = BYTES + 1024;
 };
 
 // Barriers, 8 bytes each from BARS.
 enum Bar : uint32_t {
-    kFull = 0, kEmpty = 8, kQFull = 16, kQEmpty = 18, kSFull = 20, kWReady = 22, kPvDone = 24
+    kFull = 0, kEmpty = 8, kQFull = 16, kQEmpty = 18, kSFull = 20, kWReady = 22, kPvDone = 24,
+    kPartFull = 26, kPartEmpty = 30, kJoin = 34
 };
 
 template <int R>
@@ -113,7 +117,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 }
 
 // Bounded wait of a role: after one that ran out (here or in another warp) every wait of
-// the block gives up at once, and the roles go through their loops without the work.
+// the block gives up at once, and the roles leave their loops.
 __device__ __forceinline__ bool await(uint32_t bar, uint32_t parity, volatile int *dead, unsigned *status, unsigned code)
 {
     if (mbar_try_wait(bar, parity))
@@ -130,59 +134,12 @@ __device__ __forceinline__ bool await(uint32_t bar, uint32_t parity, volatile in
     return false;
 }
 
-// A warp's way along its CTA's piece: the unit, and the key tiles [t0, t1) of it that are
-// here.  It lies in shared memory: one lane moves it, all read it.
-template <typename Cut>
-struct Walk {
-    Cursor u;
-    int64_t x, x1;
-    int t, t0, t1;
-    bool more;                // t is a tile; false past the end
-
-    __device__ __forceinline__ void start(const AttnParams &p, const Cursor &c, int64_t from, int64_t to)
-    {
-        u = c;
-        x = from;
-        x1 = to;
-        more = true;
-        enter(p);
-    }
-    // The next unit (from x on) that has tiles here.
-    __device__ __forceinline__ void enter(const AttnParams &p)
-    {
-        while (true) {
-            const int64_t first = u.at + kUnitCost, end = first + u.span.n;
-            t0 = t = int(max(x - first, int64_t(0)));
-            t1 = int(max(min(x1, end) - first, int64_t(0)));
-            x = end;
-            if (t1 > t0)
-                return;
-            if (x >= x1) {
-                more = false;
-                return;
-            }
-            Cut::next(p, u);
-        }
-    }
-    __device__ __forceinline__ void step(const AttnParams &p)
-    {
-        if (++t < t1)
-            return;
-        if (x >= x1) {
-            more = false;
-            return;
-        }
-        Cut::next(p, u);
-        enter(p);
-    }
-};
-
 // One row tile of a unit: its rows, and the positions of its first and last token.
 struct Side {
     int rows, p_first, p_last;
 };
 
-__device__ __forceinline__ Side side_of(const AttnParams &p, const Cursor &u, int tile)
+__device__ __forceinline__ Side side_of(const AttnParams &p, const Unit &u, int tile)
 {
     Side s;
     const int rho = u.r * kRows + tile * kM, all = u.q.n_new * p.group;
@@ -213,6 +170,18 @@ __device__ __forceinline__ Active active(const AttnParams &p, const Cursor &u, c
     }
     return a;
 }
+
+// What a CTA has of one unit: key tiles [t0, t1), of which the first n_sink hold the first
+// tokens, [0, sink), and the others [lo, hi).
+struct Part : Unit {
+    int t0, t1, n_sink, lo, hi, sink;
+    int more;                 // 0: past the last part
+    int begins, ends;         // holds the unit's first / last tile
+    int first, last;          // the CTAs that have parts of the unit
+    Side side[2];
+    Active act[2];
+};
+constexpr int kParts = 4;     // parts under way at once
 
 // Four codes (bytes 0..3) to bf16, in order.
 template <int FMT>
@@ -355,6 +324,23 @@ __device__ __forceinline__ float weights(uint32_t tS, const float *ks, float f, 
     return (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
 }
 
+// Joins the parts that the CTAs [first, last] left of unit u's rows, by the eight warps of
+// the weights.
+template <int DIM, int FMT>
+__device__ __noinline__ void join_unit(const AttnParams &p, const Part &u)
+{
+    constexpr int N = DIM / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n_rows = min(kRows, u.q.n_new * p.group - u.r * kRows);
+    for (int row = warp; row < n_rows; row += 8) {
+        float acc[N], m, l;
+        auto at = [&](int i) { return int64_t((u.first + i) * 2 + (i == 0)) * kRows + row; };
+        join<DIM>(u.last - u.first + 1, [&](int i, float *v) { load_vec<N>(v, p.part.cta_o + at(i) * DIM + lane * N); },
+                  [&](int i) { return __ldcg(&p.part.cta_ml[at(i)]); }, acc, m, l);
+        finish_row<kRows, DIM, FMT>(p, u, row, acc, l);
+    }
+}
+
 template <int DIM, int FMT>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__ AttnParams p)
 {
@@ -365,10 +351,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     const uint32_t raw = smem_u32(smem_raw), sm = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (sm - raw);
     __shared__ int64_t sums[kThreads / 32];
-    __shared__ Cursor found[1];
-    __shared__ Walk<Cut> walks[kThreads / 32];             // each warp's, out of its registers
+    __shared__ Cursor cursor;                              // warp 13's
+    __shared__ Part parts[kParts];
     __shared__ uint32_t poison[kScaleSlots * 4];           // per slot: keys whose value's scale is not finite
-    __shared__ Cursor units[4];                            // the load warps' unit whose queries come next
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_flag, last_flag;
     volatile int *dead = &dead_flag;
@@ -388,6 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             mbar_init(bar(kWReady + i), 4);        // the warps of one row tile
             mbar_init(bar(kPvDone + i), 1);
         }
+        for (int i = 0; i < kParts; ++i) {
+            mbar_init(bar(kPartFull + i), 1);
+            mbar_init(bar(kPartEmpty + i), 13);    // every warp that reads the parts
+        }
+        mbar_init(bar(kJoin), 8);
         fence_mbar_init();
         dead_flag = 0;
     }
@@ -402,10 +392,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     grid_dep_launch();
 
     int64_t piece, total;
-    Cut::template find<kThreads, 1>(p, sums, found, piece, total);
-    const int64_t x0 = piece * blockIdx.x, x1 = min(x0 + piece, total);
-    const bool any = x0 < x1;
-    bool ok = true;
+    Cut::template find<kThreads, 1>(p, sums, &cursor, piece, total);
+
+    // The parts in order, for the warps that read them: `part()` waits for the next and is null
+    // past the last (or when the block has given up); `part_done()` lets go of it.
+    uint32_t part_no = 0;
+    auto part = [&]() -> const Part * {
+        const bool there = await(bar(kPartFull + part_no % kParts), part_no / kParts & 1, dead, p.status, kDevTimeoutPipe);
+        const Part *q = &parts[part_no % kParts];
+        return there && q->more ? q : nullptr;
+    };
+    auto part_done = [&]() {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bar(kPartEmpty + part_no % kParts));
+        ++part_no;
+    };
 
     if (warp < 8) {
         // ------------------------------------------------------------ weights
@@ -414,24 +416,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + T * 128u, tO = tmem + lanes + 256u + T * uint32_t(DIM);
         const float sl = p.scale * 1.4426950408889634f;
-        uint32_t n_s = 0;                                  // S tiles taken so far
+        uint32_t n_s = 0, n_join = 0;                      // S tiles taken so far, joins
         int tile_no = 0;                                   // key tiles of the CTA so far
-        Walk<Cut> &w = walks[warp];
-        const Cursor &u = w.u;
-        if (lane == 0) {
-            w.more = any;
-            if (any)
-                w.start(p, found[0], x0, x1);
-        }
-        __syncwarp();
-        while (w.more) {
-            const int t0 = w.t0, t1 = w.t1;
-            const Side sd = side_of(p, u, T);
-            const Active act = active(p, u, sd);
-            const int n_sink = u.span.n_sink, lo = u.span.lo, sink_end = u.span.sink;
+        bool alive = true;
+        auto wait = [&](uint32_t b, uint32_t parity) {
+            alive = __all_sync(0xffffffffu, alive && await(bar(b), parity, dead, p.status, kDevTimeoutMma));
+            tc::fence_after_sync();
+            return alive;
+        };
+        auto meet = [&]() {                                // the eight warps of the weights
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(kJoin));
+            return wait(kJoin, n_join++ & 1);
+        };
+        while (alive) {
+            const Part *pt = part();
+            if (!__all_sync(0xffffffffu, pt != nullptr))
+                break;
+            const int t0 = pt->t0, t1 = pt->t1, n_sink = pt->n_sink, lo = pt->lo, sink_end = pt->sink;
+            const Side sd = pt->side[T];
+            const Active act = pt->act[T];
+            const bool on = row < sd.rows;
             int pos = -1;
-            if (row < sd.rows)
-                pos = u.q.len - u.q.n_new + (u.r * kRows + T * kM + row) / p.group;
+            if (on)
+                pos = pt->q.len - pt->q.n_new + (pt->r * kRows + T * kM + row) / p.group;
             float ref = -INFINITY, l = 0.f;
             bool begun = false;
 #pragma unroll 1
@@ -443,15 +452,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 const bool masked = j0 + kKeys - 1 > sd.p_first || (sink && j0 + kKeys > sink_end) ||
                                     (p.window && !sink && j0 <= sd.p_last - p.window);
                 const float *ks = reinterpret_cast<const float *>(smem + S::SCALES) + (tile_no % kScaleSlots) * 2 * kKeys;
-                ok = __all_sync(0xffffffffu, await(bar(kSFull + T), n_s & 1, dead, p.status, kDevTimeoutMma)) && ok;
-                if (!ok)
-                    continue;
-                tc::fence_after_sync();
+                if (!wait(kSFull + T, n_s & 1))
+                    break;
                 const uint32_t *odd = poison + (tile_no % kScaleSlots) * 4;
                 const bool rework = masked || (FMT == kKvBf16 ? sl <= 0.f : (odd[0] | odd[1] | odd[2] | odd[3]) != 0);
                 if (rework) {
                     // the few tiles at an edge of what the rows see: scores scaled and hidden
-                    // in place, so that the pass below has one form
+                    // in place, so that the passes below have one form
                     const int hi = (sink ? min(pos, sink_end - 1) : pos) - j0;     // last key seen
                     const int behind = p.window && !sink ? pos - p.window - j0 : -1;
                     const int kept = p.sinks - j0;
@@ -489,16 +496,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         ref = top;
                     l *= a;
                     if (begun) {                           // the products so far, at rest
-                        ok = __all_sync(0xffffffffu, await(bar(kPvDone + T), (n_s - 1) & 1, dead, p.status, kDevTimeoutMma)) && ok;
-                        tc::fence_after_sync();
+                        if (!wait(kPvDone + T, (n_s - 1) & 1))
+                            break;
 #pragma unroll 1
-                        for (int i = 0; i < DIM / 16 && ok; ++i) {
+                        for (int i = 0; i < DIM; i += 16) {
                             uint32_t v[16];
-                            tmem_ld16_raw(tO + 16 * i, v);
+                            tmem_ld16_raw(tO + i, v);
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
                                 v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
-                            tmem_st16(tO + 16 * i, v);
+                            tmem_st16(tO + i, v);
                         }
                     }
                 }
@@ -513,152 +520,110 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 ++n_s;
             }
             // the part's end
-            if (begun) {
-                ok = __all_sync(0xffffffffu, await(bar(kPvDone + T), (n_s - 1) & 1, dead, p.status, kDevTimeoutMma)) && ok;
-                tc::fence_after_sync();
-            }
-            const bool begins = t0 == 0, ends = t1 == u.span.n, on = row < sd.rows;
-            if (begins && ends) {
+            if (begun)
+                wait(kPvDone + T, (n_s - 1) & 1);
+            if (!alive)
+                break;
+            if (pt->begins && pt->ends) {
                 int64_t token, col;
-                row_place<kRows, DIM>(p, u, on ? T * kM + row : 0, token, col, pos);
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                row_place<kRows, DIM>(p, *pt, on ? T * kM + row : 0, token, col, pos);
+                const float inv = l == 0.f || !begun ? 0.f : 1.f / l;
                 bool fine = true;
                 uint16_t *dst = p.out + token * p.ldo + col;
-#pragma unroll
-                for (int i = 0; i < DIM / 32; ++i) {
-                    uint32_t v[32];
-                    if (begun && ok) {
-                        tc::tmem_ld32_nowait(tO + 32 * i, v);
-                        tc::tmem_wait_ld();
-                    }
-                    uint4 y[4];
+#pragma unroll 1
+                for (int i = 0; i < DIM; i += 16) {
+                    uint32_t v[16];
+                    tmem_ld16_raw(tO + i, v);
+                    uint4 y[2];
                     uint32_t *yw = reinterpret_cast<uint32_t *>(y);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float a = begun && l != 0.f ? __uint_as_float(v[e]) * inv : 0.f;
-                        const float b = begun && l != 0.f ? __uint_as_float(v[e + 1]) * inv : 0.f;
+                    for (int e = 0; e < 16; e += 2) {
+                        const float a = inv == 0.f ? 0.f : __uint_as_float(v[e]) * inv;
+                        const float b = inv == 0.f ? 0.f : __uint_as_float(v[e + 1]) * inv;
                         fine = fine && fabsf(a) < INFINITY && fabsf(b) < INFINITY;
                         yw[e / 2] = pack2(a, b);
                     }
-                    if (on && ok)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            *reinterpret_cast<uint4 *>(dst + 32 * i + 8 * e) = y[e];
+                    if (on) {
+                        *reinterpret_cast<uint4 *>(dst + i) = y[0];
+                        *reinterpret_cast<uint4 *>(dst + i + 8) = y[1];
+                    }
                 }
-                unsigned bad = __ballot_sync(0xffffffffu, on && ok && !fine);
+                // a sum of weights that overflowed gives zeros above; it is not finite either
+                unsigned bad = __ballot_sync(0xffffffffu, on && !(fine && l < INFINITY));
                 while (bad) {                              // rows to be done on their own
                     const int src = __ffs(bad) - 1;
                     bad &= bad - 1;
                     float o[N] = {};
-                    finish_row<kRows, DIM, FMT>(p, u, T * kM + (warp & 3) * 32 + src, o, __int_as_float(0x7fffffff));
+                    finish_row<kRows, DIM, FMT>(p, *pt, T * kM + (warp & 3) * 32 + src, o, __int_as_float(0x7fffffff));
                 }
             } else {
-                const int64_t at = ((int64_t(blockIdx.x) * 2 + begins) * kRows + T * kM + row);
+                const int64_t at = (int64_t(blockIdx.x) * 2 + pt->begins) * kRows + T * kM + row;
                 if (on)
                     p.part.cta_ml[at] = make_float2(ref, l);
-#pragma unroll
-                for (int i = 0; i < DIM / 32; ++i) {
-                    uint32_t v[32];
-                    if (begun && ok) {
-                        tc::tmem_ld32_nowait(tO + 32 * i, v);
-                        tc::tmem_wait_ld();
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            v[e] = 0;
-                    }
+#pragma unroll 1
+                for (int i = 0; i < DIM; i += 16) {
+                    uint32_t v[16];
+                    tmem_ld16_raw(tO + i, v);
                     if (on)
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4 *>(p.part.cta_o + at * DIM + 32 * i + e) =
-                                make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<uint4 *>(p.part.cta_o + at * DIM + i + e) =
+                                begun ? make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]) : make_uint4(0, 0, 0, 0);
                 }
-                const int64_t first = (u.at + kUnitCost) / piece, final_ = (u.at + kUnitCost + u.span.n - 1) / piece;
                 __threadfence();
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                if (tid == 0) {
-                    last_flag = atomicAdd(&p.part.arrived[first], 1) == int(final_ - first);
+                if (!meet())
+                    break;
+                if (warp == 0 && lane == 0) {
+                    last_flag = atomicAdd(&p.part.arrived[pt->first], 1) == pt->last - pt->first;
                     if (last_flag)
-                        p.part.arrived[first] = 0;
+                        p.part.arrived[pt->first] = 0;
                 }
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (!meet())
+                    break;
                 if (last_flag) {
                     __threadfence();
-                    const int n_rows = min(kRows, u.q.n_new * p.group - u.r * kRows);
-                    for (int rr = warp; rr < n_rows; rr += 8) {
-                        float acc[N], m, ll;
-                        auto where = [&](int i) { return ((first + i) * 2 + (i == 0)) * kRows + rr; };
-                        join<DIM>(int(final_ - first) + 1,
-                                  [&](int i, float *v) { load_vec<N>(v, p.part.cta_o + where(i) * DIM + lane * N); },
-                                  [&](int i) { return __ldcg(&p.part.cta_ml[where(i)]); }, acc, m, ll);
-                        if (ok)
-                            finish_row<kRows, DIM, FMT>(p, u, rr, acc, ll);
-                    }
+                    join_unit<DIM, FMT>(p, *pt);
                 }
-                asm volatile("bar.sync 1, 256;" ::: "memory");   // last_flag is free again
+                if (!meet())                               // last_flag is free again
+                    break;
             }
             tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                w.t = t1 - 1;
-                w.step(p);
-            }
-            __syncwarp();
+            part_done();
         }
     } else if (warp < 12) {
         // ------------------------------------------------------------ loads
         setmaxnreg_dec<Regs<FMT>::load>();
         const int lw = warp - 8;                           // this warp's 32 keys (or rows) of a tile
-        Walk<Cut> &w = walks[warp];
-        if (lane == 0) {
-            w.more = any;
-            if (any)
-                w.start(p, found[0], x0, x1);
-        }
-        __syncwarp();
-        Cursor &unit = units[lw];
-        // this warp's tile: its unit's table row, pools at its head, and the keys
-        const int32_t *table = nullptr;
-        const uint8_t *kp = nullptr, *vp = nullptr;
-        int64_t s_head = 0;
-        int t = 0, t1 = 0, n_sink = 0, lo = 0, hi = 0, sink_end = 0;
-        bool more = false, fresh = false;
-        auto enter = [&]() {
-            more = w.more;
-            if (!more)
-                return;
-            const Cursor &u = w.u;
-            table = p.b.pages + int64_t(u.s) * p.b.ld_pages;
-            kp = kv.k + u.h * kv.head_stride;
-            vp = kv.v + u.h * kv.head_stride;
-            s_head = u.h * kv.s_head;
-            t = w.t0, t1 = w.t1, n_sink = u.span.n_sink, lo = u.span.lo, hi = u.span.hi, sink_end = u.span.sink;
-            fresh = true;
-        };
-        auto step = [&]() {
-            fresh = false;
-            if (++t < t1)
-                return;
-            __syncwarp();
-            if (lane == 0) {
-                w.t = t1 - 1;
-                w.step(p);
-            }
-            __syncwarp();
-            enter();
-        };
+        bool alive = true;
         uint32_t entry = 0, slot = 0, phase = 1;           // ring entries: keys 2j, values 2j + 1
-        int part = 0, tile_no = 0;
+        int tile_no = 0;
         uint32_t pending = 0;                              // barrier of the copies under way
-
-        auto key_of = [&](int &j) -> bool {                // this lane's key of the tile
-            const bool sink = t < n_sink;
-            j = (sink ? t * kKeys : lo + (t - n_sink) * kKeys) + lw * 32 + lane;
-            return j < (sink ? sink_end : hi);
+        auto wait = [&](uint32_t b, uint32_t parity) {
+            alive = __all_sync(0xffffffffu, alive && await(bar(b), parity, dead, p.status, kDevTimeoutPipe));
+            return alive;
         };
-        auto page_id = [&]() -> int {
-            int j;
-            return more && key_of(j) ? table[page_of(kv, j)] : INT_MIN;
+        auto wait_slot = [&]() { return entry < uint32_t(ST) || wait(kEmpty + slot, phase); };
+        auto advance = [&]() {
+            ++entry;
+            if (++slot == uint32_t(ST))
+                slot = 0, phase ^= 1;
+        };
+        // The part in hand, by what a lane needs of it: its key of tile t is key0 + (t - t0) *
+        // kKeys (a part's first tokens and its window are runs of their own).
+        const Part *pt = nullptr;
+        int t = 0;
+        auto enter = [&]() {
+            pt = part();
+            if (!__all_sync(0xffffffffu, pt != nullptr))
+                pt = nullptr;
+            t = pt ? pt->t0 : 0;
+        };
+        auto page_id = [&]() -> int {                      // INT_MIN: no key
+            if (!pt)
+                return INT_MIN;
+            const bool sink = t < pt->n_sink;
+            const int j = (sink ? t * kKeys : pt->lo + (t - pt->n_sink) * kKeys) + lw * 32 + lane;
+            return j < (sink ? pt->sink : pt->hi) ? p.b.pages[int64_t(pt->s) * p.b.ld_pages + page_of(kv, j)] : INT_MIN;
         };
         auto place = [&](int page, int64_t &at, int64_t &s_at) {
             at = -1;
@@ -669,11 +634,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 raise_status(p.status, kDevBadPage);
                 return;
             }
-            int j;
-            key_of(j);
+            const int j = (t < pt->n_sink ? t * kKeys : pt->lo + (t - pt->n_sink) * kKeys) + lw * 32 + lane;
             const int cell = j - page_of(kv, j) * kv.page_size;
-            at = page * kv.page_stride + cell * kv.cell_stride;
-            s_at = page * kv.s_page + cell * kv.s_cell + s_head;
+            at = page * kv.page_stride + cell * kv.cell_stride + pt->h * kv.head_stride;
+            s_at = page * kv.s_page + cell * kv.s_cell + pt->h * kv.s_head;
+        };
+        auto q_place = [&](int T) -> int64_t {             // this lane's row of the queries, bytes
+            const int row = T * kM + lw * 32 + lane;
+            if (pt->r * kRows + row >= pt->q.n_new * p.group)
+                return -1;
+            int64_t token, col;
+            int pos;
+            row_place<kRows, DIM>(p, *pt, row, token, col, pos);
+            return (token * p.ldq + col) * 2;
         };
         // The copies before the last commit are in shared memory: hand them over.
         auto settle = [&](bool all) {
@@ -685,16 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             __syncwarp();
             if (pending && lane == 0)
                 mbar_arrive(pending);
-        };
-        auto wait_empty = [&]() {
-            if (entry >= uint32_t(ST))
-                ok = await(bar(kEmpty + slot), phase, dead, p.status, kDevTimeoutPipe) && ok;
-            ok = __all_sync(0xffffffffu, ok);
-        };
-        auto advance = [&]() {
-            ++entry;
-            if (++slot == uint32_t(ST))
-                slot = 0, phase ^= 1;
+            pending = 0;
         };
         constexpr int CH = DIM / 8, RPI = 32 / CH;         // 16-byte chunks of a bf16 row, rows an instruction
         auto copy_rows = [&](uint32_t dst, const uint8_t *src, int64_t at) {
@@ -704,53 +668,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 const int64_t a = __shfl_sync(0xffffffffu, (long long)at, rr);
                 tc::cp_async16(dst + (ch / 8) * S::HALF + tc::sw128(row, ch % 8), src + (a < 0 ? 0 : a + ch * 16), a < 0 ? 0u : 16u);
             }
+            tc::cp_async_commit();
         };
-        auto load_q = [&](const Cursor &u) {
-            for (int T = 0; T < 2; ++T) {
-                if (part > 0)
-                    ok = await(bar(kQEmpty + T), (part - 1) & 1, dead, p.status, kDevTimeoutPipe) && ok;
-                ok = __all_sync(0xffffffffu, ok);
-                const int row = T * kM + lw * 32 + lane;
-                int64_t at = -1;
-                if (u.r * kRows + row < u.q.n_new * p.group) {
-                    int64_t token, col;
-                    int pos;
-                    row_place<kRows, DIM>(p, u, row, token, col, pos);
-                    at = (token * p.ldq + col) * 2;
-                }
-                if (ok)
-                    copy_rows(sm + T * S::TILE, reinterpret_cast<const uint8_t *>(p.q), at);
-                tc::cp_async_commit();
-                settle(false);
-                pending = bar(kQFull + T);
-            }
-            ++part;
-        };
-
         enter();
         int page = page_id();
-        int64_t at, s_at;
+        int64_t at = -1, s_at = 0;
         if (FMT == kKvBf16) {
-            while (more) {
+            // per tile: keys, then the queries of a new part, then values
+            while (pt && alive) {
                 place(page, at, s_at);
-                const uint8_t *src[2] = {kp, vp};
-                const bool queries = fresh;
-                if (fresh && lane == 0)
-                    unit = w.u;
-                __syncwarp();
-                step();
+                const bool fresh = t == pt->t0;
+                const uint32_t no = part_no;
+                const int64_t qa = fresh ? q_place(0) : -1, qb = fresh ? q_place(1) : -1;
+                if (++t == pt->t1) {
+                    part_done();
+                    enter();
+                }
                 page = page_id();                          // on its way during this tile
-#pragma unroll
-                for (int side = 0; side < 2; ++side) {
-                    wait_empty();
-                    if (ok)
-                        copy_rows(sm + S::RING + slot * S::TILE, src[side], at);
-                    tc::cp_async_commit();
+#pragma unroll 1
+                for (int job = 0; job < 4; ++job) {
+                    const bool ring = job == 0 || job == 3;
+                    if (!ring && !fresh)
+                        continue;
+                    if (!(ring ? wait_slot() : no == 0 || wait(kQEmpty + job - 1, (no - 1) & 1)))
+                        break;
+                    copy_rows(ring ? sm + S::RING + slot * S::TILE : sm + (job - 1) * S::TILE,
+                              job == 0 ? kv.k : job == 3 ? kv.v : reinterpret_cast<const uint8_t *>(p.q),
+                              ring ? at : job == 1 ? qa : qb);
                     settle(false);
-                    pending = bar(kFull + slot);
-                    advance();
-                    if (side == 0 && queries)
-                        load_q(unit);
+                    pending = ring ? bar(kFull + slot) : bar(kQFull + job - 1);
+                    if (ring)
+                        advance();
                 }
             }
             settle(true);
@@ -763,202 +711,213 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     x[i] = a < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(src + a + (lane % C8) * 16);
                 }
             };
-            auto store = [&](uint32_t dst, const uint4 x[C8]) {
+            auto store = [&](const uint4 x[C8]) {          // into the ring's next slot
 #pragma unroll
                 for (int i = 0; i < C8; ++i) {
                     const int row = lw * 32 + i * R8 + lane / C8, ch = 2 * (lane % C8);
                     const uint2 a = widen4<FMT>(x[i].x), b = widen4<FMT>(x[i].y), c = widen4<FMT>(x[i].z), d = widen4<FMT>(x[i].w);
-                    uint8_t *base = smem + (dst - sm) + (ch / 8) * S::HALF;
+                    uint8_t *base = smem + S::RING + slot * S::TILE + (ch / 8) * S::HALF;
                     *reinterpret_cast<uint4 *>(base + tc::sw128(row, ch % 8)) = make_uint4(a.x, a.y, b.x, b.y);
                     *reinterpret_cast<uint4 *>(base + tc::sw128(row, ch % 8 + 1)) = make_uint4(c.x, c.y, d.x, d.y);
                 }
-            };
-            auto hand_over = [&](uint32_t b) {
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(b);
+                    mbar_arrive(bar(kFull + slot));
+                advance();
             };
             const float sl = p.scale * 1.4426950408889634f;
-            uint4 kx[C8], vx[C8];
+            // x holds the tile that is stored next, y the one after it on its way
+            uint4 x[C8], y[C8];
             float ks = 0.f, vs = 0.f;
-            auto scales = [&]() {
+            auto begin = [&]() {
+                place(page, at, s_at);
+                fetch(x, kv.k, at);
                 ks = at < 0 ? 0.f : kv.k_scale[s_at] * sl;
                 vs = at < 0 ? 0.f : kv.v_scale[s_at];
             };
-            if (more) {
-                place(page, at, s_at);
-                fetch(kx, kp, at);
-                scales();
-            }
-            while (more) {
-                const bool queries = fresh;
-                fetch(vx, vp, at);
-                if (fresh && lane == 0)
-                    unit = w.u;
-                __syncwarp();
-                step();
-                page = page_id();
-                wait_empty();
-                if (ok) {
-                    store(sm + S::RING + slot * S::TILE, kx);
-                    float *sc = reinterpret_cast<float *>(smem + S::SCALES) + (tile_no % kScaleSlots) * 2 * kKeys + lw * 32 + lane;
-                    const bool fine = fabsf(vs) < INFINITY;
-                    sc[0] = ks;
-                    sc[kKeys] = fine ? vs : 0.f;
-                    const unsigned bad = __ballot_sync(0xffffffffu, !fine);
-                    if (lane == 0)
-                        poison[(tile_no % kScaleSlots) * 4 + lw] = bad;
+            if (pt)
+                begin();
+            while (pt && alive) {
+                const bool fresh = t == pt->t0;
+                const uint32_t no = part_no;
+                fetch(y, kv.v, at);
+                const int64_t qa = fresh ? q_place(0) : -1, qb = fresh ? q_place(1) : -1;
+                if (++t == pt->t1) {
+                    part_done();
+                    enter();
                 }
-                hand_over(bar(kFull + slot));
-                advance();
-                if (queries) {
-                    pending = 0;
-                    load_q(unit);
+                page = page_id();
+                if (!wait_slot())
+                    break;
+                float *sc = reinterpret_cast<float *>(smem + S::SCALES) + (tile_no % kScaleSlots) * 2 * kKeys + lw * 32 + lane;
+                const bool fine = fabsf(vs) < INFINITY;
+                sc[0] = ks;
+                sc[kKeys] = fine ? vs : 0.f;
+                const unsigned bad = __ballot_sync(0xffffffffu, !fine);
+                if (lane == 0)
+                    poison[(tile_no % kScaleSlots) * 4 + lw] = bad;
+                store(x);
+                if (fresh) {
+#pragma unroll 1
+                    for (int T = 0; T < 2; ++T) {
+                        if (no > 0 && !wait(kQEmpty + T, (no - 1) & 1))
+                            break;
+                        copy_rows(sm + T * S::TILE, reinterpret_cast<const uint8_t *>(p.q), T ? qb : qa);
+                        settle(false);
+                        pending = bar(kQFull + T);
+                    }
                     settle(true);
                 }
-                if (more) {
-                    place(page, at, s_at);
-                    fetch(kx, kp, at);
-                    scales();
-                }
-                wait_empty();
-                if (ok)
-                    store(sm + S::RING + slot * S::TILE, vx);
-                hand_over(bar(kFull + slot));
-                advance();
+                if (pt)
+                    begin();
+                if (!wait_slot())
+                    break;
+                store(y);
                 ++tile_no;
             }
         }
-    } else {
+    } else if (warp == 12) {
         // ------------------------------------------------------------ products
         setmaxnreg_dec<Regs<FMT>::few>();
-        if (warp == 12 && lane == 0 && any) {
+        if (lane == 0) {
             constexpr uint32_t iqk = tc::idesc_bf16(kM, kKeys, 0, 0), ipv = tc::idesc_bf16(kM, DIM, 0, 1);
             const uint64_t q_desc = tc::smem_desc_sw128(sm, 16u, 1024u), k_desc = tc::smem_desc_sw128(sm + S::RING, 16u, 1024u),
                            v_desc = tc::smem_desc_sw128(sm + S::RING, S::HALF, 1024u);
             constexpr uint32_t kTile16 = S::TILE / 16, kHalf16 = S::HALF / 16;   // descriptor units
-            Walk<Cut> &w = walks[warp];
-            w.start(p, found[0], x0, x1);
             // ring slots of the keys and values in turn: keys 2j, values 2j + 1
             uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0;
-            uint32_t w_phase = 0, started = 0;             // a bit for each row tile
+            uint32_t w_phase = 0;                          // a bit for each row tile
             auto next_slot = [&](uint32_t &slot, uint32_t &phase) {
                 slot += 2;
                 if (slot >= uint32_t(ST))
                     slot -= ST, phase ^= 1;
             };
-            int part = 0;
-            // One step for one row tile: O += W V of the tile in v_slot, or S of the tile in
-            // k_slot.  One copy of the code for both and short loops (see the passes above).
-            auto product = [&](bool values, int T) {
-                const uint32_t slot = values ? v_slot : k_slot, phase = values ? v_phase : k_phase;
-                ok = ok && await(bar(kFull + slot), phase, dead, p.status, kDevTimeoutLoad);
-                const uint32_t other = values ? bar(kWReady + T) : bar(kQFull + T), parity = values ? w_phase >> T & 1 : part & 1;
-                ok = ok && await(other, parity, dead, p.status, kDevTimeoutPipe);
-                if (!ok)
-                    return;
-                tc::fence_after_sync();
-                if (values) {
-                    uint64_t v = v_desc + slot * kTile16;
-                    uint32_t a = tmem + T * 128u, acc = started >> T & 1;
-                    const uint32_t d = tmem + 256u + T * uint32_t(DIM);
-#pragma unroll 2
-                    for (int i = 0; i < kKeys / 16; ++i) {
-                        mma_tmem_a(d, a, v, ipv, acc);
-                        a += 8;
-                        v += 128;
-                        acc = 1;
-                    }
-                } else {
-                    uint64_t q = q_desc + T * kTile16, k = k_desc + slot * kTile16;
-                    uint32_t acc = 0;
-#pragma unroll 1
-                    for (int h = 0; h < DIM / 64; ++h) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            tc::mma_bf16(tmem + T * 128u, q + 2 * i, k + 2 * i, iqk, acc);
-                            acc = 1;
-                        }
-                        q += kHalf16;
-                        k += kHalf16;
-                    }
-                }
-                tc::mma_commit(values ? bar(kPvDone + T) : bar(kSFull + T));
+            bool alive = true;
+            auto wait = [&](uint32_t b, uint32_t parity) {
+                alive = alive && await(bar(b), parity, dead, p.status, kDevTimeoutPipe);
+                return alive;
             };
-            // this part's tiles: which of them are A's and B's, and the last
-            Active act_a, act_b;
-            int t = 0, t1 = 0;
-            auto enter = [&]() {
-                act_a = active(p, w.u, side_of(p, w.u, 0));
-                act_b = active(p, w.u, side_of(p, w.u, 1));
-                t = w.t0;
-                t1 = w.t1;
-            };
-            // The order of the steps: the values of tile i for A, the scores of tile i + 1 for
-            // A, then the same for B; at the end of a unit the values for both come first, as
-            // the next one's queries may still be on their way.
-            bool more = w.more, have = false;              // have: tile t's scores are out
-            if (more)
-                enter();
-            while (more) {
-                const bool turn = have && t + 1 == t1;     // the last tile of its part
-                const bool now_a = have && act_a(t), now_b = have && act_b(t);
+            while (alive) {
+                const Part *pt = part();
+                if (!pt)
+                    break;
+                const Active act_a = pt->act[0], act_b = pt->act[1];
+                const int t0 = pt->t0, t1 = pt->t1;
+                mbar_arrive(bar(kPartEmpty + part_no % kParts));
+                uint32_t started = 0;
+                // Round t: the values of tile t - 1 and the scores of tile t, for A, then for B.
 #pragma unroll 1
-                for (int step = 0; step < 4; ++step) {
-                    const bool values = turn ? step < 2 : (step & 1) == 0;
-                    const int T = turn ? step & 1 : step >> 1;
-                    if (step == 2 && turn) {
-                        started = 0;
-                        ++part;
-                        w.t = t1 - 1;
-                        w.step(p);
-                        more = w.more;
-                        if (more)
-                            enter();
-                    }
-                    if (values) {
-                        if (T ? now_b : now_a) {
-                            product(true, T);
+                for (int t = t0; t <= t1 && alive; ++t) {
+                    const bool with_v = t > t0, with_s = t < t1;
+                    if (with_v && !wait(kFull + v_slot, v_phase))
+                        break;
+#pragma unroll 1
+                    for (int T = 0; T < 2; ++T) {
+                        const Active act{T ? act_b.from : act_a.from, T ? act_b.to : act_a.to, T ? act_b.behind : act_a.behind};
+                        if (with_v && act(t - 1)) {
+                            if (!wait(kWReady + T, w_phase >> T & 1))
+                                break;
                             w_phase ^= 1u << T;
+                            tc::fence_after_sync();
+                            const uint64_t v = v_desc + v_slot * kTile16;
+                            const uint32_t a = tmem + T * 128u, d = tmem + 256u + T * uint32_t(DIM);
+                            mma_tmem_a(d, a, v, ipv, started >> T & 1);
+#pragma unroll
+                            for (int i = 1; i < kKeys / 16; ++i)
+                                mma_tmem_a(d, a + 8 * i, v + 128 * i, ipv, 1);
+                            tc::mma_commit(bar(kPvDone + T));
                             started |= 1u << T;
                         }
-                        if (T == 1 && have && ok)
+                        if (with_v && T == 1)
                             tc::mma_commit(bar(kEmpty + v_slot));
-                    } else if (more) {
-                        const int i = turn || !have ? t : t + 1;
-                        if (T ? act_b(i) : act_a(i))
-                            product(false, T);
-                        if (ok && i + 1 == t1)
-                            tc::mma_commit(bar(kQEmpty + T));
-                        if (ok && T == 1)
-                            tc::mma_commit(bar(kEmpty + k_slot));
+                        if (with_s) {
+                            if (T == 0 && !wait(kFull + k_slot, k_phase))
+                                break;
+                            if (t == t0 && !wait(kQFull + T, part_no & 1))
+                                break;
+                            if (act(t)) {
+                                tc::fence_after_sync();
+                                const uint64_t q = q_desc + T * kTile16, k = k_desc + k_slot * kTile16;
+                                const uint32_t d = tmem + T * 128u;
+#pragma unroll
+                                for (int i = 0; i < DIM / 16; ++i)
+                                    tc::mma_bf16(d, q + (i / 4) * kHalf16 + 2 * (i % 4), k + (i / 4) * kHalf16 + 2 * (i % 4), iqk, i > 0);
+                                tc::mma_commit(bar(kSFull + T));
+                            }
+                            if (t + 1 == t1)
+                                tc::mma_commit(bar(kQEmpty + T));
+                            if (T == 1)
+                                tc::mma_commit(bar(kEmpty + k_slot));
+                        }
                     }
+                    if (with_v)
+                        next_slot(v_slot, v_phase);
+                    if (with_s)
+                        next_slot(k_slot, k_phase);
                 }
-                if (have) {
-                    next_slot(v_slot, v_phase);
-                    if (!turn)
-                        ++t;
-                }
-                next_slot(k_slot, k_phase);
-                have = true;
+                ++part_no;
             }
         }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ parts
+        setmaxnreg_dec<Regs<FMT>::few>();
+        if (warp == 13 && lane == 0) {
+            int64_t x = piece * blockIdx.x;
+            const int64_t x1 = min(x + piece, total);
+            bool more = true;
+            while (more) {
+                int t0 = 0, t1 = 0;
+                while (x < x1) {                           // the next unit that has tiles here
+                    const int64_t first = cursor.at + kUnitCost, end = first + cursor.span.n;
+                    t0 = int(max(x - first, int64_t(0)));
+                    t1 = int(max(min(x1, end) - first, int64_t(0)));
+                    x = end;
+                    if (t1 > t0)
+                        break;
+                    if (x < x1)
+                        Cut::next(p, cursor);
+                }
+                more = t1 > t0;
+                const uint32_t slot = part_no % kParts;
+                if (part_no >= kParts &&
+                    !await(bar(kPartEmpty + slot), (part_no / kParts - 1) & 1, dead, p.status, kDevTimeoutPipe))
+                    break;
+                Part &q = parts[slot];
+                q.more = more;
+                if (more) {
+                    q.s = cursor.s, q.r = cursor.r, q.h = cursor.h, q.q = cursor.q;
+                    q.t0 = t0, q.t1 = t1;
+                    q.n_sink = cursor.span.n_sink, q.lo = cursor.span.lo, q.hi = cursor.span.hi, q.sink = cursor.span.sink;
+                    q.begins = t0 == 0;
+                    q.ends = t1 == cursor.span.n;
+                    q.first = int((cursor.at + kUnitCost) / piece);
+                    q.last = int((cursor.at + kUnitCost + cursor.span.n - 1) / piece);
+                    for (int T = 0; T < 2; ++T) {
+                        q.side[T] = side_of(p, cursor, T);
+                        q.act[T] = active(p, cursor, q.side[T]);
+                    }
+                }
+                mbar_arrive(bar(kPartFull + slot));
+                ++part_no;
+                if (more && x < x1)
+                    Cut::next(p, cursor);
+            }
+        }
+        __syncwarp();
     }
-    // Every product has ended: the weights' warps waited for each tile's last, and a role
-    // that gave up is waited for here.
+    // Every product has ended: the weights' warps waited for each tile's last.  Where the
+    // roles gave up, those under way get the time that they can take at most.
     tc::fence_before_sync();
     __syncthreads();
-    if (dead_flag && warp == 12) {
-        if (lane == 0) {
-            tc::mma_commit(bar(kSFull));
+    if (warp == 12) {
+        if (dead_flag) {
             const uint64_t t = globaltimer_ns();
             while (globaltimer_ns() - t < 1000000ull) {
             }
         }
         __syncwarp();
-    }
-    if (warp == 12) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, 512);
     }
