@@ -2,13 +2,13 @@
 // back as bf16 rows.
 //
 // One vector is the dim elements of one (row, head): dim / 8 lanes take 8 elements
-// (16 bytes of bf16) each.  A CTA serves one row: its warps find the row's sequence
-// and cell once, then go over the 2 * heads vectors (keys, then values).
+// (16 bytes of bf16) each.  A CTA serves up to eight rows: a warp finds each row's sequence
+// and cell, then all go over the rows' 2 * heads vectors (keys, then values).
 //
 // 8-bit formats, per vector: scale = max |x| / T (T = 127 for int8, 448 for e4m3; one
 // fp32 division, rounded to nearest), code = x / scale rounded to nearest even and
-// limited to +-T.  x / scale is a true division: the code is the nearest one, not one
-// off at a tie as with a rounded reciprocal.  A vector that holds an infinity or a
+// limited to +-T.  x / scale means the true quotient: the code is the nearest one, not one
+// off next to a tie as with a rounded reciprocal.  A vector that holds an infinity or a
 // NaN gets a NaN scale and zero codes, so it reads back as NaN; a zero vector gets
 // scale 0.
 //
@@ -16,6 +16,8 @@
 // launch plus three dependent loads (starts and lens, page id, data) for a decode batch.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "kv.h"
 #include "ptx.cuh"
@@ -27,6 +29,7 @@ namespace lora {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxRows = kThreads / 32;      // rows a CTA: a warp looks up each
 
 // Row `row`'s place in the cache, found by a whole warp: byte offset of the page's
 // cell in the pools (without the head) and element offset in the scales.
@@ -78,48 +81,55 @@ __device__ __forceinline__ Place find_row(const KvView &kv, const BatchView &b, 
     return pl;
 }
 
+// `rows` rows from the CTA's first: their vectors one after another, kPer at a time.
 template <int DIM, int FMT>
-__global__ void __launch_bounds__(kThreads) k_kv_write(const __grid_constant__ KvRowsParams p)
+__global__ void __launch_bounds__(kThreads) k_kv_write(const __grid_constant__ KvRowsParams p, int rows)
 {
     constexpr int kLanes = DIM / 8;                  // lanes per vector
     constexpr int kPer = kThreads / kLanes;          // vectors per pass of the CTA
     constexpr int kUnroll = 4;
-    const int row = blockIdx.x, sub = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
+    __shared__ Place places[kMaxRows];
+    const int row0 = blockIdx.x * rows, sub = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
+    const int warp = threadIdx.x >> 5;
     const KvView &kv = p.kv;
     grid_dep_wait();
     grid_dep_launch();
-    const int nvec = 2 * kv.heads;
-    // the row's vectors are on their way while its place is looked up
-    for (int v0 = blockIdx.y * kPer * kUnroll; v0 < nvec; v0 += gridDim.y * kPer * kUnroll) {
-        uint4 x[kUnroll];
+    const int nvec = 2 * kv.heads, all = min(rows, p.b.n_rows - row0) * nvec;
+    const int stride = gridDim.y * kPer * kUnroll;
+    uint4 x[kUnroll];
+    auto load = [&](int v0) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int vec = v0 + u * kPer + sub;
-            x[u] = uint4{0, 0, 0, 0};
-            if (vec < nvec) {
-                const bool is_v = vec >= kv.heads;
-                const uint16_t *src = is_v ? p.v + int64_t(row) * p.ldv : p.k + int64_t(row) * p.ldk;
-                x[u] = *reinterpret_cast<const uint4 *>(src + (is_v ? vec - kv.heads : vec) * DIM + l * 8);
-            }
-        }
-        const Place pl = find_row(kv, p.b, row, p.status);
-        if (!pl.stored)
-            return;
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int vec = v0 + u * kPer + sub;
-            const bool on = vec < nvec;
+            const int i = v0 + u * kPer + sub, row = row0 + i / nvec, vec = i % nvec;
             const bool is_v = vec >= kv.heads;
-            const int head = on ? (is_v ? vec - kv.heads : vec) : 0;
+            const uint16_t *src = is_v ? p.v + int64_t(row) * p.ldv : p.k + int64_t(row) * p.ldk;
+            x[u] = i < all ? *reinterpret_cast<const uint4 *>(src + (is_v ? vec - kv.heads : vec) * DIM + l * 8)
+                           : uint4{0, 0, 0, 0};
+        }
+    };
+    // the first vectors are on their way while the rows' places are looked up
+    int v0 = blockIdx.y * kPer * kUnroll;
+    load(v0);
+    if (warp < rows) {
+        const Place pl = row0 + warp < p.b.n_rows ? find_row(kv, p.b, row0 + warp, p.status) : Place{false, false, 0, 0};
+        if ((threadIdx.x & 31) == 0)
+            places[warp] = pl;
+    }
+    __syncthreads();
+    for (; v0 < all; v0 += stride) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = v0 + u * kPer + sub, vec = i % nvec;
+            const Place &pl = places[min(i / nvec, rows - 1)];
+            const bool on = i < all && pl.stored, is_v = vec >= kv.heads;
+            const int head = is_v ? vec - kv.heads : vec;
             uint8_t *dst = (is_v ? kv.v : kv.k) + pl.at + head * kv.head_stride;
             if (FMT == kKvBf16) {
                 if (on)
                     *reinterpret_cast<uint4 *>(dst + l * 16) = x[u];
             } else {
-                float f[8];
-                unpack8(x[u], f);
                 float scale;
-                const uint2 code = encode8<FMT, kLanes>(f, scale);
+                const uint2 code = encode8<FMT, kLanes>(x[u], scale);
                 if (on) {
                     *reinterpret_cast<uint2 *>(dst + l * 8) = code;
                     if (l == 0)
@@ -127,32 +137,40 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(const __grid_constant__ K
                 }
             }
         }
+        if (v0 + stride < all)
+            load(v0 + stride);
     }
 }
 
 template <int DIM, int FMT>
-__global__ void __launch_bounds__(kThreads) k_kv_read(const __grid_constant__ KvRowsParams p)
+__global__ void __launch_bounds__(kThreads) k_kv_read(const __grid_constant__ KvRowsParams p, int rows)
 {
     constexpr int kLanes = DIM / 8;
     constexpr int kPer = kThreads / kLanes;
     constexpr int kUnroll = 4;
-    const int row = blockIdx.x, sub = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
+    __shared__ Place places[kMaxRows];
+    const int row0 = blockIdx.x * rows, sub = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
+    const int warp = threadIdx.x >> 5;
     const KvView &kv = p.kv;
     grid_dep_wait();
     grid_dep_launch();
-    const int nvec = 2 * kv.heads;
-    const Place pl = find_row(kv, p.b, row, p.status);
-    if (!pl.live)
-        return;
-    for (int v0 = blockIdx.y * kPer * kUnroll; v0 < nvec; v0 += gridDim.y * kPer * kUnroll) {
+    const int nvec = 2 * kv.heads, all = min(rows, p.b.n_rows - row0) * nvec;
+    if (warp < rows) {
+        const Place pl = row0 + warp < p.b.n_rows ? find_row(kv, p.b, row0 + warp, p.status) : Place{false, false, 0, 0};
+        if ((threadIdx.x & 31) == 0)
+            places[warp] = pl;
+    }
+    __syncthreads();
+    for (int v0 = blockIdx.y * kPer * kUnroll; v0 < all; v0 += gridDim.y * kPer * kUnroll) {
         uint4 x[kUnroll];
         float scale[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int vec = v0 + u * kPer + sub;
+            const int i = v0 + u * kPer + sub, vec = i % nvec;
+            const Place &pl = places[min(i / nvec, rows - 1)];
             x[u] = uint4{0, 0, 0, 0};
             scale[u] = 0.f;
-            if (vec < nvec && pl.stored) {
+            if (i < all && pl.stored) {
                 const bool is_v = vec >= kv.heads;
                 const int head = is_v ? vec - kv.heads : vec;
                 const uint8_t *src = (is_v ? kv.v : kv.k) + pl.at + head * kv.head_stride;
@@ -168,8 +186,9 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const __grid_constant__ Kv
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int vec = v0 + u * kPer + sub;
-            if (vec >= nvec)
+            const int i = v0 + u * kPer + sub, row = row0 + i / nvec, vec = i % nvec;
+            const Place &pl = places[min(i / nvec, rows - 1)];
+            if (i >= all || !pl.live)
                 continue;
             const bool is_v = vec >= kv.heads;
             uint16_t *dst = is_v ? p.v + int64_t(row) * p.ldv : p.k + int64_t(row) * p.ldk;
@@ -190,12 +209,13 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const __grid_constant__ Kv
 template <typename F>
 cudaError_t launch(F kernel, const KvRowsParams &p, cudaStream_t stream)
 {
-    // one CTA per row; rows of many vectors are split when the batch alone would not
-    // fill the SMs
+    // As many rows a CTA as leave two CTAs for each SM (their look-ups then run side by
+    // side); a few rows of many vectors are cut instead, to spread over the SMs.
+    const int rows = int(std::min<int64_t>(kMaxRows, std::max<int64_t>(1, p.b.n_rows / 304)));
     const int per = kThreads / (p.kv.dim / 8) * 4;
-    const int parts = (2 * p.kv.heads + per - 1) / per;
+    const int parts = rows == 1 ? (2 * p.kv.heads + per - 1) / per : 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(p.b.n_rows), unsigned(p.b.n_rows < 1024 ? parts : 1));
+    cfg.gridDim = dim3(unsigned((p.b.n_rows + rows - 1) / rows), unsigned(parts));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
@@ -203,7 +223,7 @@ cudaError_t launch(F kernel, const KvRowsParams &p, cudaStream_t stream)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p, rows);
 }
 
 }  // namespace
