@@ -183,28 +183,6 @@ struct Part : Unit {
 };
 constexpr int kParts = 4;     // parts under way at once
 
-// Four codes (bytes 0..3) to bf16, in order.
-template <int FMT>
-__device__ __forceinline__ uint2 widen4(uint32_t r)
-{
-    uint2 y;
-    if (FMT == kKvInt8) {
-        // 128 + the low seven bits, less 128 or (sign bit) 256: exact in bf16
-        const uint32_t a = __byte_perm(r, 0, 0x4140), b = __byte_perm(r, 0, 0x4342);
-        const uint32_t a1 = (a & 0x007f007fu) | 0x43004300u, a0 = (a & 0x00800080u) | 0x43004300u;
-        const uint32_t b1 = (b & 0x007f007fu) | 0x43004300u, b0 = (b & 0x00800080u) | 0x43004300u;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y.x) : "r"(a1), "r"(a0));
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y.y) : "r"(b1), "r"(b0));
-    } else {
-        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(r & 0xffffu), __NV_E4M3);
-        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(r >> 16), __NV_E4M3);
-        const float2 fa = __half22float2(__half2(a)), fb = __half22float2(__half2(b));
-        y.x = pack2(fa.x, fa.y);
-        y.y = pack2(fb.x, fb.y);
-    }
-    return y;
-}
-
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
     uint64_t d;

@@ -1,8 +1,8 @@
 // Writing new keys and values into the pages of the cache, and reading cached ones
 // back as bf16 rows.
 //
-// One vector is the dim elements of one (row, head): dim / 8 lanes take 8 elements
-// (16 bytes of bf16) each.  A CTA serves up to eight rows: a warp finds each row's sequence
+// One vector is the dim elements of one (row, head): dim / 16 lanes take 16 elements
+// (32 bytes of bf16) each.  A CTA serves up to eight rows: a warp finds each row's sequence
 // and cell, then all go over the rows' 2 * heads vectors (keys, then values).
 //
 // 8-bit formats, per vector: scale = max |x| / T (T = 127 for int8, 448 for e4m3; one
@@ -85,9 +85,9 @@ __device__ __forceinline__ Place find_row(const KvView &kv, const BatchView &b, 
 template <int DIM, int FMT>
 __global__ void __launch_bounds__(kThreads) k_kv_write(const __grid_constant__ KvRowsParams p, int rows)
 {
-    constexpr int kLanes = DIM / 8;                  // lanes per vector
+    constexpr int kLanes = DIM / 16;                 // lanes per vector
     constexpr int kPer = kThreads / kLanes;          // vectors per pass of the CTA
-    constexpr int kUnroll = 4;
+    constexpr int kUnroll = 2;
     __shared__ Place places[kMaxRows];
     const int row0 = blockIdx.x * rows, sub = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
     const int warp = threadIdx.x >> 5;
@@ -96,15 +96,16 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(const __grid_constant__ K
     grid_dep_launch();
     const int nvec = 2 * kv.heads, all = min(rows, p.b.n_rows - row0) * nvec;
     const int stride = gridDim.y * kPer * kUnroll;
-    uint4 x[kUnroll];
+    uint4 x[kUnroll][2];
     auto load = [&](int v0) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int i = v0 + u * kPer + sub, row = row0 + i / nvec, vec = i % nvec;
+            const int i = v0 + u * kPer + sub, r = p.per_row.quotient(i), row = row0 + r, vec = i - r * nvec;
             const bool is_v = vec >= kv.heads;
-            const uint16_t *src = is_v ? p.v + int64_t(row) * p.ldv : p.k + int64_t(row) * p.ldk;
-            x[u] = i < all ? *reinterpret_cast<const uint4 *>(src + (is_v ? vec - kv.heads : vec) * DIM + l * 8)
-                           : uint4{0, 0, 0, 0};
+            const uint16_t *src = (is_v ? p.v + int64_t(row) * p.ldv - kv.heads * DIM : p.k + int64_t(row) * p.ldk) + vec * DIM + l * 16;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                x[u][e] = i < all ? reinterpret_cast<const uint4 *>(src)[e] : uint4{0, 0, 0, 0};
         }
     };
     // the first vectors are on their way while the rows' places are looked up
@@ -119,19 +120,21 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(const __grid_constant__ K
     for (; v0 < all; v0 += stride) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int i = v0 + u * kPer + sub, vec = i % nvec;
-            const Place &pl = places[min(i / nvec, rows - 1)];
+            const int i = v0 + u * kPer + sub, r = p.per_row.quotient(i), vec = i - r * nvec;
+            const Place &pl = places[min(r, rows - 1)];
             const bool on = i < all && pl.stored, is_v = vec >= kv.heads;
             const int head = is_v ? vec - kv.heads : vec;
             uint8_t *dst = (is_v ? kv.v : kv.k) + pl.at + head * kv.head_stride;
             if (FMT == kKvBf16) {
-                if (on)
-                    *reinterpret_cast<uint4 *>(dst + l * 16) = x[u];
+                if (on) {
+                    reinterpret_cast<uint4 *>(dst + l * 32)[0] = x[u][0];
+                    reinterpret_cast<uint4 *>(dst + l * 32)[1] = x[u][1];
+                }
             } else {
                 float scale;
-                const uint2 code = encode8<FMT, kLanes>(x[u], scale);
+                const uint4 code = encode16<FMT, kLanes>(x[u], scale);
                 if (on) {
-                    *reinterpret_cast<uint2 *>(dst + l * 8) = code;
+                    *reinterpret_cast<uint4 *>(dst + l * 16) = code;
                     if (l == 0)
                         (is_v ? kv.v_scale : kv.k_scale)[pl.s_at + head * kv.s_head] = scale;
                 }
@@ -145,9 +148,9 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(const __grid_constant__ K
 template <int DIM, int FMT>
 __global__ void __launch_bounds__(kThreads) k_kv_read(const __grid_constant__ KvRowsParams p, int rows)
 {
-    constexpr int kLanes = DIM / 8;
+    constexpr int kLanes = DIM / 16;
     constexpr int kPer = kThreads / kLanes;
-    constexpr int kUnroll = 4;
+    constexpr int kUnroll = 2;
     __shared__ Place places[kMaxRows];
     const int row0 = blockIdx.x * rows, sub = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
     const int warp = threadIdx.x >> 5;
@@ -162,57 +165,52 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const __grid_constant__ Kv
     }
     __syncthreads();
     for (int v0 = blockIdx.y * kPer * kUnroll; v0 < all; v0 += gridDim.y * kPer * kUnroll) {
-        uint4 x[kUnroll];
+        uint4 x[kUnroll][2];
         float scale[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int i = v0 + u * kPer + sub, vec = i % nvec;
-            const Place &pl = places[min(i / nvec, rows - 1)];
-            x[u] = uint4{0, 0, 0, 0};
+            const int i = v0 + u * kPer + sub, r = p.per_row.quotient(i), vec = i - r * nvec;
+            const Place &pl = places[min(r, rows - 1)];
+            x[u][0] = x[u][1] = uint4{0, 0, 0, 0};
             scale[u] = 0.f;
             if (i < all && pl.stored) {
                 const bool is_v = vec >= kv.heads;
                 const int head = is_v ? vec - kv.heads : vec;
                 const uint8_t *src = (is_v ? kv.v : kv.k) + pl.at + head * kv.head_stride;
                 if (FMT == kKvBf16) {
-                    x[u] = *reinterpret_cast<const uint4 *>(src + l * 16);
+                    x[u][0] = reinterpret_cast<const uint4 *>(src + l * 32)[0];
+                    x[u][1] = reinterpret_cast<const uint4 *>(src + l * 32)[1];
                 } else {
-                    const uint2 c = *reinterpret_cast<const uint2 *>(src + l * 8);
-                    x[u].x = c.x;
-                    x[u].y = c.y;
+                    x[u][0] = *reinterpret_cast<const uint4 *>(src + l * 16);
                     scale[u] = (is_v ? kv.v_scale : kv.k_scale)[pl.s_at + head * kv.s_head];
                 }
             }
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int i = v0 + u * kPer + sub, row = row0 + i / nvec, vec = i % nvec;
-            const Place &pl = places[min(i / nvec, rows - 1)];
+            const int i = v0 + u * kPer + sub, r = p.per_row.quotient(i), row = row0 + r, vec = i - r * nvec;
+            const Place &pl = places[min(r, rows - 1)];
             if (i >= all || !pl.live)
                 continue;
             const bool is_v = vec >= kv.heads;
-            uint16_t *dst = is_v ? p.v + int64_t(row) * p.ldv : p.k + int64_t(row) * p.ldk;
-            uint4 y = x[u];
-            if (FMT != kKvBf16 && pl.stored) {
-                float f[8];
-                decode8<FMT>(make_uint2(x[u].x, x[u].y), f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    f[e] *= scale[u];
-                y = pack8(f);
-            }
-            *reinterpret_cast<uint4 *>(dst + (is_v ? vec - kv.heads : vec) * DIM + l * 8) = y;
+            uint16_t *dst = (is_v ? p.v + int64_t(row) * p.ldv - kv.heads * DIM : p.k + int64_t(row) * p.ldk) + vec * DIM + l * 16;
+            uint4 y[2] = {x[u][0], x[u][1]};
+            if (FMT != kKvBf16)
+                decode16<FMT>(x[u][0], scale[u], y);       // no cell: zero codes, zero scale
+            reinterpret_cast<uint4 *>(dst)[0] = y[0];
+            reinterpret_cast<uint4 *>(dst)[1] = y[1];
         }
     }
 }
 
 template <typename F>
-cudaError_t launch(F kernel, const KvRowsParams &p, cudaStream_t stream)
+cudaError_t launch(F kernel, KvRowsParams p, cudaStream_t stream)
 {
     // As many rows a CTA as leave two CTAs for each SM (their look-ups then run side by
     // side); a few rows of many vectors are cut instead, to spread over the SMs.
     const int rows = int(std::min<int64_t>(kMaxRows, std::max<int64_t>(1, p.b.n_rows / 304)));
-    const int per = kThreads / (p.kv.dim / 8) * 4;
+    const int per = kThreads / (p.kv.dim / 16) * 2;
+    p.per_row = Divider(2 * p.kv.heads);
     const int parts = rows == 1 ? (2 * p.kv.heads + per - 1) / per : 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned((p.b.n_rows + rows - 1) / rows), unsigned(parts));

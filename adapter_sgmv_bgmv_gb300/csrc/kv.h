@@ -41,11 +41,22 @@ struct BatchView {
     int capacity;             // positions the page table has room for
 };
 
+// i / d by a product, for 0 <= i and i * d < 2^32.
+struct Divider {
+    uint32_t m = 0;
+    Divider() = default;
+    explicit Divider(int d) : m(d > 1 ? uint32_t(((uint64_t(1) << 32) + d - 1) / d) : 0) {}
+#ifdef __CUDACC__
+    __device__ __forceinline__ int quotient(int i) const { return int(m ? __umulhi(uint32_t(i), m) : uint32_t(i)); }
+#endif
+};
+
 struct KvRowsParams {
     KvView kv;
     BatchView b;
     uint16_t *k, *v;          // bf16 rows, read by the write and written by the read
     int64_t ldk, ldv;
+    Divider per_row;          // by a row's vectors
     unsigned *status;
 };
 cudaError_t launch_kv_write(const KvRowsParams &p, cudaStream_t stream);

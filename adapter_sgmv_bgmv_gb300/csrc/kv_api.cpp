@@ -109,7 +109,7 @@ int lora_kv_create(lora_ctx *ctx, const lora_kv_desc *d, lora_kv **out)
         return LORA_E_INVAL;
     if (d->head_dim != 64 && d->head_dim != 128)
         return LORA_E_UNSUPPORTED;
-    if (d->n_pages >= (int64_t(1) << 31) || d->page_size > (1 << 20) || d->n_heads > (1 << 16))
+    if (d->n_pages >= (int64_t(1) << 31) || d->page_size > (1 << 20) || d->n_heads > 4096)
         return LORA_E_CAPACITY;
     const int size = d->format == LORA_KV_BF16 ? 2 : 1;
     const int64_t strides[3] = {d->page_stride, d->cell_stride, d->head_stride};

@@ -478,7 +478,7 @@ typedef struct {
 
 /* Register a cache with a context.  The first one of a context allocates its attention
  * scratch; no later call allocates.  LORA_E_UNSUPPORTED: head_dim; LORA_E_CAPACITY: 2^31
- * pages or more, page_size above 2^20. */
+ * pages or more, page_size above 2^20, more than 4096 heads. */
 int lora_kv_create(lora_ctx *ctx, const lora_kv_desc *desc, lora_kv **out);
 int lora_kv_destroy(lora_kv *kv);
 
