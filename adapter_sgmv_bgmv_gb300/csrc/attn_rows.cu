@@ -2,12 +2,16 @@
 //
 //   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q.k_j - m),  m = the running maximum
 //
-// over the keys j a row sees.  Every key and value is read from DRAM once per 16 query
-// rows (the group that shares a key head, and a few tokens), so at one new token the
-// bytes of the cache bound it: 16 rows are one m16n8k16 tensor-core tile (bf16 in, fp32
-// sums), whose arithmetic is a few percent of the time the bytes take.
+// over the keys a row sees.  Every key and value is read from DRAM once per unit of 8 (or
+// 16) query rows: the query heads that share a key head, and a few tokens.  At one new
+// token the bytes of the cache bound it, and the arithmetic has to hide behind them: S^T = K Q^T
+// and O^T += V^T W on m16n8k16 tensor-core products (bf16 in, fp32 sums) with the keys and
+// the values' columns on the side of 16 and the query rows on the side of 8, so that a unit
+// of at most 8 rows wastes nothing of a product on rows that are not there.  W^T comes out
+// of the first product as the second one's operand but for a transposition within the
+// warp (movmatrix).
 //
-// Layout.  All (sequence, key head, 16 rows) units are cut into tiles of BT keys and laid
+// Layout.  All (sequence, key head, rows) units are cut into tiles of BT keys and laid
 // on a line that is split evenly over the warps of the grid (attn.cuh).  A warp goes
 // through its piece alone: its own ring of ST stages in shared memory, filled by 16-byte
 // cp.async (any page size, any strides: each row of a stage has its own address), its own
@@ -32,19 +36,23 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;
 constexpr int kUnitCost = 3;   // a unit's start and end, in tiles
+constexpr int kMaxRows = 16;   // of a unit
+constexpr int kMaxCtas = 3;    // a SM
 
-template <int DIM, int FMT>
+// NR: groups of 8 query rows of a unit.
+template <int DIM, int FMT, int NR>
 struct Shape {
+    static constexpr int ROWS = 8 * NR;
     static constexpr int ES = FMT == kKvBf16 ? 2 : 1;
     static constexpr int RB = DIM * ES;                    // bytes of a key row
     static constexpr int BT = FMT == kKvBf16 && DIM == 128 ? 16 : 32;
-    static constexpr int ST = 3;
+    static constexpr int CTAS = FMT == kKvBf16 || NR == 2 ? 2 : 3;
     static constexpr int SCALES = FMT == kKvBf16 ? 0 : BT * 8;
     static constexpr int STAGE = 2 * BT * RB + SCALES;
+    static constexpr int ST = CTAS == 3 && DIM == 128 ? 2 : 3;
     static constexpr int SMEM = kWarps * ST * STAGE + 128;
-    static_assert(ST * STAGE >= kRows * DIM * 4, "a warp's partial takes the place of its ring");
+    static_assert(ST * STAGE >= ROWS * DIM * 4, "a warp's partial takes the place of its ring");
 };
 
 // Byte offset of 16-byte chunk c of row r: rows of RB bytes, chunks exchanged so that
@@ -75,6 +83,14 @@ __device__ __forceinline__ void mma(float c[4], const uint32_t a[4], uint32_t b0
                  "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The 8 x 8 block of bf16 held a row a four lanes, transposed.
+__device__ __forceinline__ uint32_t flip(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ uint32_t bf2(float lo, float hi)
@@ -113,20 +129,21 @@ struct Part {
     Cursor u;
 };
 
-template <int DIM, int FMT>
-__global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant__ AttnParams p)
+template <int DIM, int FMT, int NR>
+__global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_rows(const __grid_constant__ AttnParams p)
 {
-    using S = Shape<DIM, FMT>;
+    using S = Shape<DIM, FMT, NR>;
+    constexpr int kRows = S::ROWS;
     using Cut = Split<kRows, S::BT, kUnitCost>;
     constexpr int BT = S::BT, ST = S::ST, RB = S::RB, N = DIM / 32;
-    constexpr int NT = BT / 8;                             // 8-key tiles of scores
+    constexpr int MT = BT / 16;                            // 16-key tiles of scores
     constexpr int KS = DIM / 16;                           // k-steps of q.k
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     __shared__ int64_t sums[kWarps];
     __shared__ Cursor found[kWarps];
     __shared__ Part parts[2 * kWarps];
-    __shared__ float2 tail_ml[kWarps][kRows];
+    __shared__ float2 tail_ml[kWarps][kMaxRows];
     __shared__ int last_flag;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, g = lane >> 2;
     const KvView &kv = p.kv;
@@ -229,28 +246,33 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
         for (int i = 0; i < ST; ++i)
             pid[i] = page_at(t0 + i);
 
-        // this thread's rows g and g + 8: position, query (as the products want it)
-        int pos[2];
-        uint32_t qf[KS][4];
+        // The queries of rows 8r + g, as the products want them, and the positions of this
+        // thread's rows of the scores, 8r + 2c and 8r + 2c + 1.
+        int pos[NR][2];
+        uint32_t qf[NR][KS][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = g + 8 * i;
+        for (int r = 0; r < NR; ++r) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 8 * r + 2 * c + e;
+                pos[r][e] = row < n_rows ? base + (u.r * kRows + row) / p.group : -1;
+            }
+            const int row = 8 * r + g;
             const bool on = row < n_rows;
             int64_t token, col;
-            row_place<kRows, DIM>(p, u, on ? row : 0, token, col, pos[i]);
-            if (!on)
-                pos[i] = -1;
+            int unused;
+            row_place<kRows, DIM>(p, u, on ? row : 0, token, col, unused);
             const uint16_t *src = p.q + token * p.ldq + col;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 if (FMT == kKvBf16) {
-                    qf[k][i] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 2 * c) : 0u;
-                    qf[k][i + 2] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 8 + 2 * c) : 0u;
+                    qf[r][k][0] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 2 * c) : 0u;
+                    qf[r][k][1] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 8 + 2 * c) : 0u;
                 } else {
                     // the codes of d = 4c .. 4c + 3 arrive as pairs (0, 2) and (1, 3)
                     const uint2 w = on ? *reinterpret_cast<const uint2 *>(src + 16 * k + 4 * c) : make_uint2(0, 0);
-                    qf[k][i] = __byte_perm(w.x, w.y, 0x5410);
-                    qf[k][i + 2] = __byte_perm(w.x, w.y, 0x7632);
+                    qf[r][k][0] = __byte_perm(w.x, w.y, 0x5410);
+                    qf[r][k][1] = __byte_perm(w.x, w.y, 0x7632);
                 }
             }
         }
@@ -259,12 +281,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
             issue(t0 + i, pid[i]);
         int page_next = pid[ST - 1];
 
-        float o[DIM / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float o[DIM / 16][NR][4], m[NR][2], l[NR][2];
 #pragma unroll
-        for (int i = 0; i < DIM / 8; ++i)
+        for (int r = 0; r < NR; ++r) {
+            m[r][0] = m[r][1] = -INFINITY;
+            l[r][0] = l[r][1] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[i][e] = 0.f;
+            for (int i = 0; i < DIM / 16; ++i)
+                o[i][r][0] = o[i][r][1] = o[i][r][2] = o[i][r][3] = 0.f;
+        }
 
         for (int t = t0; t < t1; ++t) {
             tc::cp_async_wait<ST - 2>();
@@ -273,140 +298,149 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
             keys(t, j0, j1);
             const uint32_t st = ring + uint32_t(t % ST) * S::STAGE;
             if (j0 < j1) {
-                // scores of 16 rows x BT keys
-                float s[NT][4];
+                // scores: this thread has keys 16i + g and 16i + g + 8, rows 8r + 2c and + 1
+                float s[MT][NR][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int i = 0; i < MT; ++i) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        s[n][e] = 0.f;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint32_t row = n * 8 + (lane & 7);
+                    for (int r = 0; r < NR; ++r)
+                        s[i][r][0] = s[i][r][1] = s[i][r][2] = s[i][r][3] = 0.f;
+                    const uint32_t row = i * 16 + (lane & 15);
                     if (FMT == kKvBf16) {
 #pragma unroll
-                        for (int k = 0; k < KS; k += 2) {  // four 8 x 8 blocks: two k-steps
+                        for (int k = 0; k < KS; ++k) {
                             uint32_t f[4];
-                            ldsm4(st + cell_at<RB>(row, 2 * k + (lane >> 3)), f);
-                            mma(s[n], qf[k], f[0], f[1]);
-                            mma(s[n], qf[k + 1], f[2], f[3]);
+                            ldsm4(st + cell_at<RB>(row, 2 * k + (lane >> 4)), f);
+#pragma unroll
+                            for (int r = 0; r < NR; ++r)
+                                mma(s[i][r], f, qf[r][k][0], qf[r][k][1]);
                         }
                     } else {
 #pragma unroll
-                        for (int k = 0; k < KS; k += 4) {  // four k-steps
-                            uint32_t f[4];
-                            ldsm4(st + cell_at<RB>(row, k + (lane >> 3)), f);
+                        for (int k = 0; k < KS; k += 2) {  // two 16-element chunks
+                            uint32_t f[4], a[2][4];
+                            ldsm4(st + cell_at<RB>(row, k + (lane >> 4)), f);
+                            widen<FMT>(f[0], a[0][0], a[0][2]);
+                            widen<FMT>(f[1], a[0][1], a[0][3]);
+                            widen<FMT>(f[2], a[1][0], a[1][2]);
+                            widen<FMT>(f[3], a[1][1], a[1][3]);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t lo, hi;
-                                widen<FMT>(f[e], lo, hi);
-                                mma(s[n], qf[k + e], lo, hi);
+                            for (int r = 0; r < NR; ++r) {
+                                mma(s[i][r], a[0], qf[r][k][0], qf[r][k][1]);
+                                mma(s[i][r], a[1], qf[r][k + 1][0], qf[r][k + 1][1]);
                             }
                         }
                     }
                 }
                 // scale, mask, running maximum
                 const float *sc = reinterpret_cast<const float *>(mine + (t % ST) * S::STAGE + 2 * BT * RB);
-                float mx[2] = {m[0], m[1]};
                 const int je = min(j0 + BT, j1);
                 const bool all = je - 1 <= u.span.p0 && je - j0 == BT &&
                                  (p.window == 0 || t < u.span.n_sink || j0 > base + (u.r * kRows + n_rows - 1) / p.group - p.window);
+                float mx[NR][2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float ks[2] = {sl, sl};
-                    if (FMT != kKvBf16) {
-                        const float2 t2 = *reinterpret_cast<const float2 *>(sc + n * 8 + 2 * c);
-                        ks[0] *= t2.x;
-                        ks[1] *= t2.y;
+                for (int r = 0; r < NR; ++r)
+                    mx[r][0] = m[r][0], mx[r][1] = m[r][1];
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int k = 16 * i + 8 * h + g, j = j0 + k;
+                        const float ks = FMT == kKvBf16 ? sl : sl * sc[k];
+#pragma unroll
+                        for (int r = 0; r < NR; ++r)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float v = s[i][r][2 * h + e] * ks;
+                                if (!all && (j >= j1 || !sees(pos[r][e], j, p.window, p.sinks)))
+                                    v = -INFINITY;
+                                s[i][r][2 * h + e] = v;
+                                mx[r][e] = fmaxf(mx[r][e], v);
+                            }
                     }
+                float ref[NR][2];
+                bool moved = false;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v = s[n][e] * ks[e & 1];
-                        if (!all) {
-                            const int j = j0 + n * 8 + 2 * c + (e & 1);
-                            if (j >= j1 || !sees(pos[e >> 1], j, p.window, p.sinks))
-                                v = -INFINITY;
-                        }
-                        s[n][e] = v;
-                        mx[e >> 1] = fmaxf(mx[e >> 1], v);
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1)
+                            mx[r][e] = fmaxf(mx[r][e], __shfl_xor_sync(0xffffffffu, mx[r][e], d));
+                        ref[r][e] = mx[r][e] == -INFINITY ? 0.f : mx[r][e];
+                        moved = moved || mx[r][e] != m[r][e];
                     }
-                }
-                float ref[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-                    ref[i] = mx[i] == -INFINITY ? 0.f : mx[i];
-                }
                 // most tiles of a long sequence leave every maximum as it was
-                if (__any_sync(0xffffffffu, mx[0] != m[0] || mx[1] != m[1])) {
+                if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float a = exp2_fast(m[i] - ref[i]);
-                        m[i] = mx[i];
-                        l[i] *= a;
+                    for (int r = 0; r < NR; ++r)
 #pragma unroll
-                        for (int d = 0; d < DIM / 8; ++d) {
-                            o[d][2 * i] *= a;
-                            o[d][2 * i + 1] *= a;
+                        for (int e = 0; e < 2; ++e) {
+                            const float a = exp2_fast(m[r][e] - ref[r][e]);
+                            m[r][e] = mx[r][e];
+                            l[r][e] *= a;
+#pragma unroll
+                            for (int d = 0; d < DIM / 16; ++d) {
+                                o[d][r][e] *= a;
+                                o[d][r][2 + e] *= a;
+                            }
+                        }
+                }
+                // weights, as the right operand of the second product
+                uint32_t w[MT][NR][2], wl[MT][NR][2];
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float vs = FMT == kKvBf16 ? 1.f : sc[BT + 16 * i + 8 * h + g];
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) {
+                            float q[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float x = s[i][r][2 * h + e], v = exp2_fast(x - ref[r][e]);
+                                l[r][e] += v;
+                                // a key that is not seen has weight 0 whatever its scale is
+                                q[e] = FMT == kKvBf16 ? v : x == -INFINITY ? 0.f : v * vs;
+                            }
+                            const uint32_t hi = bf2(q[0], q[1]);
+                            w[i][r][h] = flip(hi);
+                            wl[i][r][h] = flip(bf2(q[0] - __uint_as_float(hi << 16), q[1] - __uint_as_float(hi & 0xffff0000u)));
                         }
                     }
-                }
-                // weights, as the left operand of the second product
-                uint32_t w[BT / 16][4], wl[BT / 16][4];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float vs[2] = {1.f, 1.f};
-                    if (FMT != kKvBf16) {
-                        const float2 t2 = *reinterpret_cast<const float2 *>(sc + BT + n * 8 + 2 * c);
-                        vs[0] = t2.x;
-                        vs[1] = t2.y;
-                    }
-                    float e[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float v = exp2_fast(s[n][i] - ref[i >> 1]);
-                        l[i >> 1] += v;
-                        // a key that is not seen has weight 0 whatever its scale is
-                        e[i] = FMT == kKvBf16 ? v : s[n][i] == -INFINITY ? 0.f : v * vs[i & 1];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t hi = bf2(e[2 * i], e[2 * i + 1]);
-                        w[n / 2][(n & 1) * 2 + i] = hi;
-                        wl[n / 2][(n & 1) * 2 + i] = bf2(e[2 * i] - __uint_as_float(hi << 16),
-                                                         e[2 * i + 1] - __uint_as_float(hi & 0xffff0000u));
-                    }
-                }
-                // o += w v
+                // o^T += v^T w: this thread has columns of v (d) and rows 8r + 2c, + 1
                 const uint32_t sv = st + BT * RB;
 #pragma unroll
-                for (int kk = 0; kk < BT / 16; ++kk) {
-                    const uint32_t row = kk * 16 + (lane & 15);
+                for (int i = 0; i < MT; ++i) {
                     if (FMT == kKvBf16) {
+                        const uint32_t row = i * 16 + (lane & 7) + 8 * (lane >> 4);
 #pragma unroll
                         for (int d = 0; d < DIM / 16; ++d) {
                             uint32_t f[4];
-                            ldsm4t(sv + cell_at<RB>(row, 2 * d + (lane >> 4)), f);
-                            mma(o[2 * d], w[kk], f[0], f[1]);
-                            mma(o[2 * d + 1], w[kk], f[2], f[3]);
-                            mma(o[2 * d], wl[kk], f[0], f[1]);
-                            mma(o[2 * d + 1], wl[kk], f[2], f[3]);
+                            ldsm4t(sv + cell_at<RB>(row, 2 * d + (lane >> 3 & 1)), f);
+#pragma unroll
+                            for (int r = 0; r < NR; ++r) {
+                                mma(o[d][r], f, w[i][r][0], w[i][r][1]);
+                                mma(o[d][r], f, wl[i][r][0], wl[i][r][1]);
+                            }
                         }
                     } else {
+                        const uint32_t row = i * 16 + (lane & 15);
 #pragma unroll
                         for (int d = 0; d < DIM / 16; d += 2) {   // 16-element chunks d, d + 1
-                            uint32_t f[4], e0, o0, e1, o1;
+                            uint32_t f[4], a[2][4];
                             ldsm4t(sv + cell_at<RB>(row, d + (lane >> 4)), f);
+                            widen<FMT>(f[0], a[0][0], a[0][1]);
+                            widen<FMT>(f[1], a[0][2], a[0][3]);
+                            widen<FMT>(f[2], a[1][0], a[1][1]);
+                            widen<FMT>(f[3], a[1][2], a[1][3]);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                widen<FMT>(f[2 * e], e0, o0);
-                                widen<FMT>(f[2 * e + 1], e1, o1);
-                                mma(o[2 * (d + e)], w[kk], e0, e1);
-                                mma(o[2 * (d + e) + 1], w[kk], o0, o1);
-                                mma(o[2 * (d + e)], wl[kk], e0, e1);
-                                mma(o[2 * (d + e) + 1], wl[kk], o0, o1);
-                            }
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int r = 0; r < NR; ++r) {
+                                    mma(o[d + e][r], a[e], w[i][r][0], w[i][r][1]);
+                                    mma(o[d + e][r], a[e], wl[i][r][0], wl[i][r][1]);
+                                }
                         }
                     }
                 }
@@ -419,35 +453,40 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
         tc::cp_async_wait<0>();
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        }
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
+                    l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], d);
 
-        // Where the rows go: the unit's end, or a partial.  Element d of the output held as
-        // o[i][e]: bf16 pools, 8i + 2c + (e & 1); 8-bit pools, tiles come in even / odd
-        // pairs of one 16-wide chunk, 16 (i / 2) + 4c + 2 (e & 1) + (i & 1).
+        // Where the rows go: the unit's end, or a partial.  o[i][r][e] is row 8r + 2c + (e & 1)
+        // and element d = 16i + g + 8 (e / 2) for bf16 pools, 16i + 2g + e / 2 for 8-bit ones
+        // (their chunks come apart into even and odd elements).
         const bool begins = t0 == 0, ends = t1 == u.span.n;
         const bool head = ends && !begins;
-        float *dst = head ? p.part.warp_o + int64_t(worker) * kRows * DIM : reinterpret_cast<float *>(mine);
-        float2 *dml = head ? p.part.warp_ml + int64_t(worker) * kRows : tail_ml[warp];
+        float *dst = head ? p.part.warp_o + int64_t(worker) * kMaxRows * DIM : reinterpret_cast<float *>(mine);
+        float2 *dml = head ? p.part.warp_ml + int64_t(worker) * kMaxRows : tail_ml[warp];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = g + 8 * i;
-            if (row < n_rows) {
-                if (c == 0)
-                    dml[row] = make_float2(m[i], l[i]);
+        for (int r = 0; r < NR; ++r)
 #pragma unroll
-                for (int d = 0; d < DIM / 8; ++d) {
+            for (int e = 0; e < 2; ++e) {
+                const int row = 8 * r + 2 * c + e;
+                if (row >= n_rows)
+                    continue;
+                if (g == 0)
+                    dml[row] = make_float2(m[r][e], l[r][e]);
+#pragma unroll
+                for (int i = 0; i < DIM / 16; ++i) {
+                    float *at = dst + row * DIM + 16 * i;
                     if (FMT == kKvBf16) {
-                        *reinterpret_cast<float2 *>(dst + row * DIM + 8 * d + 2 * c) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
-                    } else if ((d & 1) == 0) {
-                        *reinterpret_cast<float4 *>(dst + row * DIM + 8 * d + 4 * c) =
-                            make_float4(o[d][2 * i], o[d + 1][2 * i], o[d][2 * i + 1], o[d + 1][2 * i + 1]);
+                        at[g] = o[i][r][e];
+                        at[g + 8] = o[i][r][2 + e];
+                    } else {
+                        *reinterpret_cast<float2 *>(at + 2 * g) = make_float2(o[i][r][e], o[i][r][2 + e]);
                     }
                 }
             }
-        }
         __syncwarp();
         if (begins && ends) {
             for (int row = 0; row < n_rows; ++row) {
@@ -499,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
                 float acc[N], m, l;
                 auto ml = [&](int k) {
                     const int w = idx[k] >> 1;
-                    return (idx[k] & 1) ? tail_ml[w][row] : __ldcg(&p.part.warp_ml[(int64_t(blockIdx.x) * kWarps + w) * kRows + row]);
+                    return (idx[k] & 1) ? tail_ml[w][row] : __ldcg(&p.part.warp_ml[(int64_t(blockIdx.x) * kWarps + w) * kMaxRows + row]);
                 };
                 auto o = [&](int k, float *v) {
                     const int w = idx[k] >> 1;
@@ -509,14 +548,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
                         for (int e = 0; e < N; ++e)
                             v[e] = src[e];
                     } else {
-                        load_vec<N>(v, p.part.warp_o + ((int64_t(blockIdx.x) * kWarps + w) * kRows + row) * DIM + lane * N);
+                        load_vec<N>(v, p.part.warp_o + ((int64_t(blockIdx.x) * kWarps + w) * kMaxRows + row) * DIM + lane * N);
                     }
                 };
                 join<DIM>(n, o, ml, acc, m, l);
                 if (begins && ends) {
                     finish_row<kRows, DIM, FMT>(p, parts[i].u, row, acc, l);
                 } else {
-                    const int64_t at2 = (int64_t(blockIdx.x) * 2 + begins) * kRows + row;
+                    const int64_t at2 = (int64_t(blockIdx.x) * 2 + begins) * kMaxRows + row;
 #pragma unroll
                     for (int e = 0; e < N; ++e)
                         p.part.cta_o[at2 * DIM + lane * N + e] = acc[e];
@@ -546,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
         __threadfence();
         for (int row = warp; row < pt.m_rows; row += kWarps) {
             float acc[N], m, l;
-            auto at = [&](int i) { return ((first + i) * 2 + (i == 0)) * kRows + row; };
+            auto at = [&](int i) { return ((first + i) * 2 + (i == 0)) * kMaxRows + row; };
             join<DIM>(int(final_ - first) + 1,
                       [&](int i, float *v) { load_vec<N>(v, p.part.cta_o + at(i) * DIM + lane * N); },
                       [&](int i) { return __ldcg(&p.part.cta_ml[at(i)]); }, acc, m, l);
@@ -558,35 +597,46 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const __grid_constant
         grid_dep_wait();
 }
 
-template <int DIM, int FMT>
+template <int DIM, int FMT, int NR>
 cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream)
 {
+    using S = Shape<DIM, FMT, NR>;
     static bool configured = false;
     if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(k_attn_rows<DIM, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Shape<DIM, FMT>::SMEM);
+        cudaError_t e = cudaFuncSetAttribute(k_attn_rows<DIM, FMT, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
         if (e != cudaSuccess)
             return e;
         configured = true;
     }
+    static_assert(S::CTAS <= kMaxCtas, "the scratch has room for every CTA");
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(2 * sms));
+    cfg.gridDim = dim3(unsigned(S::CTAS * sms));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Shape<DIM, FMT>::SMEM;
+    cfg.dynamicSmemBytes = S::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn_rows<DIM, FMT>, p);
+    return cudaLaunchKernelEx(&cfg, k_attn_rows<DIM, FMT, NR>, p);
+}
+
+// Units of 8 rows where no sequence can have more; else of 16.
+template <int FMT>
+cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream)
+{
+    const bool wide = p.kv.dim == 128;
+    if (int64_t(p.b.max_new) * p.group <= 8)
+        return wide ? launch<128, FMT, 1>(p, sms, stream) : launch<64, FMT, 1>(p, sms, stream);
+    return wide ? launch<128, FMT, 2>(p, sms, stream) : launch<64, FMT, 2>(p, sms, stream);
 }
 
 }  // namespace
 
 size_t attn_rows_scratch(uint8_t *base, int sms, AttnScratch *s)
 {
-    const size_t ctas = size_t(sms) * 2, warps = ctas * kWarps;
+    const size_t ctas = size_t(sms) * kMaxCtas, warps = ctas * kWarps;
     const size_t row = 128 * sizeof(float);
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -595,10 +645,10 @@ size_t attn_rows_scratch(uint8_t *base, int sms, AttnScratch *s)
         return p;
     };
     AttnScratch t;
-    t.cta_o = reinterpret_cast<float *>(take(ctas * 2 * kRows * row));
-    t.cta_ml = reinterpret_cast<float2 *>(take(ctas * 2 * kRows * sizeof(float2)));
-    t.warp_o = reinterpret_cast<float *>(take(warps * kRows * row));
-    t.warp_ml = reinterpret_cast<float2 *>(take(warps * kRows * sizeof(float2)));
+    t.cta_o = reinterpret_cast<float *>(take(ctas * 2 * kMaxRows * row));
+    t.cta_ml = reinterpret_cast<float2 *>(take(ctas * 2 * kMaxRows * sizeof(float2)));
+    t.warp_o = reinterpret_cast<float *>(take(warps * kMaxRows * row));
+    t.warp_ml = reinterpret_cast<float2 *>(take(warps * kMaxRows * sizeof(float2)));
     t.arrived = reinterpret_cast<int *>(take(ctas * sizeof(int)));
     if (s)
         *s = t;
@@ -607,11 +657,10 @@ size_t attn_rows_scratch(uint8_t *base, int sms, AttnScratch *s)
 
 cudaError_t launch_attn_rows(const AttnParams &p, int sms, cudaStream_t stream)
 {
-    const bool wide = p.kv.dim == 128;
     switch (p.kv.format) {
-    case kKvBf16: return wide ? launch<128, kKvBf16>(p, sms, stream) : launch<64, kKvBf16>(p, sms, stream);
-    case kKvInt8: return wide ? launch<128, kKvInt8>(p, sms, stream) : launch<64, kKvInt8>(p, sms, stream);
-    default: return wide ? launch<128, kKvFp8>(p, sms, stream) : launch<64, kKvFp8>(p, sms, stream);
+    case kKvBf16: return launch<kKvBf16>(p, sms, stream);
+    case kKvInt8: return launch<kKvInt8>(p, sms, stream);
+    default: return launch<kKvFp8>(p, sms, stream);
     }
 }
 
