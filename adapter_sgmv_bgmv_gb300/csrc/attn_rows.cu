@@ -38,7 +38,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnitCost = 3;   // a unit's start and end, in tiles
 constexpr int kMaxRows = 16;   // of a unit
-constexpr int kMaxCtas = 3;    // a SM
+constexpr int kMaxCtas = 2;    // a SM
 
 // NR: groups of 8 query rows of a unit.
 template <int DIM, int FMT, int NR>
@@ -46,11 +46,11 @@ struct Shape {
     static constexpr int ROWS = 8 * NR;
     static constexpr int ES = FMT == kKvBf16 ? 2 : 1;
     static constexpr int RB = DIM * ES;                    // bytes of a key row
+    static constexpr int CTAS = 2;
     static constexpr int BT = FMT == kKvBf16 && DIM == 128 ? 16 : 32;
-    static constexpr int CTAS = FMT == kKvBf16 || NR == 2 ? 2 : 3;
     static constexpr int SCALES = FMT == kKvBf16 ? 0 : BT * 8;
     static constexpr int STAGE = 2 * BT * RB + SCALES;
-    static constexpr int ST = CTAS == 3 && DIM == 128 ? 2 : 3;
+    static constexpr int ST = 3;
     static constexpr int SMEM = kWarps * ST * STAGE + 128;
     static_assert(ST * STAGE >= ROWS * DIM * 4, "a warp's partial takes the place of its ring");
 };
@@ -99,17 +99,16 @@ __device__ __forceinline__ uint32_t bf2(float lo, float hi)
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
-// Four codes (bytes b0..b3) to the bf16 pairs (b0, b2) and (b1, b3).
+// Four codes (bytes b0..b3) to the bf16 pairs (b0, b2) and (b1, b3), times kCodeUnit.
 template <int FMT>
 __device__ __forceinline__ void widen(uint32_t r, uint32_t &even, uint32_t &odd)
 {
     if (FMT == kKvInt8) {
-        // 128 + the low seven bits, less 128 or (sign bit) 256: exact in bf16
-        const uint32_t o = r >> 8;
-        const uint32_t e1 = (r & 0x007f007fu) | 0x43004300u, e0 = (r & 0x00800080u) | 0x43004300u;
-        const uint32_t o1 = (o & 0x007f007fu) | 0x43004300u, o0 = (o & 0x00800080u) | 0x43004300u;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(even) : "r"(e1), "r"(e0));
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(o1), "r"(o0));
+        // code + 128 as a byte is a bf16 of (code + 128) 2^-133; times 2^127, less 2, it is
+        // code 2^-6, exact, in one operation that does not load the integer pipe
+        const uint32_t e = (r & 0x00ff00ffu) ^ 0x00800080u, o = ((r >> 8) & 0x00ff00ffu) ^ 0x00800080u;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(even) : "r"(e), "r"(0x7f007f00u), "r"(0xc000c000u));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(odd) : "r"(o), "r"(0x7f007f00u), "r"(0xc000c000u));
     } else {
         const uint32_t s = __byte_perm(r, 0, 0x3120);      // b0 b2 b1 b3
         const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(s & 0xffffu), __NV_E4M3);
@@ -346,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int k = 16 * i + 8 * h + g, j = j0 + k;
-                        const float ks = FMT == kKvBf16 ? sl : sl * sc[k];
+                        const float ks = FMT == kKvBf16 ? sl : sl / kCodeUnit<FMT> * sc[k];
 #pragma unroll
                         for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -392,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float vs = FMT == kKvBf16 ? 1.f : sc[BT + 16 * i + 8 * h + g];
+                        const float vs = FMT == kKvBf16 ? 1.f : sc[BT + 16 * i + 8 * h + g] / kCodeUnit<FMT>;
 #pragma unroll
                         for (int r = 0; r < NR; ++r) {
                             float q[2];

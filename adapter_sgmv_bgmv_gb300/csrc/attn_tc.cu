@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
 #pragma unroll
                 for (int i = 0; i < C8; ++i) {
                     const int row = lw * 32 + i * R8 + lane / C8, ch = 2 * (lane % C8);
-                    const uint2 a = widen4<FMT>(x[i].x), b = widen4<FMT>(x[i].y), c = widen4<FMT>(x[i].z), d = widen4<FMT>(x[i].w);
+                    const uint2 a = widen4_unit<FMT>(x[i].x), b = widen4_unit<FMT>(x[i].y), c = widen4_unit<FMT>(x[i].z), d = widen4_unit<FMT>(x[i].w);
                     uint8_t *base = smem + S::RING + slot * S::TILE + (ch / 8) * S::HALF;
                     *reinterpret_cast<uint4 *>(base + tc::sw128(row, ch % 8)) = make_uint4(a.x, a.y, b.x, b.y);
                     *reinterpret_cast<uint4 *>(base + tc::sw128(row, ch % 8 + 1)) = make_uint4(c.x, c.y, d.x, d.y);
@@ -711,8 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             auto begin = [&]() {
                 place(page, at, s_at);
                 fetch(x, kv.k, at);
-                ks = at < 0 ? 0.f : kv.k_scale[s_at] * sl;
-                vs = at < 0 ? 0.f : kv.v_scale[s_at];
+                ks = at < 0 ? 0.f : kv.k_scale[s_at] * (sl / kCodeUnit<FMT>);
+                vs = at < 0 ? 0.f : kv.v_scale[s_at] * (1.f / kCodeUnit<FMT>);
             };
             if (pt)
                 begin();

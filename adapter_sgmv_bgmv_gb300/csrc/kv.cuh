@@ -119,6 +119,25 @@ __device__ __forceinline__ uint2 widen4(uint32_t r)
     return y;
 }
 
+// What the attention kernels' products take of a code: kCodeUnit times it.
+template <int FMT>
+constexpr float kCodeUnit = FMT == kKvInt8 ? 0x1p-6f : 1.f;
+
+// Four codes (bytes 0..3) as bf16, in order, times kCodeUnit; exact.
+template <int FMT>
+__device__ __forceinline__ uint2 widen4_unit(uint32_t r)
+{
+    if (FMT != kKvInt8)
+        return widen4<FMT>(r);
+    // code + 128 as a byte is a bf16 of (code + 128) 2^-133; times 2^127, less 2, it is
+    // code 2^-6, in one operation that does not load the integer pipe
+    const uint32_t t = r ^ 0x80808080u, a = __byte_perm(t, 0, 0x4140), b = __byte_perm(t, 0, 0x4342);
+    uint2 y;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y.x) : "r"(a), "r"(0x7f007f00u), "r"(0xc000c000u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y.y) : "r"(b), "r"(0x7f007f00u), "r"(0xc000c000u));
+    return y;
+}
+
 // scale times 16 codes, rounded to bf16 once.
 template <int FMT>
 __device__ __forceinline__ void decode16(uint4 c, float scale, uint4 y[2])
