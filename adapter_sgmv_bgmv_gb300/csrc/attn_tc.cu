@@ -16,8 +16,12 @@
 //   warps 8-11       loads: cells of the pages to 128-byte-swizzled tiles, each row with its
 //                    own address (any page size, any strides); bf16 by cp.async, 8-bit codes
 //                    through registers, where they become bf16 (exact).
-//   warp 12          one thread issues the products.
-//   warp 13          one thread goes along the CTA's piece ahead of the others and leaves
+//   warps 12, 13     one thread each issues the products of tile A / B: an issue holds its
+//                    thread until the tensor cores have taken it, so with one thread for both
+//                    they stood still while it waited for barriers (2 400 of 5 400 cycles a
+//                    key tile).  The two take turns: left to themselves the tiles fall into
+//                    step, both at their weights and then both at their products.
+//   warp 14          one thread goes along the CTA's piece ahead of the others and leaves
 //                    them what they need of each unit (the only copy of that code: see below
 //                    on code size).
 //
@@ -71,7 +75,7 @@ struct TcShape {
 // Barriers, 8 bytes each from BARS.
 enum Bar : uint32_t {
     kFull = 0, kEmpty = 8, kQFull = 16, kQEmpty = 18, kSFull = 20, kWReady = 22, kPvDone = 24,
-    kPartFull = 26, kPartEmpty = 30, kJoin = 34
+    kPartFull = 26, kPartEmpty = 30, kJoin = 34, kTurn = 35
 };
 
 template <int R>
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     const uint32_t raw = smem_u32(smem_raw), sm = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (sm - raw);
     __shared__ int64_t sums[kThreads / 32];
-    __shared__ Cursor cursor;                              // warp 13's
+    __shared__ Cursor cursor;                              // warp 14's
     __shared__ Part parts[kParts];
     __shared__ uint32_t poison[kScaleSlots * 4];           // per slot: keys whose value's scale is not finite
     __shared__ uint32_t tmem_slot;
@@ -341,11 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
 
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
-            mbar_init(bar(kFull + i), 4);          // the load warps
-            mbar_init(bar(kEmpty + i), 1);         // a commit
+            // the load warps' lanes as their copies end, or the warps as they have stored
+            mbar_init(bar(kFull + i), FMT == kKvBf16 ? 128 : 4);
+            mbar_init(bar(kEmpty + i), 2);         // a commit of each row tile's products
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kQFull + i), 4);
+            mbar_init(bar(kQFull + i), 128);
             mbar_init(bar(kQEmpty + i), 1);
             mbar_init(bar(kSFull + i), 1);
             mbar_init(bar(kWReady + i), 4);        // the warps of one row tile
@@ -353,9 +358,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         }
         for (int i = 0; i < kParts; ++i) {
             mbar_init(bar(kPartFull + i), 1);
-            mbar_init(bar(kPartEmpty + i), 13);    // every warp that reads the parts
+            mbar_init(bar(kPartEmpty + i), 14);    // every warp that reads the parts
         }
         mbar_init(bar(kJoin), 8);
+        mbar_init(bar(kTurn + 0), 1);
+        mbar_init(bar(kTurn + 1), 1);
         fence_mbar_init();
         dead_flag = 0;
     }
@@ -575,7 +582,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         bool alive = true;
         uint32_t entry = 0, slot = 0, phase = 1;           // ring entries: keys 2j, values 2j + 1
         int tile_no = 0;
-        uint32_t pending = 0;                              // barrier of the copies under way
         auto wait = [&](uint32_t b, uint32_t parity) {
             alive = __all_sync(0xffffffffu, alive && await(bar(b), parity, dead, p.status, kDevTimeoutPipe));
             return alive;
@@ -626,27 +632,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             row_place<kRows, DIM>(p, *pt, row, token, col, pos);
             return (token * p.ldq + col) * 2;
         };
-        // The copies before the last commit are in shared memory: hand them over.
-        auto settle = [&](bool all) {
-            if (all)
-                tc::cp_async_wait<0>();
-            else
-                tc::cp_async_wait<1>();
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (pending && lane == 0)
-                mbar_arrive(pending);
-            pending = 0;
-        };
         constexpr int CH = DIM / 8, RPI = 32 / CH;         // 16-byte chunks of a bf16 row, rows an instruction
-        auto copy_rows = [&](uint32_t dst, const uint8_t *src, int64_t at) {
+        // The copies arrive on `done` by themselves, lane by lane, as they end; the warp that
+        // reads them by the tensor cores makes them visible to those.
+        auto copy_rows = [&](uint32_t dst, const uint8_t *src, int64_t at, uint32_t done) {
 #pragma unroll 4
             for (int i = 0; i < CH; ++i) {
                 const int rr = i * RPI + lane / CH, ch = lane % CH, row = lw * 32 + rr;
                 const int64_t a = __shfl_sync(0xffffffffu, (long long)at, rr);
                 tc::cp_async16(dst + (ch / 8) * S::HALF + tc::sw128(row, ch % 8), src + (a < 0 ? 0 : a + ch * 16), a < 0 ? 0u : 16u);
             }
-            tc::cp_async_commit();
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(done)) : "memory");
         };
         enter();
         int page = page_id();
@@ -672,14 +668,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         break;
                     copy_rows(ring ? sm + S::RING + slot * S::TILE : sm + (job - 1) * S::TILE,
                               job == 0 ? kv.k : job == 3 ? kv.v : reinterpret_cast<const uint8_t *>(p.q),
-                              ring ? at : job == 1 ? qa : qb);
-                    settle(false);
-                    pending = ring ? bar(kFull + slot) : bar(kQFull + job - 1);
+                              ring ? at : job == 1 ? qa : qb, ring ? kFull + slot : kQFull + job - 1);
                     if (ring)
                         advance();
                 }
             }
-            settle(true);
         } else {
             constexpr int C8 = DIM / 16, R8 = 32 / C8;     // 16-byte chunks of a row of codes
             auto fetch = [&](uint4 x[C8], const uint8_t *src, int64_t at) {
@@ -741,11 +734,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     for (int T = 0; T < 2; ++T) {
                         if (no > 0 && !wait(kQEmpty + T, (no - 1) & 1))
                             break;
-                        copy_rows(sm + T * S::TILE, reinterpret_cast<const uint8_t *>(p.q), T ? qb : qa);
-                        settle(false);
-                        pending = bar(kQFull + T);
+                        copy_rows(sm + T * S::TILE, reinterpret_cast<const uint8_t *>(p.q), T ? qb : qa, kQFull + T);
                     }
-                    settle(true);
                 }
                 if (pt)
                     begin();
@@ -755,17 +745,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 ++tile_no;
             }
         }
-    } else if (warp == 12) {
+    } else if (warp < 14) {
         // ------------------------------------------------------------ products
         setmaxnreg_dec<Regs<FMT>::few>();
+        const int T = warp - 12;
         if (lane == 0) {
             constexpr uint32_t iqk = tc::idesc_bf16(kM, kKeys, 0, 0), ipv = tc::idesc_bf16(kM, DIM, 0, 1);
-            const uint64_t q_desc = tc::smem_desc_sw128(sm, 16u, 1024u), k_desc = tc::smem_desc_sw128(sm + S::RING, 16u, 1024u),
-                           v_desc = tc::smem_desc_sw128(sm + S::RING, S::HALF, 1024u);
             constexpr uint32_t kTile16 = S::TILE / 16, kHalf16 = S::HALF / 16;   // descriptor units
+            const uint64_t q = tc::smem_desc_sw128(sm + T * S::TILE, 16u, 1024u),
+                           k_desc = tc::smem_desc_sw128(sm + S::RING, 16u, 1024u),
+                           v_desc = tc::smem_desc_sw128(sm + S::RING, S::HALF, 1024u);
+            const uint32_t tS = tmem + T * 128u, tO = tmem + 256u + T * uint32_t(DIM);
             // ring slots of the keys and values in turn: keys 2j, values 2j + 1
-            uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0;
-            uint32_t w_phase = 0;                          // a bit for each row tile
+            uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0, w_phase = 0;
+            uint32_t turn = 0;                             // rounds so far
             auto next_slot = [&](uint32_t &slot, uint32_t &phase) {
                 slot += 2;
                 if (slot >= uint32_t(ST))
@@ -780,59 +773,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 const Part *pt = part();
                 if (!pt)
                     break;
-                const Active act_a = pt->act[0], act_b = pt->act[1];
+                const Active act = pt->act[T];
                 const int t0 = pt->t0, t1 = pt->t1;
                 mbar_arrive(bar(kPartEmpty + part_no % kParts));
                 uint32_t started = 0;
-                // Round t: the values of tile t - 1 and the scores of tile t, for A, then for B.
+                // Round t: the values of tile t - 1 and the scores of tile t, one behind the
+                // other; what they need besides the weights is waited for ahead.
 #pragma unroll 1
-                for (int t = t0; t <= t1 && alive; ++t) {
+                for (int t = t0; t <= t1; ++t) {
                     const bool with_v = t > t0, with_s = t < t1;
                     if (with_v && !wait(kFull + v_slot, v_phase))
                         break;
-#pragma unroll 1
-                    for (int T = 0; T < 2; ++T) {
-                        const Active act{T ? act_b.from : act_a.from, T ? act_b.to : act_a.to, T ? act_b.behind : act_a.behind};
-                        if (with_v && act(t - 1)) {
-                            if (!wait(kWReady + T, w_phase >> T & 1))
-                                break;
-                            w_phase ^= 1u << T;
+                    if (with_s && !wait(kFull + k_slot, k_phase))
+                        break;
+                    if (t == t0 && !wait(kQFull + T, part_no & 1))
+                        break;
+                    tc::fence_proxy_async_smem();          // the copies that were waited for
+                    const bool values = with_v && act(t - 1);
+                    if (values && !wait(kWReady + T, w_phase))
+                        break;
+                    // A's round, then B's, by turns: A's first needs no leave, B's n-th and A's
+                    // next have the other's
+                    if ((T == 1 || turn > 0) && !wait(kTurn + T, (turn - (T == 0)) & 1))
+                        break;
+                    ++turn;
+                    if (with_v) {
+                        if (values) {
+                            w_phase ^= 1;
                             tc::fence_after_sync();
                             const uint64_t v = v_desc + v_slot * kTile16;
-                            const uint32_t a = tmem + T * 128u, d = tmem + 256u + T * uint32_t(DIM);
-                            mma_tmem_a(d, a, v, ipv, started >> T & 1);
+                            mma_tmem_a(tO, tS, v, ipv, started);
 #pragma unroll
                             for (int i = 1; i < kKeys / 16; ++i)
-                                mma_tmem_a(d, a + 8 * i, v + 128 * i, ipv, 1);
+                                mma_tmem_a(tO, tS + 8 * i, v + 128 * i, ipv, 1);
                             tc::mma_commit(bar(kPvDone + T));
-                            started |= 1u << T;
+                            started = 1;
                         }
-                        if (with_v && T == 1)
-                            tc::mma_commit(bar(kEmpty + v_slot));
-                        if (with_s) {
-                            if (T == 0 && !wait(kFull + k_slot, k_phase))
-                                break;
-                            if (t == t0 && !wait(kQFull + T, part_no & 1))
-                                break;
-                            if (act(t)) {
-                                tc::fence_after_sync();
-                                const uint64_t q = q_desc + T * kTile16, k = k_desc + k_slot * kTile16;
-                                const uint32_t d = tmem + T * 128u;
+                        tc::mma_commit(bar(kEmpty + v_slot));
+                        next_slot(v_slot, v_phase);
+                    }
+                    if (with_s) {
+                        if (act(t)) {
+                            tc::fence_after_sync();
+                            const uint64_t k = k_desc + k_slot * kTile16;
 #pragma unroll
-                                for (int i = 0; i < DIM / 16; ++i)
-                                    tc::mma_bf16(d, q + (i / 4) * kHalf16 + 2 * (i % 4), k + (i / 4) * kHalf16 + 2 * (i % 4), iqk, i > 0);
-                                tc::mma_commit(bar(kSFull + T));
-                            }
-                            if (t + 1 == t1)
-                                tc::mma_commit(bar(kQEmpty + T));
-                            if (T == 1)
-                                tc::mma_commit(bar(kEmpty + k_slot));
+                            for (int i = 0; i < DIM / 16; ++i)
+                                tc::mma_bf16(tS, q + (i / 4) * kHalf16 + 2 * (i % 4), k + (i / 4) * kHalf16 + 2 * (i % 4), iqk, i > 0);
+                            tc::mma_commit(bar(kSFull + T));
                         }
                     }
-                    if (with_v)
-                        next_slot(v_slot, v_phase);
-                    if (with_s)
+                    mbar_arrive(bar(kTurn + 1 - T));
+                    if (with_s) {
+                        if (t + 1 == t1)
+                            tc::mma_commit(bar(kQEmpty + T));
+                        tc::mma_commit(bar(kEmpty + k_slot));
                         next_slot(k_slot, k_phase);
+                    }
                 }
                 ++part_no;
             }
@@ -841,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     } else {
         // ------------------------------------------------------------ parts
         setmaxnreg_dec<Regs<FMT>::few>();
-        if (warp == 13 && lane == 0) {
+        if (warp == 14 && lane == 0) {
             int64_t x = piece * blockIdx.x;
             const int64_t x1 = min(x + piece, total);
             bool more = true;
@@ -885,6 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         }
         __syncwarp();
     }
+    tc::cp_async_wait_all();
     // Every product has ended: the weights' warps waited for each tile's last.  Where the
     // roles gave up, those under way get the time that they can take at most.
     tc::fence_before_sync();
