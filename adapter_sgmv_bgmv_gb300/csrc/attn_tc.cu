@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + T * 128u, tO = tmem + lanes + 256u + T * uint32_t(DIM);
         const float sl = p.scale * 1.4426950408889634f;
-        uint32_t n_s = 0, n_join = 0;                      // S tiles taken so far, joins
+        uint32_t n_s = 0, n_end = 0, n_join = 0;           // S tiles taken so far, parts ended, joins
         int tile_no = 0;                                   // key tiles of the CTA so far
         bool alive = true;
         auto wait = [&](uint32_t b, uint32_t parity) {
@@ -480,9 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     if (move)
                         ref = top;
                     l *= a;
-                    if (begun) {                           // the products so far, at rest
-                        if (!wait(kPvDone + T, (n_s - 1) & 1))
-                            break;
+                    if (begun) {                           // S here says that the products so far are at rest
 #pragma unroll 1
                         for (int i = 0; i < DIM; i += 16) {
                             uint32_t v[16];
@@ -506,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             }
             // the part's end
             if (begun)
-                wait(kPvDone + T, (n_s - 1) & 1);
+                wait(kPvDone + T, n_end++ & 1);
             if (!alive)
                 break;
             if (pt->begins && pt->ends) {
@@ -797,37 +795,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     if ((T == 1 || turn > 0) && !wait(kTurn + T, (turn - (T == 0)) & 1))
                         break;
                     ++turn;
-                    if (with_v) {
-                        if (values) {
-                            w_phase ^= 1;
-                            tc::fence_after_sync();
-                            const uint64_t v = v_desc + v_slot * kTile16;
-                            mma_tmem_a(tO, tS, v, ipv, started);
+                    tc::fence_after_sync();
+                    if (values) {
+                        w_phase ^= 1;
+                        const uint64_t v = v_desc + v_slot * kTile16;
+                        mma_tmem_a(tO, tS, v, ipv, started);
 #pragma unroll
-                            for (int i = 1; i < kKeys / 16; ++i)
-                                mma_tmem_a(tO, tS + 8 * i, v + 128 * i, ipv, 1);
-                            tc::mma_commit(bar(kPvDone + T));
-                            started = 1;
-                        }
+                        for (int i = 1; i < kKeys / 16; ++i)
+                            mma_tmem_a(tO, tS + 8 * i, v + 128 * i, ipv, 1);
+                        started = 1;
+                    }
+                    if (with_s && act(t)) {
+                        const uint64_t k = k_desc + k_slot * kTile16;
+#pragma unroll
+                        for (int i = 0; i < DIM / 16; ++i)
+                            tc::mma_bf16(tS, q + (i / 4) * kHalf16 + 2 * (i % 4), k + (i / 4) * kHalf16 + 2 * (i % 4), iqk, i > 0);
+                        // says that every product so far has ended, the values' among them
+                        tc::mma_commit(bar(kSFull + T));
+                    }
+                    mbar_arrive(bar(kTurn + 1 - T));
+                    if (t == t1 && started)
+                        tc::mma_commit(bar(kPvDone + T));
+                    if (with_v) {
                         tc::mma_commit(bar(kEmpty + v_slot));
                         next_slot(v_slot, v_phase);
                     }
                     if (with_s) {
-                        if (act(t)) {
-                            tc::fence_after_sync();
-                            const uint64_t k = k_desc + k_slot * kTile16;
-#pragma unroll
-                            for (int i = 0; i < DIM / 16; ++i)
-                                tc::mma_bf16(tS, q + (i / 4) * kHalf16 + 2 * (i % 4), k + (i / 4) * kHalf16 + 2 * (i % 4), iqk, i > 0);
-                            tc::mma_commit(bar(kSFull + T));
-                        }
-                    }
-                    mbar_arrive(bar(kTurn + 1 - T));
-                    if (with_s) {
-                        if (t + 1 == t1)
-                            tc::mma_commit(bar(kQEmpty + T));
                         tc::mma_commit(bar(kEmpty + k_slot));
                         next_slot(k_slot, k_phase);
+                        if (t + 1 == t1)
+                            tc::mma_commit(bar(kQEmpty + T));
                     }
                 }
                 ++part_no;
