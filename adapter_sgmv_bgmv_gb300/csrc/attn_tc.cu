@@ -74,8 +74,9 @@ struct TcShape {
 
 // Barriers, 8 bytes each from BARS.
 enum Bar : uint32_t {
-    kFull = 0, kEmpty = 8, kQFull = 16, kQEmpty = 18, kSFull = 20, kWReady = 22, kPvDone = 24,
-    kPartFull = 26, kPartEmpty = 30, kJoin = 34, kTurn = 35
+    kFull = 0, kEmpty = 8, kQFull = 16, kQEmpty = 18, kSFull = 20, kPvDone = 24,
+    kPartFull = 26, kPartEmpty = 30, kJoin = 34, kTurn = 35,
+    kWReady = 37                  // of A's first and second half of the keys, then B's
 };
 
 template <int R>
@@ -261,9 +262,11 @@ __device__ __forceinline__ float maximum(uint32_t tS, const float *ks)
 }
 
 // The weights exp2(s * f - m), written as bf16 (times the values' scales, ks + kKeys) over
-// the columns of S they came from; returns their sum.
+// the columns of S they came from; returns their sum.  Each half of the keys is handed
+// over as it is written (`ready`, and the next barrier), so that the products with the
+// first half run during the second.
 template <int FMT, bool SCALED>
-__device__ __forceinline__ float weights(uint32_t tS, const float *ks, float f, float m)
+__device__ __forceinline__ float weights(uint32_t tS, const float *ks, float f, float m, uint32_t ready)
 {
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float2 ff = make_float2(f, f), less = make_float2(-m, -m);
@@ -302,6 +305,11 @@ __device__ __forceinline__ float weights(uint32_t tS, const float *ks, float f, 
             tc::tmem_wait_ld();
             tmem_st16(tS + 32 * h + 16 * b, pk);
         }
+        tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            mbar_arrive(ready + 8 * h);
     }
     return (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
 }
@@ -353,7 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             mbar_init(bar(kQFull + i), 128);
             mbar_init(bar(kQEmpty + i), 1);
             mbar_init(bar(kSFull + i), 1);
-            mbar_init(bar(kWReady + i), 4);        // the warps of one row tile
+            mbar_init(bar(kWReady + 2 * i), 4);    // the warps of one row tile
+            mbar_init(bar(kWReady + 2 * i + 1), 4);
             mbar_init(bar(kPvDone + i), 1);
         }
         for (int i = 0; i < kParts; ++i) {
@@ -493,12 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     }
                 }
                 const float m = ref == -INFINITY ? 0.f : ref;
-                l += plain ? weights<FMT, false>(tS, ks, f, m) : weights<FMT, true>(tS, ks, f, m);
-                tmem_wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar(kWReady + T));
+                const uint32_t ready = bar(kWReady + 2 * T);
+                l += plain ? weights<FMT, false>(tS, ks, f, m, ready) : weights<FMT, true>(tS, ks, f, m, ready);
                 begun = true;
                 ++n_s;
             }
@@ -788,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         break;
                     tc::fence_proxy_async_smem();          // the copies that were waited for
                     const bool values = with_v && act(t - 1);
-                    if (values && !wait(kWReady + T, w_phase))
+                    if (values && !wait(kWReady + 2 * T, w_phase))
                         break;
                     // A's round, then B's, by turns: A's first needs no leave, B's n-th and A's
                     // next have the other's
@@ -797,12 +802,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     ++turn;
                     tc::fence_after_sync();
                     if (values) {
-                        w_phase ^= 1;
                         const uint64_t v = v_desc + v_slot * kTile16;
                         mma_tmem_a(tO, tS, v, ipv, started);
 #pragma unroll
-                        for (int i = 1; i < kKeys / 16; ++i)
+                        for (int i = 1; i < kKeys / 32; ++i)
                             mma_tmem_a(tO, tS + 8 * i, v + 128 * i, ipv, 1);
+                        if (!wait(kWReady + 2 * T + 1, w_phase))
+                            break;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int i = kKeys / 32; i < kKeys / 16; ++i)
+                            mma_tmem_a(tO, tS + 8 * i, v + 128 * i, ipv, 1);
+                        w_phase ^= 1;
                         started = 1;
                     }
                     if (with_s && act(t)) {
