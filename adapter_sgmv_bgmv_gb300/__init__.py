@@ -10,7 +10,6 @@ without the built library raises: there is no other implementation.
 from __future__ import annotations
 
 import ctypes
-import math
 import weakref
 
 import numpy as np
@@ -449,6 +448,7 @@ def lora_page_in(ctx: Context, table: AdapterTable, adapter: int, host_a: torch.
                            _stream(stream, ctx.device)), ctx)
 
 
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _KV_FORMATS = {torch.bfloat16: 0, torch.int8: 1, torch.float8_e4m3fn: 2}
 
 
@@ -542,19 +542,32 @@ class KvBatch:
 def _head_rows(t: torch.Tensor, what: str, head_dim: int):
     """(pointer, row stride, rows, heads) of bf16 rows [n, heads, head_dim] (the heads one
     after another) or [n, heads * head_dim]."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{what} must be a CUDA tensor")
-    st, sh = t.stride(), t.shape
-    if len(sh) == 3:
-        ok = sh[2] == head_dim and st[2] == 1 and (sh[1] == 1 or st[1] == head_dim)
-        heads = sh[1]
-    else:
-        ok = len(sh) == 2 and st[1] == 1 and sh[1] % head_dim == 0
-        heads = sh[1] // head_dim if ok else 0
-    if not ok or t.element_size() != 2:
+    try:
+        sh, st = t.shape, t.stride()
+        if len(sh) == 3:
+            n, heads, width = sh
+            ok = width == head_dim and st[2] == 1 and (heads == 1 or st[1] == head_dim)
+        else:
+            n, width = sh
+            heads = width // head_dim
+            ok = st[1] == 1 and heads * head_dim == width
+        ok = ok and t.is_cuda and t.element_size() == 2
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{what} must be a CUDA tensor")
         raise ValueError(f"{what} must be bf16 [n, heads, {head_dim}] or [n, heads * {head_dim}] rows")
     # the stride of a single row says nothing
-    return t.data_ptr(), st[0] if sh[0] > 1 else heads * head_dim, sh[0], heads
+    return t.data_ptr(), st[0] if n > 1 else heads * head_dim, n, heads
+
+
+def _raw_stream(stream, ctx: Context):
+    """_stream for the calls of a decode loop: the current stream's handle without a
+    Stream object around it."""
+    if stream is None and _current_raw_stream is not None and ctx.device is not None:
+        return _current_raw_stream(ctx.device.index or 0)
+    return _stream(stream, ctx.device)
 
 
 def _kv_rows(ctx, cache, batch, k, v, stream, fn):
@@ -562,7 +575,7 @@ def _kv_rows(ctx, cache, batch, k, v, stream, fn):
     pv, ldv, nv, hv = _head_rows(v, "v", cache.head_dim)
     if nv != n or hk != cache.n_heads or hv != cache.n_heads:
         raise ValueError("k and v must have one row a token and the cache's heads")
-    rc = fn(ctx.handle, cache.handle, batch._ref, n, pk, ldk, pv, ldv, _stream(stream, ctx.device))
+    rc = fn(ctx.handle, cache.handle, batch._ref, n, pk, ldk, pv, ldv, _raw_stream(stream, ctx))
     if rc:
         _check(rc, ctx)
 
@@ -591,9 +604,9 @@ def lora_attention(ctx: Context, cache: KvCache, batch: KvBatch, q: torch.Tensor
     if no != n or ho != hq:
         raise ValueError("out must have the shape of q")
     if scale is None:
-        scale = 1.0 / math.sqrt(cache.head_dim)
+        scale = cache.head_dim ** -0.5
     rc = _L.lora_attention(ctx.handle, cache.handle, batch._ref, n, pq, ldq, hq, scale, window, sinks,
-                           po, ldo, _stream(stream, ctx.device))
+                           po, ldo, _raw_stream(stream, ctx))
     if rc:
         _check(rc, ctx)
 

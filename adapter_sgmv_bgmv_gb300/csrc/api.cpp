@@ -1974,6 +1974,9 @@ int lora_sync_status(lora_ctx *ctx, void *stream)
     CUDA_TRY(ctx, cudaMemcpy(&word, ctx->d_status, sizeof word, cudaMemcpyDeviceToHost));
     if (word != 0) {
         CUDA_TRY(ctx, cudaMemset(ctx->d_status, 0, sizeof word));
+        // an attention that gave up may have left arrivals behind
+        if (ctx->attn && word >= kDevTimeoutLoad && word <= kDevTimeoutPipe)
+            CUDA_TRY(ctx, cudaMemset(ctx->attn, 0, ctx->attn_bytes));
         return word == kDevBadId ? LORA_E_ADAPTER : word == kDevBadBatch ? LORA_E_INVAL
                : word == kDevBadPage ? LORA_E_PAGE : LORA_E_TIMEOUT;
     }

@@ -49,6 +49,15 @@ __device__ __forceinline__ int row_tiles(int n_new, int group, int rows)
 // the host.  A piece [x0, x1) holds the tiles [x0 - at - OV, x1 - at - OV) of the unit at
 // `at`, as far as it has them.  Only sequences with min_rows <= rows < max_rows (rows =
 // new tokens * group) take part: the rest are another kernel's.
+static __device__ __noinline__ int64_t wide_quotient(int64_t a, int64_t b) { return a / b; }
+
+// a / b for a >= 0, b > 0; most of a launch's instructions run once, and a 64-bit division
+// is a hundred of them to fetch.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    return ((a | b) >> 31) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : wide_quotient(a, b);
+}
+
 struct Unit {
     int s, r, h;              // sequence, row tile, key head
     SeqInfo q;
@@ -76,6 +85,7 @@ struct Split {
             return 0;
         int64_t n = 0;
         const int tiles = row_tiles(q.n_new, p.group, ROWS);
+#pragma unroll 1
         for (int r = 0; r < tiles; ++r)
             n += span_of<ROWS, TOK>(q, r, p.group, p.window, p.sinks).n + OV;
         return n * p.kv.heads;
@@ -116,50 +126,57 @@ struct Split {
                                 int64_t &total)
     {
         const int tid = threadIdx.x;
-        const int64_t c0 = cost(p, tid);        // the only pass's, up to THREADS sequences
-        const int64_t upto0 = scan<THREADS>(c0, sums, total);
-        for (int base = THREADS; base < p.b.n_seqs; base += THREADS) {
-            int64_t t;
-            scan<THREADS>(cost(p, base + tid), sums, t);
-            total += t;
-        }
-        const int64_t workers = int64_t(gridDim.x) * N;
-        piece = (total + workers - 1) / workers;
-        const int64_t x0 = piece * N * blockIdx.x;
-        if (x0 >= total)
-            return;
-        int64_t before = 0;
-        for (int base = 0; base < p.b.n_seqs; base += THREADS) {
-            int64_t t = 0, c = c0, upto = upto0;
-            if (p.b.n_seqs > THREADS) {
-                c = base ? cost(p, base + tid) : c0;
-                upto = before + scan<THREADS>(c, sums, t);
-            }
+        // Once over the sequences for the total, once more for the units (without a second
+        // look where one round of the block's threads has all of them).
+        int64_t c = 0, upto = 0, x0 = 0;
+        total = 0;
 #pragma unroll 1
-            for (int i = 0; i < N; ++i) {
-                const int64_t x = x0 + i * piece;
-                if (upto > x && upto - c <= x) {
-                    Cursor u;
-                    u.s = base + tid;
-                    u.q = seq_info(p.b, u.s, nullptr);
-                    u.at = upto - c;
-                    u.r = 0;
-                    while (true) {
-                        u.span = span_of<ROWS, TOK>(u.q, u.r, p.group, p.window, p.sinks);
-                        const int64_t w = int64_t(u.span.n + OV) * p.kv.heads;
-                        if (u.at + w > x)
-                            break;
-                        u.at += w;
-                        ++u.r;
-                    }
-                    u.h = int((x - u.at) / (u.span.n + OV));
-                    u.at += int64_t(u.h) * (u.span.n + OV);
-                    found[i] = u;
+        for (int pass = 0; pass < 2; ++pass) {
+            int64_t before = 0;
+#pragma unroll 1
+            for (int base = 0; base < p.b.n_seqs; base += THREADS) {
+                int64_t t = 0;
+                if (pass == 0 || p.b.n_seqs > THREADS) {
+                    c = cost(p, base + tid);
+                    upto = before + scan<THREADS>(c, sums, t);
+                    before += t;
                 }
+                if (pass == 0)
+                    continue;
+#pragma unroll 1
+                for (int i = 0; i < N; ++i) {
+                    const int64_t x = x0 + i * piece;
+                    if (upto > x && upto - c <= x) {
+                        Cursor u;
+                        u.s = base + tid;
+                        u.q = seq_info(p.b, u.s, nullptr);
+                        u.at = upto - c;
+                        u.r = 0;
+#pragma unroll 1
+                        while (true) {
+                            u.span = span_of<ROWS, TOK>(u.q, u.r, p.group, p.window, p.sinks);
+                            const int64_t w = int64_t(u.span.n + OV) * p.kv.heads;
+                            if (u.at + w > x)
+                                break;
+                            u.at += w;
+                            ++u.r;
+                        }
+                        u.h = int(quotient(x - u.at, u.span.n + OV));
+                        u.at += int64_t(u.h) * (u.span.n + OV);
+                        found[i] = u;
+                    }
+                }
+                if (p.b.n_seqs > THREADS && before >= x0 + N * piece)
+                    break;
             }
-            before += t;
-            if (before >= x0 + N * piece)
-                break;
+            if (pass == 0) {
+                total = before;
+                const int64_t workers = int64_t(gridDim.x) * N;
+                piece = quotient(total + workers - 1, workers);
+                x0 = piece * N * blockIdx.x;
+                if (x0 >= total)
+                    return;
+            }
         }
         __syncthreads();
     }
@@ -280,7 +297,7 @@ __device__ __forceinline__ void join(int n, O &&o, ML &&ml, float acc[DIM / 32],
 #pragma unroll
     for (int e = 0; e < N; ++e)
         acc[e] = 0.f;
-#pragma unroll 8
+#pragma unroll 2
     for (int i = 0; i < n; ++i) {
         const float2 t = ml(i);
         const float a = exp2_fast(t.x - ref);

@@ -240,10 +240,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
             tc::cp_async_commit();
         };
 
-        int pid[ST];
-#pragma unroll
-        for (int i = 0; i < ST; ++i)
-            pid[i] = page_at(t0 + i);
+        int page_next = page_at(t0);
 
         // The queries of rows 8r + g, as the products want them, and the positions of this
         // thread's rows of the scores, 8r + 2c and 8r + 2c + 1.
@@ -275,11 +272,6 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
                 }
             }
         }
-#pragma unroll
-        for (int i = 0; i < ST - 1; ++i)
-            issue(t0 + i, pid[i]);
-        int page_next = pid[ST - 1];
-
         float o[DIM / 16][NR][4], m[NR][2], l[NR][2];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -290,13 +282,17 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
                 o[i][r][0] = o[i][r][1] = o[i][r][2] = o[i][r][3] = 0.f;
         }
 
-        for (int t = t0; t < t1; ++t) {
-            tc::cp_async_wait<ST - 2>();
-            __syncwarp();
-            int j0, j1;
-            keys(t, j0, j1);
-            const uint32_t st = ring + uint32_t(t % ST) * S::STAGE;
+        // The first ST - 1 rounds only issue copies: one copy of that code.
+#pragma unroll 1
+        for (int t = t0 - (ST - 1); t < t1; ++t) {
+            int j0 = 0, j1 = 0;
+            if (t >= t0) {
+                tc::cp_async_wait<ST - 2>();
+                __syncwarp();
+                keys(t, j0, j1);
+            }
             if (j0 < j1) {
+                const uint32_t st = ring + uint32_t(t % ST) * S::STAGE;
                 // scores: this thread has keys 16i + g and 16i + g + 8, rows 8r + 2c and + 1
                 float s[MT][NR][4];
 #pragma unroll
@@ -445,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
                 }
             }
             __syncwarp();
-            const int ahead = page_at(t + ST);
+            const int ahead = page_at(t + ST);             // on its way during the next round
             issue(t + ST - 1, page_next);
             page_next = ahead;
         }
@@ -488,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
             }
         __syncwarp();
         if (begins && ends) {
+#pragma unroll 1
             for (int row = 0; row < n_rows; ++row) {
                 float f[N];
 #pragma unroll
@@ -513,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
     __syncthreads();
     int cross[2] = {-1, -1};                               // parts of the runs that came in / go on
     int run = 0;
+#pragma unroll 1
     for (int i = 0; i < 2 * kWarps;) {
         if (!parts[i].there) {
             ++i;
@@ -520,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
         }
         const int64_t at = parts[i].u.at;
         int idx[2 * kWarps], n = 0, j = i;
+#pragma unroll 1
         for (; j < 2 * kWarps; ++j) {
             if (!parts[j].there)
                 continue;
@@ -533,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
         else if (!ends)
             cross[1] = i;
         if (run++ % kWarps == warp) {
+#pragma unroll 1
             for (int row = 0; row < parts[i].m_rows; ++row) {
                 float acc[N], m, l;
                 auto ml = [&](int k) {
@@ -566,11 +566,12 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
         i = j;
     }
     // Units that cross CTAs: the last to arrive adds the CTAs' partials, all its warps.
+#pragma unroll 1
     for (int k = 0; k < 2; ++k) {
         if (cross[k] < 0)
             continue;
         const Part &pt = parts[cross[k]];
-        const int64_t first = (pt.u.at + kUnitCost) / share, final_ = (pt.u.at + kUnitCost + pt.u.span.n - 1) / share;
+        const int64_t first = quotient(pt.u.at + kUnitCost, share), final_ = quotient(pt.u.at + kUnitCost + pt.u.span.n - 1, share);
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -582,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
         if (!last_flag)
             continue;
         __threadfence();
+#pragma unroll 1
         for (int row = warp; row < pt.m_rows; row += kWarps) {
             float acc[N], m, l;
             auto at = [&](int i) { return ((first + i) * 2 + (i == 0)) * kMaxRows + row; };

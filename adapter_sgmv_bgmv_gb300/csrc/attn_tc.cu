@@ -874,8 +874,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     q.n_sink = cursor.span.n_sink, q.lo = cursor.span.lo, q.hi = cursor.span.hi, q.sink = cursor.span.sink;
                     q.begins = t0 == 0;
                     q.ends = t1 == cursor.span.n;
-                    q.first = int((cursor.at + kUnitCost) / piece);
-                    q.last = int((cursor.at + kUnitCost + cursor.span.n - 1) / piece);
+                    q.first = int(quotient(cursor.at + kUnitCost, piece));
+                    q.last = int(quotient(cursor.at + kUnitCost + cursor.span.n - 1, piece));
                     for (int T = 0; T < 2; ++T) {
                         q.side[T] = side_of(p, cursor, T);
                         q.act[T] = active(p, cursor, q.side[T]);

@@ -500,9 +500,11 @@ int lora_kv_read(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch, i
  * out are [n][n_heads * head_dim] bf16 with row strides ldq / ldo; n_heads is a
  * multiple of the cache's heads, and query head h reads key head
  * h / (n_heads / cache heads).  A row without a position gets zeros.  Positions a row
- * does not see never reach its result, whatever they hold.  out may not overlap q.
+ * does not see never reach its result, whatever they hold.  out may not overlap q.  (A
+ * delta call right behind, with `out` as its x, must run without LORA_OPT_EARLY_INPUT,
+ * which reads x ahead of the kernel before.)
  * Scores, weights' sums and outputs are kept in fp32.  For the product with v, weights
- * are taken as two bf16 terms (about 16 bits) for sequences of at most 16 rows
+ * are taken as two bf16 terms (about 16 bits) for sequences of at most 32 rows
  * (n_new * query heads per key head), and rounded to bf16 for longer ones. */
 int lora_attention(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch, int64_t n,
                    const void *q, int64_t ldq, int n_heads, float scale, int window,
