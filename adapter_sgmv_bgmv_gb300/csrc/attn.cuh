@@ -119,8 +119,9 @@ struct Split {
     }
 
     // The pieces of this CTA's N workers: worker i of CTA c has [(c * N + i) * piece, + piece)
-    // cut at `total`; found[i] is the unit that holds its start, where that is before
-    // `total`.  Every thread of the block calls it.
+    // cut at `total`; found[i].s is the sequence that holds its start and found[i].at where
+    // that sequence begins, where the start is before `total`.  Every thread of the block
+    // calls it, then locate() each worker.
     template <int THREADS, int N>
     static __device__ void find(const AttnParams &p, int64_t *sums, Cursor *found, int64_t &piece,
                                 int64_t &total)
@@ -147,23 +148,8 @@ struct Split {
                 for (int i = 0; i < N; ++i) {
                     const int64_t x = x0 + i * piece;
                     if (upto > x && upto - c <= x) {
-                        Cursor u;
-                        u.s = base + tid;
-                        u.q = seq_info(p.b, u.s, nullptr);
-                        u.at = upto - c;
-                        u.r = 0;
-#pragma unroll 1
-                        while (true) {
-                            u.span = span_of<ROWS, TOK>(u.q, u.r, p.group, p.window, p.sinks);
-                            const int64_t w = int64_t(u.span.n + OV) * p.kv.heads;
-                            if (u.at + w > x)
-                                break;
-                            u.at += w;
-                            ++u.r;
-                        }
-                        u.h = int(quotient(x - u.at, u.span.n + OV));
-                        u.at += int64_t(u.h) * (u.span.n + OV);
-                        found[i] = u;
+                        found[i].s = base + tid;
+                        found[i].at = upto - c;
                     }
                 }
                 if (p.b.n_seqs > THREADS && before >= x0 + N * piece)
@@ -179,6 +165,24 @@ struct Split {
             }
         }
         __syncthreads();
+    }
+
+    // From the sequence that holds x to its unit that does.
+    static __device__ __forceinline__ void locate(const AttnParams &p, int64_t x, Cursor &u)
+    {
+        u.q = seq_info(p.b, u.s, nullptr);
+        u.r = 0;
+#pragma unroll 1
+        while (true) {
+            u.span = span_of<ROWS, TOK>(u.q, u.r, p.group, p.window, p.sinks);
+            const int64_t w = int64_t(u.span.n + OV) * p.kv.heads;
+            if (u.at + w > x)
+                break;
+            u.at += w;
+            ++u.r;
+        }
+        u.h = int(quotient(x - u.at, u.span.n + OV));
+        u.at += int64_t(u.h) * (u.span.n + OV);
     }
 
     // The unit after `u` (the caller knows that there is one).
@@ -281,7 +285,7 @@ __device__ __noinline__ void careful_row(const AttnParams &p, const SeqInfo &s, 
 
 // Adds `n` partials (the i-th's row at o(i), its maximum and sum ml(i)) of one row in order;
 // a whole warp, lane l the DIM / 32 elements from l * DIM / 32.
-template <int DIM, typename O, typename ML>
+template <int DIM, int UNROLL, typename O, typename ML>
 __device__ __forceinline__ void join(int n, O &&o, ML &&ml, float acc[DIM / 32], float &m, float &l)
 {
     constexpr int N = DIM / 32;
@@ -297,7 +301,7 @@ __device__ __forceinline__ void join(int n, O &&o, ML &&ml, float acc[DIM / 32],
 #pragma unroll
     for (int e = 0; e < N; ++e)
         acc[e] = 0.f;
-#pragma unroll 2
+#pragma unroll UNROLL
     for (int i = 0; i < n; ++i) {
         const float2 t = ml(i);
         const float a = exp2_fast(t.x - ref);

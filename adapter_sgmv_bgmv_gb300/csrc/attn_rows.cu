@@ -172,8 +172,11 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
     __syncwarp();
 
     Cursor u;
-    if (x < x1)
-        u = found[warp];
+    if (x < x1) {
+        u.s = found[warp].s;
+        u.at = found[warp].at;
+        Cut::locate(p, x, u);
+    }
     while (x < x1) {
         const int64_t first = u.at + kUnitCost, end = first + u.span.n;
         const int t0 = int(max(x - first, int64_t(0)));
@@ -297,9 +300,12 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
                 float s[MT][NR][4];
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
+                    float s2[NR][4];                       // every other step's: half the chain
 #pragma unroll
                     for (int r = 0; r < NR; ++r)
-                        s[i][r][0] = s[i][r][1] = s[i][r][2] = s[i][r][3] = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[i][r][e] = s2[r][e] = 0.f;
                     const uint32_t row = i * 16 + (lane & 15);
                     if (FMT == kKvBf16) {
 #pragma unroll
@@ -308,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
                             ldsm4(st + cell_at<RB>(row, 2 * k + (lane >> 4)), f);
 #pragma unroll
                             for (int r = 0; r < NR; ++r)
-                                mma(s[i][r], f, qf[r][k][0], qf[r][k][1]);
+                                mma(k & 1 ? s2[r] : s[i][r], f, qf[r][k][0], qf[r][k][1]);
                         }
                     } else {
 #pragma unroll
@@ -322,10 +328,15 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
 #pragma unroll
                             for (int r = 0; r < NR; ++r) {
                                 mma(s[i][r], a[0], qf[r][k][0], qf[r][k][1]);
-                                mma(s[i][r], a[1], qf[r][k + 1][0], qf[r][k + 1][1]);
+                                mma(s2[r], a[1], qf[r][k + 1][0], qf[r][k + 1][1]);
                             }
                         }
                     }
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[i][r][e] += s2[r][e];
                 }
                 // scale, mask, running maximum
                 const float *sc = reinterpret_cast<const float *>(mine + (t % ST) * S::STAGE + 2 * BT * RB);
@@ -550,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
                         load_vec<N>(v, p.part.warp_o + ((int64_t(blockIdx.x) * kWarps + w) * kMaxRows + row) * DIM + lane * N);
                     }
                 };
-                join<DIM>(n, o, ml, acc, m, l);
+                join<DIM, 2>(n, o, ml, acc, m, l);
                 if (begins && ends) {
                     finish_row<kRows, DIM, FMT>(p, parts[i].u, row, acc, l);
                 } else {
@@ -587,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
         for (int row = warp; row < pt.m_rows; row += kWarps) {
             float acc[N], m, l;
             auto at = [&](int i) { return ((first + i) * 2 + (i == 0)) * kMaxRows + row; };
-            join<DIM>(int(final_ - first) + 1,
+            join<DIM, 8>(int(final_ - first) + 1,
                       [&](int i, float *v) { load_vec<N>(v, p.part.cta_o + at(i) * DIM + lane * N); },
                       [&](int i) { return __ldcg(&p.part.cta_ml[at(i)]); }, acc, m, l);
             finish_row<kRows, DIM, FMT>(p, pt.u, row, acc, l);

@@ -325,7 +325,7 @@ __device__ __noinline__ void join_unit(const AttnParams &p, const Part &u)
     for (int row = warp; row < n_rows; row += 8) {
         float acc[N], m, l;
         auto at = [&](int i) { return int64_t((u.first + i) * 2 + (i == 0)) * kRows + row; };
-        join<DIM>(u.last - u.first + 1, [&](int i, float *v) { load_vec<N>(v, p.part.cta_o + at(i) * DIM + lane * N); },
+        join<DIM, 2>(u.last - u.first + 1, [&](int i, float *v) { load_vec<N>(v, p.part.cta_o + at(i) * DIM + lane * N); },
                   [&](int i) { return __ldcg(&p.part.cta_ml[at(i)]); }, acc, m, l);
         finish_row<kRows, DIM, FMT>(p, u, row, acc, l);
     }
@@ -848,6 +848,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         if (warp == 14 && lane == 0) {
             int64_t x = piece * blockIdx.x;
             const int64_t x1 = min(x + piece, total);
+            if (x < x1)
+                Cut::locate(p, x, cursor);
             bool more = true;
             while (more) {
                 int t0 = 0, t1 = 0;
