@@ -891,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         }
         __syncwarp();
     }
-    tc::cp_async_wait_all();
+    asm volatile("cp.async.wait_all;" ::: "memory");
     // Every product has ended: the weights' warps waited for each tile's last.  Where the
     // roles gave up, those under way get the time that they can take at most.
     tc::fence_before_sync();
