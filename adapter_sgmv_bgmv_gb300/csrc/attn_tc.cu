@@ -13,15 +13,15 @@
 //                    reference is the running maximum, but it is moved (and O rescaled in
 //                    TMEM) only when the maximum passes it by 2^8: weights stay below 2^8,
 //                    and the sums are divided out at the end all the same.
-//   warps 8-11       loads: cells of the pages to 128-byte-swizzled tiles, each row with its
+//   then 4 or 8      loads: cells of the pages to 128-byte-swizzled tiles, each row with its
 //                    own address (any page size, any strides); bf16 by cp.async, 8-bit codes
 //                    through registers, where they become bf16 (exact).
-//   warps 12, 13     one thread each issues the products of tile A / B: an issue holds its
+//   then two         one thread each issues the products of tile A / B: an issue holds its
 //                    thread until the tensor cores have taken it, so with one thread for both
 //                    they stood still while it waited for barriers (2 400 of 5 400 cycles a
 //                    key tile).  The two take turns: left to themselves the tiles fall into
 //                    step, both at their weights and then both at their products.
-//   warp 14          one thread goes along the CTA's piece ahead of the others and leaves
+//   then one         one thread goes along the CTA's piece ahead of the others and leaves
 //                    them what they need of each unit (the only copy of that code: see below
 //                    on code size).
 //
@@ -45,18 +45,23 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 512;
 constexpr int kM = 128;              // rows of a row tile
 constexpr int kRows = 2 * kM;
 constexpr int kKeys = 128;           // keys of a key tile
 constexpr int kUnitCost = 2;         // a unit's start and end, in key tiles
 constexpr int kScaleSlots = 4;
-// Registers, of 512 x 128 at launch: the warps of the loads and of the products (three of
-// which are there for their registers alone) give some to the weights.
+// Warps: 8 of the weights, LOADS of the loads (8-bit codes pass through their registers:
+// twice as many), two of the products, one of the parts, one there for its registers, of
+// which these two kinds give some to the weights.
 template <int FMT>
-struct Regs {
-    static constexpr int more = 152, load = 120, few = 88;
-    static_assert(2 * more + load + few == 512, "the registers of the block");
+struct Crew {
+    static constexpr int LOADS = FMT == kKvBf16 ? 4 : 8;
+    static constexpr int ROWS = 128 / LOADS;             // of a tile, for a load warp
+    static constexpr int WARPS = 12 + LOADS;
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int launch = FMT == kKvBf16 ? 128 : 96;
+    static constexpr int more = FMT == kKvBf16 ? 152 : 144, load = FMT == kKvBf16 ? 120 : 64, few = FMT == kKvBf16 ? 88 : 64;
+    static_assert(8 * more + LOADS * load + 4 * few == WARPS * launch, "the registers of the block");
 };
 
 template <int DIM>
@@ -332,16 +337,17 @@ __device__ __noinline__ void join_unit(const AttnParams &p, const Part &u)
 }
 
 template <int DIM, int FMT>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(Crew<FMT>::THREADS, 1) k_attn_tc(const __grid_constant__ AttnParams p)
 {
     using S = TcShape<DIM>;
     using Cut = Split<kRows, kKeys, kUnitCost>;
     constexpr int ST = S::STAGES, N = DIM / 32;
+    constexpr int kThreads = Crew<FMT>::THREADS, LW = Crew<FMT>::LOADS, LR = Crew<FMT>::ROWS;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), sm = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (sm - raw);
     __shared__ int64_t sums[kThreads / 32];
-    __shared__ Cursor cursor;                              // warp 14's
+    __shared__ Cursor cursor;                              // the parts' warp's
     __shared__ Part parts[kParts];
     __shared__ uint32_t poison[kScaleSlots * 4];           // per slot: keys whose value's scale is not finite
     __shared__ uint32_t tmem_slot;
@@ -354,11 +360,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             // the load warps' lanes as their copies end, or the warps as they have stored
-            mbar_init(bar(kFull + i), FMT == kKvBf16 ? 128 : 4);
+            mbar_init(bar(kFull + i), FMT == kKvBf16 ? 32 * LW : LW);
             mbar_init(bar(kEmpty + i), 2);         // a commit of each row tile's products
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kQFull + i), 128);
+            mbar_init(bar(kQFull + i), 32 * LW);
             mbar_init(bar(kQEmpty + i), 1);
             mbar_init(bar(kSFull + i), 1);
             mbar_init(bar(kWReady + 2 * i), 4);    // the warps of one row tile
@@ -367,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         }
         for (int i = 0; i < kParts; ++i) {
             mbar_init(bar(kPartFull + i), 1);
-            mbar_init(bar(kPartEmpty + i), 14);    // every warp that reads the parts
+            mbar_init(bar(kPartEmpty + i), 10 + LW);   // every warp that reads the parts
         }
         mbar_init(bar(kJoin), 8);
         mbar_init(bar(kTurn + 0), 1);
@@ -375,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         fence_mbar_init();
         dead_flag = 0;
     }
-    if (warp == 12)
+    if (warp == 8 + LW)
         tc::tmem_alloc(smem_u32(&tmem_slot), 512);
     tc::fence_before_sync();
     __syncthreads();
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
 
     if (warp < 8) {
         // ------------------------------------------------------------ weights
-        setmaxnreg_inc<Regs<FMT>::more>();
+        setmaxnreg_inc<Crew<FMT>::more>();
         const int T = warp >> 2, row = tid & 127;
         const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + T * 128u, tO = tmem + lanes + 256u + T * uint32_t(DIM);
@@ -578,10 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             tc::fence_before_sync();
             part_done();
         }
-    } else if (warp < 12) {
+    } else if (warp < 8 + LW) {
         // ------------------------------------------------------------ loads
-        setmaxnreg_dec<Regs<FMT>::load>();
-        const int lw = warp - 8;                           // this warp's 32 keys (or rows) of a tile
+        setmaxnreg_dec<Crew<FMT>::load>();
+        const int lw = warp - 8;                           // this warp has LR keys (or rows) of a tile,
+        const int mine = lw * LR + lane;                   // this lane one of them (of the lanes below LR)
         bool alive = true;
         uint32_t entry = 0, slot = 0, phase = 1;           // ring entries: keys 2j, values 2j + 1
         int tile_no = 0;
@@ -609,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             if (!pt)
                 return INT_MIN;
             const bool sink = t < pt->n_sink;
-            const int j = (sink ? t * kKeys : pt->lo + (t - pt->n_sink) * kKeys) + lw * 32 + lane;
-            return j < (sink ? pt->sink : pt->hi) ? p.b.pages[int64_t(pt->s) * p.b.ld_pages + page_of(kv, j)] : INT_MIN;
+            const int j = (sink ? t * kKeys : pt->lo + (t - pt->n_sink) * kKeys) + mine;
+            return lane < LR && j < (sink ? pt->sink : pt->hi) ? p.b.pages[int64_t(pt->s) * p.b.ld_pages + page_of(kv, j)] : INT_MIN;
         };
         auto place = [&](int page, int64_t &at, int64_t &s_at) {
             at = -1;
@@ -621,14 +628,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 raise_status(p.status, kDevBadPage);
                 return;
             }
-            const int j = (t < pt->n_sink ? t * kKeys : pt->lo + (t - pt->n_sink) * kKeys) + lw * 32 + lane;
+            const int j = (t < pt->n_sink ? t * kKeys : pt->lo + (t - pt->n_sink) * kKeys) + mine;
             const int cell = j - page_of(kv, j) * kv.page_size;
             at = page * kv.page_stride + cell * kv.cell_stride + pt->h * kv.head_stride;
             s_at = page * kv.s_page + cell * kv.s_cell + pt->h * kv.s_head;
         };
         auto q_place = [&](int T) -> int64_t {             // this lane's row of the queries, bytes
-            const int row = T * kM + lw * 32 + lane;
-            if (pt->r * kRows + row >= pt->q.n_new * p.group)
+            const int row = T * kM + mine;
+            if (lane >= LR || pt->r * kRows + row >= pt->q.n_new * p.group)
                 return -1;
             int64_t token, col;
             int pos;
@@ -640,8 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         // reads them by the tensor cores makes them visible to those.
         auto copy_rows = [&](uint32_t dst, const uint8_t *src, int64_t at, uint32_t done) {
 #pragma unroll 4
-            for (int i = 0; i < CH; ++i) {
-                const int rr = i * RPI + lane / CH, ch = lane % CH, row = lw * 32 + rr;
+            for (int i = 0; i < LR / RPI; ++i) {
+                const int rr = i * RPI + lane / CH, ch = lane % CH, row = lw * LR + rr;
                 const int64_t a = __shfl_sync(0xffffffffu, (long long)at, rr);
                 tc::cp_async16(dst + (ch / 8) * S::HALF + tc::sw128(row, ch % 8), src + (a < 0 ? 0 : a + ch * 16), a < 0 ? 0u : 16u);
             }
@@ -677,18 +684,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 }
             }
         } else {
-            constexpr int C8 = DIM / 16, R8 = 32 / C8;     // 16-byte chunks of a row of codes
-            auto fetch = [&](uint4 x[C8], const uint8_t *src, int64_t at) {
+            constexpr int C8 = DIM / 16, R8 = 32 / C8;     // 16-byte chunks of a row of codes, rows an instruction
+            constexpr int XN = LR / R8;
+            auto fetch = [&](uint4 x[XN], const uint8_t *src, int64_t at) {
 #pragma unroll
-                for (int i = 0; i < C8; ++i) {
+                for (int i = 0; i < XN; ++i) {
                     const int64_t a = __shfl_sync(0xffffffffu, (long long)at, i * R8 + lane / C8);
                     x[i] = a < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(src + a + (lane % C8) * 16);
                 }
             };
-            auto store = [&](const uint4 x[C8]) {          // into the ring's next slot
+            auto store = [&](const uint4 x[XN]) {          // into the ring's next slot
 #pragma unroll
-                for (int i = 0; i < C8; ++i) {
-                    const int row = lw * 32 + i * R8 + lane / C8, ch = 2 * (lane % C8);
+                for (int i = 0; i < XN; ++i) {
+                    const int row = lw * LR + i * R8 + lane / C8, ch = 2 * (lane % C8);
                     const uint2 a = widen4_unit<FMT>(x[i].x), b = widen4_unit<FMT>(x[i].y), c = widen4_unit<FMT>(x[i].z), d = widen4_unit<FMT>(x[i].w);
                     uint8_t *base = smem + S::RING + slot * S::TILE + (ch / 8) * S::HALF;
                     *reinterpret_cast<uint4 *>(base + tc::sw128(row, ch % 8)) = make_uint4(a.x, a.y, b.x, b.y);
@@ -702,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             };
             const float sl = p.scale * 1.4426950408889634f;
             // x holds the tile that is stored next, y the one after it on its way
-            uint4 x[C8], y[C8];
+            uint4 x[XN], y[XN];
             float ks = 0.f, vs = 0.f;
             auto begin = [&]() {
                 place(page, at, s_at);
@@ -724,13 +732,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 page = page_id();
                 if (!wait_slot())
                     break;
-                float *sc = reinterpret_cast<float *>(smem + S::SCALES) + (tile_no % kScaleSlots) * 2 * kKeys + lw * 32 + lane;
+                float *sc = reinterpret_cast<float *>(smem + S::SCALES) + (tile_no % kScaleSlots) * 2 * kKeys + mine;
                 const bool fine = fabsf(vs) < INFINITY;
-                sc[0] = ks;
-                sc[kKeys] = fine ? vs : 0.f;
+                if (lane < LR) {
+                    sc[0] = ks;
+                    sc[kKeys] = fine ? vs : 0.f;
+                }
                 const unsigned bad = __ballot_sync(0xffffffffu, !fine);
                 if (lane == 0)
-                    poison[(tile_no % kScaleSlots) * 4 + lw] = bad;
+                    reinterpret_cast<uint16_t *>(poison)[(tile_no % kScaleSlots) * 8 + lw] = uint16_t(bad);
                 store(x);
                 if (fresh) {
 #pragma unroll 1
@@ -748,10 +758,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 ++tile_no;
             }
         }
-    } else if (warp < 14) {
+    } else if (warp < 10 + LW) {
         // ------------------------------------------------------------ products
-        setmaxnreg_dec<Regs<FMT>::few>();
-        const int T = warp - 12;
+        setmaxnreg_dec<Crew<FMT>::few>();
+        const int T = warp - 8 - LW;
         if (lane == 0) {
             constexpr uint32_t iqk = tc::idesc_bf16(kM, kKeys, 0, 0), ipv = tc::idesc_bf16(kM, DIM, 0, 1);
             constexpr uint32_t kTile16 = S::TILE / 16, kHalf16 = S::HALF / 16;   // descriptor units
@@ -844,8 +854,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         __syncwarp();
     } else {
         // ------------------------------------------------------------ parts
-        setmaxnreg_dec<Regs<FMT>::few>();
-        if (warp == 14 && lane == 0) {
+        setmaxnreg_dec<Crew<FMT>::few>();
+        if (warp == 10 + LW && lane == 0) {
             int64_t x = piece * blockIdx.x;
             const int64_t x1 = min(x + piece, total);
             if (x < x1)
@@ -896,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     // roles gave up, those under way get the time that they can take at most.
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 8 + LW) {
         if (dead_flag) {
             const uint64_t t = globaltimer_ns();
             while (globaltimer_ns() - t < 1000000ull) {
@@ -921,7 +931,7 @@ cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream)
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(sms));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Crew<FMT>::THREADS);
     cfg.dynamicSmemBytes = TcShape<DIM>::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
