@@ -75,8 +75,9 @@ struct Split {
         return rows >= p.min_rows && rows < p.max_rows;
     }
 
-    // Sequence s's length on the line.
-    static __device__ int64_t cost(const AttnParams &p, int s)
+    // Sequence s's length on the line.  `longest` (in shared memory, or null) is raised to
+    // the mean length of its units.
+    static __device__ int64_t cost(const AttnParams &p, int s, int *longest)
     {
         if (s >= p.b.n_seqs)
             return 0;
@@ -88,6 +89,8 @@ struct Split {
 #pragma unroll 1
         for (int r = 0; r < tiles; ++r)
             n += span_of<ROWS, TOK>(q, r, p.group, p.window, p.sinks).n + OV;
+        if (longest && tiles)
+            atomicMax(longest, int(quotient(n, tiles)));
         return n * p.kv.heads;
     }
 
@@ -124,7 +127,7 @@ struct Split {
     // calls it, then locate() each worker.
     template <int THREADS, int N>
     static __device__ void find(const AttnParams &p, int64_t *sums, Cursor *found, int64_t &piece,
-                                int64_t &total)
+                                int64_t &total, int *longest = nullptr)
     {
         const int tid = threadIdx.x;
         // Once over the sequences for the total, once more for the units (without a second
@@ -138,7 +141,7 @@ struct Split {
             for (int base = 0; base < p.b.n_seqs; base += THREADS) {
                 int64_t t = 0;
                 if (pass == 0 || p.b.n_seqs > THREADS) {
-                    c = cost(p, base + tid);
+                    c = cost(p, base + tid, longest);
                     upto = before + scan<THREADS>(c, sums, t);
                     before += t;
                 }
@@ -159,6 +162,11 @@ struct Split {
                 total = before;
                 const int64_t workers = int64_t(gridDim.x) * N;
                 piece = quotient(total + workers - 1, workers);
+                // A unit in many parts is soon read but long joined (by one CTA): with k
+                // tiles a part the two take k a + (n / k) rows b, least at k = sqrt(n rows b / a);
+                // a = 2.5 us for a key tile, b = 2.5 ns for a row of a part.
+                if (longest)
+                    piece = max(piece, int64_t(sqrtf(float(*longest) * (ROWS * 1e-3f))));
                 x0 = piece * N * blockIdx.x;
                 if (x0 >= total)
                     return;

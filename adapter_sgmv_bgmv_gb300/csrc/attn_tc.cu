@@ -326,13 +326,52 @@ __device__ __noinline__ void join_unit(const AttnParams &p, const Part &u)
 {
     constexpr int N = DIM / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n_rows = min(kRows, u.q.n_new * p.group - u.r * kRows);
-    for (int row = warp; row < n_rows; row += 8) {
-        float acc[N], m, l;
-        auto at = [&](int i) { return int64_t((u.first + i) * 2 + (i == 0)) * kRows + row; };
-        join<DIM, 2>(u.last - u.first + 1, [&](int i, float *v) { load_vec<N>(v, p.part.cta_o + at(i) * DIM + lane * N); },
-                  [&](int i) { return __ldcg(&p.part.cta_ml[at(i)]); }, acc, m, l);
-        finish_row<kRows, DIM, FMT>(p, u, row, acc, l);
+    const int n_rows = min(kRows, u.q.n_new * p.group - u.r * kRows), n = u.last - u.first + 1;
+    auto at = [&](int i, int row) { return int64_t((u.first + i) * 2 + (i == 0)) * kRows + min(row, n_rows - 1); };
+    // four rows at a time: one by one, the loads' latency was most of a short chunk's time
+    constexpr int B = 4;
+#pragma unroll 1
+    for (int row = warp * B; row < n_rows; row += 8 * B) {
+        float acc[B][N], m[B], l[B];
+#pragma unroll
+        for (int r = 0; r < B; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                acc[r][e] = 0.f;
+        }
+        for (int i = lane; i < n; i += 32)
+#pragma unroll
+            for (int r = 0; r < B; ++r)
+                m[r] = fmaxf(m[r], __ldcg(&p.part.cta_ml[at(i, row + r)]).x);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1)
+#pragma unroll
+            for (int r = 0; r < B; ++r)
+                m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], k));
+#pragma unroll 2
+        for (int i = 0; i < n; ++i) {
+            float2 t[B];
+            float v[B][N];
+#pragma unroll
+            for (int r = 0; r < B; ++r) {
+                t[r] = __ldcg(&p.part.cta_ml[at(i, row + r)]);
+                load_vec<N>(v[r], p.part.cta_o + at(i, row + r) * DIM + lane * N);
+            }
+#pragma unroll
+            for (int r = 0; r < B; ++r) {
+                const float a = exp2_fast(t[r].x - (m[r] == -INFINITY ? 0.f : m[r]));
+                l[r] += t[r].y * a;
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    acc[r][e] = fmaf(a, v[r][e], acc[r][e]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < B; ++r)
+            if (row + r < n_rows)
+                finish_row<kRows, DIM, FMT>(p, u, row + r, acc[r], l[r]);
     }
 }
 
@@ -351,7 +390,7 @@ __global__ void __launch_bounds__(Crew<FMT>::THREADS, 1) k_attn_tc(const __grid_
     __shared__ Part parts[kParts];
     __shared__ uint32_t poison[kScaleSlots * 4];           // per slot: keys whose value's scale is not finite
     __shared__ uint32_t tmem_slot;
-    __shared__ int dead_flag, last_flag;
+    __shared__ int dead_flag, last_flag, longest;
     volatile int *dead = &dead_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const KvView &kv = p.kv;
@@ -380,6 +419,7 @@ __global__ void __launch_bounds__(Crew<FMT>::THREADS, 1) k_attn_tc(const __grid_
         mbar_init(bar(kTurn + 1), 1);
         fence_mbar_init();
         dead_flag = 0;
+        longest = 0;
     }
     if (warp == 8 + LW)
         tc::tmem_alloc(smem_u32(&tmem_slot), 512);
@@ -392,7 +432,7 @@ __global__ void __launch_bounds__(Crew<FMT>::THREADS, 1) k_attn_tc(const __grid_
     grid_dep_launch();
 
     int64_t piece, total;
-    Cut::template find<kThreads, 1>(p, sums, &cursor, piece, total);
+    Cut::template find<kThreads, 1>(p, sums, &cursor, piece, total, &longest);
 
     // The parts in order, for the warps that read them: `part()` waits for the next and is null
     // past the last (or when the block has given up); `part_done()` lets go of it.
