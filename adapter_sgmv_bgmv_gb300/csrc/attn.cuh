@@ -75,8 +75,8 @@ struct Split {
         return rows >= p.min_rows && rows < p.max_rows;
     }
 
-    // Sequence s's length on the line.  `longest` (in shared memory, or null) is raised to
-    // the mean length of its units.
+    // Sequence s's length on the line.  `longest` (in shared memory) is raised to the
+    // mean length of its units.
     static __device__ int64_t cost(const AttnParams &p, int s, int *longest)
     {
         if (s >= p.b.n_seqs)
@@ -89,7 +89,7 @@ struct Split {
 #pragma unroll 1
         for (int r = 0; r < tiles; ++r)
             n += span_of<ROWS, TOK>(q, r, p.group, p.window, p.sinks).n + OV;
-        if (longest && tiles)
+        if (tiles)
             atomicMax(longest, int(quotient(n, tiles)));
         return n * p.kv.heads;
     }
@@ -124,10 +124,10 @@ struct Split {
     // The pieces of this CTA's N workers: worker i of CTA c has [(c * N + i) * piece, + piece)
     // cut at `total`; found[i].s is the sequence that holds its start and found[i].at where
     // that sequence begins, where the start is before `total`.  Every thread of the block
-    // calls it, then locate() each worker.
+    // calls it, then locate() each worker.  `join_pace` is b / (N a) of the kernel (below).
     template <int THREADS, int N>
     static __device__ void find(const AttnParams &p, int64_t *sums, Cursor *found, int64_t &piece,
-                                int64_t &total, int *longest = nullptr)
+                                int64_t &total, int *longest, float join_pace)
     {
         const int tid = threadIdx.x;
         // Once over the sequences for the total, once more for the units (without a second
@@ -162,11 +162,11 @@ struct Split {
                 total = before;
                 const int64_t workers = int64_t(gridDim.x) * N;
                 piece = quotient(total + workers - 1, workers);
-                // A unit in many parts is soon read but long joined (by one CTA): with k
-                // tiles a part the two take k a + (n / k) rows b, least at k = sqrt(n rows b / a);
-                // a = 2.5 us for a key tile, b = 2.5 ns for a row of a part.
-                if (longest)
-                    piece = max(piece, int64_t(sqrtf(float(*longest) * (ROWS * 1e-3f))));
+                // A unit in many parts is soon read but long joined (by one CTA): pieces of k
+                // tiles take k a, and the n / (k N) parts of `rows` rows b each to join; the sum is
+                // least at k = sqrt(n rows b / (N a)).
+                const float rows = float(min(int64_t(ROWS), int64_t(p.b.max_new) * p.group));
+                piece = max(piece, int64_t(sqrtf(float(*longest) * rows * join_pace)));
                 x0 = piece * N * blockIdx.x;
                 if (x0 >= total)
                     return;

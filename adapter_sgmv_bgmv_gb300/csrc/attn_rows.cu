@@ -38,6 +38,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnitCost = 3;   // a unit's start and end, in tiles
 constexpr int kMaxRows = 16;   // of a unit
+// 20 ns for a row of a part (eight parts' loads under way in four warps) to four times
+// 0.6 us for a tile: see Split::find.
+constexpr float kJoinPace = 8e-3f;
 constexpr int kMaxCtas = 2;    // a SM
 
 // NR: groups of 8 query rows of a unit.
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
     __shared__ Cursor found[kWarps];
     __shared__ Part parts[2 * kWarps];
     __shared__ float2 tail_ml[kWarps][kMaxRows];
-    __shared__ int last_flag;
+    __shared__ int last_flag, longest;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, g = lane >> 2;
     const KvView &kv = p.kv;
     const BatchView &b = p.b;
@@ -154,7 +157,10 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
     }
 
     int64_t piece, total;
-    Cut::template find<kThreads, kWarps>(p, sums, found, piece, total);
+    if (threadIdx.x == 0)
+        longest = 0;
+    __syncthreads();
+    Cut::template find<kThreads, kWarps>(p, sums, found, piece, total, &longest, kJoinPace);
     const int64_t share = piece * kWarps;
     if (share * blockIdx.x >= total) {
         if (p.behind)

@@ -50,6 +50,9 @@ constexpr int kRows = 2 * kM;
 constexpr int kKeys = 128;           // keys of a key tile
 constexpr int kUnitCost = 2;         // a unit's start and end, in key tiles
 constexpr int kScaleSlots = 4;
+// 5 ns for a row of a part (loads of four rows of four parts under way in eight warps) to
+// 2.5 us for a key tile: see Split::find.
+constexpr float kJoinPace = 2e-3f;
 // Warps: 8 of the weights, LOADS of the loads (8-bit codes pass through their registers:
 // twice as many), two of the products, one of the parts, one there for its registers, of
 // which these two kinds give some to the weights.
@@ -350,7 +353,7 @@ __device__ __noinline__ void join_unit(const AttnParams &p, const Part &u)
 #pragma unroll
             for (int r = 0; r < B; ++r)
                 m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], k));
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < n; ++i) {
             float2 t[B];
             float v[B][N];
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(Crew<FMT>::THREADS, 1) k_attn_tc(const __grid_
     grid_dep_launch();
 
     int64_t piece, total;
-    Cut::template find<kThreads, 1>(p, sums, &cursor, piece, total, &longest);
+    Cut::template find<kThreads, 1>(p, sums, &cursor, piece, total, &longest, kJoinPace);
 
     // The parts in order, for the warps that read them: `part()` waits for the next and is null
     // past the last (or when the block has given up); `part_done()` lets go of it.
