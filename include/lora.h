@@ -504,7 +504,7 @@ int lora_kv_read(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch, i
  * delta call right behind, with `out` as its x, must run without LORA_OPT_EARLY_INPUT,
  * which reads x ahead of the kernel before.)
  * Scores, weights' sums and outputs are kept in fp32.  For the product with v, weights
- * are taken as two bf16 terms (about 16 bits) for sequences of at most 32 rows
+ * are taken as two bf16 terms (about 16 bits) for sequences of at most 16 rows
  * (n_new * query heads per key head), and rounded to bf16 for longer ones. */
 int lora_attention(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch, int64_t n,
                    const void *q, int64_t ldq, int n_heads, float scale, int window,
