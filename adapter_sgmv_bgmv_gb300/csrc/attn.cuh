@@ -248,42 +248,61 @@ __device__ __noinline__ void careful_row(const AttnParams &p, const SeqInfo &s, 
         qf[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(q)[lane * N + e]);
         o[e] = 0.f;
     }
-    for (int j = 0; j <= pos; ++j) {
-        if (!sees(pos, j, p.window, p.sinks))
-            continue;
-        const int jp = page_of(p.kv, j);
-        const int page = p.b.pages[int64_t(seq) * p.b.ld_pages + jp];
-        const bool there = page >= 0 && page < p.kv.n_pages;
-        const int cell = j - jp * p.kv.page_size;
-        const int64_t at = there ? page * p.kv.page_stride + cell * p.kv.cell_stride + head * p.kv.head_stride : 0;
-        const int64_t sat = there ? page * p.kv.s_page + cell * p.kv.s_cell + head * p.kv.s_head : 0;
-        float kf[N], vf[N], dot = 0.f;
+    constexpr int B = 4;                    // keys under way at once
+#pragma unroll 1
+    for (int j0 = 0; j0 <= pos; j0 += B) {
+        if (p.window && j0 >= p.sinks && j0 <= pos - p.window)
+            j0 = pos - p.window + 1;        // past what the window hides
+        float kf[B][N], vf[B][N], dot[B];
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int d = lane * N + e;
-            float a, b;
-            if (FMT == kKvBf16) {
-                a = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.kv.k + at)[d]);
-                b = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.kv.v + at)[d]);
-            } else if (FMT == kKvInt8) {
-                a = float(reinterpret_cast<const int8_t *>(p.kv.k + at)[d]) * p.kv.k_scale[sat];
-                b = float(reinterpret_cast<const int8_t *>(p.kv.v + at)[d]) * p.kv.v_scale[sat];
-            } else {
-                a = float(reinterpret_cast<const __nv_fp8_e4m3 *>(p.kv.k + at)[d]) * p.kv.k_scale[sat];
-                b = float(reinterpret_cast<const __nv_fp8_e4m3 *>(p.kv.v + at)[d]) * p.kv.v_scale[sat];
+        for (int b = 0; b < B; ++b) {
+            const int j = j0 + b;
+            bool there = j <= pos && sees(pos, j, p.window, p.sinks);
+            const int jp = there ? page_of(p.kv, j) : 0;
+            const int page = there ? p.b.pages[int64_t(seq) * p.b.ld_pages + jp] : -1;
+            there = page >= 0 && page < p.kv.n_pages;
+            const int cell = j - jp * p.kv.page_size;
+            const int64_t at = there ? page * p.kv.page_stride + cell * p.kv.cell_stride + head * p.kv.head_stride : 0;
+            const int64_t sat = there ? page * p.kv.s_page + cell * p.kv.s_cell + head * p.kv.s_head : 0;
+            const float ks = FMT == kKvBf16 ? 1.f : p.kv.k_scale[sat], vs = FMT == kKvBf16 ? 1.f : p.kv.v_scale[sat];
+            dot[b] = 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const int d = lane * N + e;
+                float x, y;
+                if (FMT == kKvBf16) {
+                    x = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.kv.k + at)[d]);
+                    y = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.kv.v + at)[d]);
+                } else if (FMT == kKvInt8) {
+                    x = float(reinterpret_cast<const int8_t *>(p.kv.k + at)[d]) * ks;
+                    y = float(reinterpret_cast<const int8_t *>(p.kv.v + at)[d]) * vs;
+                } else {
+                    x = float(reinterpret_cast<const __nv_fp8_e4m3 *>(p.kv.k + at)[d]) * ks;
+                    y = float(reinterpret_cast<const __nv_fp8_e4m3 *>(p.kv.v + at)[d]) * vs;
+                }
+                kf[b][e] = there ? x : 0.f;
+                vf[b][e] = there ? y : 0.f;
+                dot[b] = fmaf(qf[e], kf[b][e], dot[b]);
             }
-            kf[e] = there ? a : 0.f;
-            vf[e] = there ? b : 0.f;
-            dot = fmaf(qf[e], kf[e], dot);
         }
-        const float sc = warp_sum(dot) * p.scale;
-        const float mn = fmaxf(m, sc), ref = mn == -INFINITY ? 0.f : mn;
-        const float a = expf(m - ref), w = sc == INFINITY ? __int_as_float(0x7fffffff) : expf(sc - ref);
-        m = mn;
-        l = l * a + w;
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-            o[e] = o[e] * a + w * vf[e];
+        for (int b = 0; b < B; ++b)
+            dot[b] = warp_sum(dot[b]);
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (j0 + b > pos || !sees(pos, j0 + b, p.window, p.sinks))
+                continue;
+            const float sc = dot[b] * p.scale;
+            const float mn = fmaxf(m, sc), ref = mn == -INFINITY ? 0.f : mn;
+            const float a = expf(m - ref), w = sc == INFINITY ? __int_as_float(0x7fffffff) : expf(sc - ref);
+            m = mn;
+            l = l * a + w;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                o[e] = o[e] * a + w * vf[b][e];
+        }
+        if (l != l)                         // every element is a NaN from here on
+            break;
     }
     const float inv = l > 0.f ? 1.f / l : l;            // no key: 0; a NaN stays one
 #pragma unroll
