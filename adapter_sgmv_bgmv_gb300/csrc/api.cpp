@@ -174,6 +174,22 @@ int cuda_fail(lora_ctx *ctx, cudaError_t e)
     return LORA_E_CUDA;
 }
 
+// Zero device memory, done when this returns.  A cudaMemset alone returns ahead of its
+// work, which runs on the legacy stream, and non-blocking streams do not wait for that: a
+// kernel on one could run beside it.  A stream of its own does not wait for the caller's
+// work on the legacy stream either.
+cudaError_t zero_now(void *p, size_t bytes)
+{
+    cudaStream_t stream = nullptr;
+    cudaError_t e = cudaStreamCreateWithFlags(&stream, cudaStreamNonBlocking);
+    if (e != cudaSuccess)
+        return e;
+    e = cudaMemsetAsync(p, 0, bytes, stream);
+    const cudaError_t waited = cudaStreamSynchronize(stream);
+    cudaStreamDestroy(stream);
+    return e != cudaSuccess ? e : waited;
+}
+
 #define CUDA_TRY(ctx, expr)                          \
     do {                                             \
         cudaError_t _e = (expr);                     \
@@ -1135,7 +1151,7 @@ int ctx_attn_scratch(lora_ctx *ctx, size_t bytes, uint8_t **out)
             (void)cudaGetLastError();
             return LORA_E_NOMEM;
         }
-        const cudaError_t e = cudaMemset(p, 0, bytes);
+        const cudaError_t e = zero_now(p, bytes);
         if (e != cudaSuccess) {
             cudaFree(p);
             return cuda_fail(ctx, e);
@@ -1220,7 +1236,7 @@ int lora_ctx_create(int device, int64_t max_rows, int max_rank, lora_ctx **out)
     cudaGetDevice(&prev);
     if (cudaSetDevice(device) != cudaSuccess ||
         cudaMalloc(reinterpret_cast<void **>(&ctx->d_status), 16) != cudaSuccess ||
-        cudaMemset(ctx->d_status, 0, 16) != cudaSuccess ||
+        zero_now(ctx->d_status, 16) != cudaSuccess ||
         cudaMalloc(reinterpret_cast<void **>(&ctx->d_dplan), size_t(max_rows) * 20 + 64) != cudaSuccess) {
         lora_ctx_destroy(ctx);
         cudaSetDevice(prev);
@@ -1973,10 +1989,10 @@ int lora_sync_status(lora_ctx *ctx, void *stream)
     unsigned word = 0;
     CUDA_TRY(ctx, cudaMemcpy(&word, ctx->d_status, sizeof word, cudaMemcpyDeviceToHost));
     if (word != 0) {
-        CUDA_TRY(ctx, cudaMemset(ctx->d_status, 0, sizeof word));
+        CUDA_TRY(ctx, zero_now(ctx->d_status, sizeof word));
         // an attention that gave up may have left arrivals behind
         if (ctx->attn && word >= kDevTimeoutLoad && word <= kDevTimeoutPipe)
-            CUDA_TRY(ctx, cudaMemset(ctx->attn, 0, ctx->attn_bytes));
+            CUDA_TRY(ctx, zero_now(ctx->attn, ctx->attn_bytes));
         return word == kDevBadId ? LORA_E_ADAPTER : word == kDevBadBatch ? LORA_E_INVAL
                : word == kDevBadPage ? LORA_E_PAGE : LORA_E_TIMEOUT;
     }
