@@ -354,11 +354,13 @@ __device__ __forceinline__ void load_vec(float v[N], const float *src)
 }
 
 // The end of one row, by a whole warp: its sums o (lane l has the DIM / 32 elements from
-// l * DIM / 32) over the sum of its weights l, as bf16; by careful_row where that is not
-// finite.
-template <int ROWS, int DIM, int FMT>
-__device__ __noinline__ void finish_row(const AttnParams &p, const Unit &u, int row,
-                                           const float o[DIM / 32], float l)
+// l * DIM / 32) over the sum of its weights l, as bf16.  Where that is not finite the row
+// takes careful_row, which may walk a long context: at once, or LATER by a caller whom
+// others wait for now.  Such a row is left as NaNs, which no finished one begins with, and
+// true is returned.
+template <int ROWS, int DIM, int FMT, bool LATER = false>
+__device__ __noinline__ bool finish_row(const AttnParams &p, const Unit &u, int row,
+                                        const float o[DIM / 32], float l)
 {
     constexpr int N = DIM / 32;
     const int lane = threadIdx.x & 31;
@@ -372,8 +374,16 @@ __device__ __noinline__ void finish_row(const AttnParams &p, const Unit &u, int 
         f[e] = l == 0.f ? 0.f : o[e] / l;
         ok = ok && fabsf(f[e]) < INFINITY;
     }
-    if (!__all_sync(0xffffffffu, ok))
-        careful_row<DIM, FMT>(p, u.q, u.s, u.h, pos, p.q + token * p.ldq + col, f);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) {
+        if (LATER) {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                f[e] = __int_as_float(0x7fffffff);
+        } else {
+            careful_row<DIM, FMT>(p, u.q, u.s, u.h, pos, p.q + token * p.ldq + col, f);
+        }
+    }
     uint16_t *dst = p.out + token * p.ldo + col + lane * N;
     __nv_bfloat162 w[N / 2];
 #pragma unroll
@@ -383,6 +393,7 @@ __device__ __noinline__ void finish_row(const AttnParams &p, const Unit &u, int 
         *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<uint2 *>(w);
     else
         *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<uint32_t *>(w);
+    return !ok;
 }
 
 }  // namespace lora

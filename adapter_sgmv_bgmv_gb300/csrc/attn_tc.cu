@@ -35,6 +35,9 @@
 // last one ends.  A unit cut by the ends of pieces leaves its parts in scratch, and the CTA
 // that arrives last joins them in the order of the CTAs.
 //
+// Rows whose result is not finite (attn.cuh) are only marked on the way, and redone when the
+// piece is done: each walks its whole context again, and the other roles' waits are bounded.
+//
 // Code size.  The four kinds of warps run different programs on one instruction cache: with
 // bodies unrolled to a thousand instructions each waited longer for instructions than for
 // anything else (1909 -> 592 us for the 8191-token prompt below went with short loops, one
@@ -335,10 +338,11 @@ __device__ __forceinline__ float weights(uint32_t tS, const float *ks, float f, 
 }
 
 // Joins the parts that the CTAs [first, last] left of unit u's rows, by the eight warps of
-// the weights.
+// the weights; true in a warp that left a row to redo_rows.
 template <int DIM, int FMT>
-__device__ __noinline__ void join_unit(const AttnParams &p, const Part &u)
+__device__ __noinline__ bool join_unit(const AttnParams &p, const Part &u)
 {
+    bool odd = false;
     constexpr int N = DIM / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n_rows = min(kRows, u.q.n_new * p.group - u.r * kRows), n = u.last - u.first + 1;
@@ -386,7 +390,62 @@ __device__ __noinline__ void join_unit(const AttnParams &p, const Part &u)
 #pragma unroll
         for (int r = 0; r < B; ++r)
             if (row + r < n_rows)
-                finish_row<kRows, DIM, FMT>(p, u, row + r, acc[r], l[r]);
+                odd |= finish_row<kRows, DIM, FMT, true>(p, u, row + r, acc[r], l[r]);
+    }
+    return odd;
+}
+
+// A CTA's piece [x, x1) and what it ended of it, for redo_rows.
+struct Piece {
+    int64_t x, x1;
+    int64_t at;               // where the sequence that holds x, s, begins
+    int s;
+    int odd;                  // some row was left
+    int joined;               // units cut by the piece's ends that were joined here: bit 1 the
+                              // one that begins in the piece, bit 0 the one that does not
+};
+
+// The rows whose result was not finite, each on its own.  They may take seconds over a long
+// context, so the eight warps of the weights come here once every part is done and nobody
+// waits for them within a bounded wait.
+template <int DIM, int FMT>
+__device__ __noinline__ void redo_rows(const AttnParams &p, const Piece &piece)
+{
+    using Cut = Split<kRows, kKeys, kUnitCost>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = piece.x;
+    const int64_t x1 = piece.x1;
+    Cursor u;
+    u.s = piece.s;
+    u.at = piece.at;
+    Cut::locate(p, x, u);
+#pragma unroll 1
+    while (true) {
+        const int64_t first = u.at + kUnitCost, end = first + u.span.n;
+        const int t0 = int(max(x - first, int64_t(0))), t1 = int(max(min(x1, end) - first, int64_t(0)));
+        const bool begins = t0 == 0, ends = t1 == u.span.n;
+        if (t1 > t0 && ((begins && ends) || (piece.joined >> int(begins) & 1))) {
+            // a warp looks at every eighth row, so that only it sees what it writes
+            const int row = 8 * lane + warp;
+            bool odd = false;
+            if (row < min(kRows, u.q.n_new * p.group - u.r * kRows)) {
+                int64_t token, col;
+                int pos;
+                row_place<kRows, DIM>(p, u, row, token, col, pos);
+                odd = (p.out[token * p.ldo + col] & 0x7fffu) > 0x7f80u;
+            }
+            unsigned rows = __ballot_sync(0xffffffffu, odd);
+            const float o[DIM / 32] = {};
+#pragma unroll 1
+            while (rows) {
+                finish_row<kRows, DIM, FMT>(p, u, 8 * (__ffs(rows) - 1) + warp, o, __int_as_float(0x7fffffff));
+                rows &= rows - 1;
+            }
+        }
+        x = end;
+        if (x >= x1)
+            break;
+        Cut::next(p, u);
     }
 }
 
@@ -395,7 +454,7 @@ __global__ void __launch_bounds__(Crew<FMT>::THREADS, 1) k_attn_tc(const __grid_
 {
     using S = TcShape<DIM>;
     using Cut = Split<kRows, kKeys, kUnitCost>;
-    constexpr int ST = S::STAGES, N = DIM / 32;
+    constexpr int ST = S::STAGES;
     constexpr int kThreads = Crew<FMT>::THREADS, LW = Crew<FMT>::LOADS, LR = Crew<FMT>::ROWS;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), sm = (raw + 1023u) & ~1023u;
@@ -406,6 +465,7 @@ __global__ void __launch_bounds__(Crew<FMT>::THREADS, 1) k_attn_tc(const __grid_
     __shared__ uint32_t poison[kScaleSlots * 4];           // per slot: keys whose value's scale is not finite
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_flag, last_flag, longest;
+    __shared__ Piece whole;
     volatile int *dead = &dead_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const KvView &kv = p.kv;
@@ -435,6 +495,7 @@ __global__ void __launch_bounds__(Crew<FMT>::THREADS, 1) k_attn_tc(const __grid_
         fence_mbar_init();
         dead_flag = 0;
         longest = 0;
+        whole.odd = whole.joined = 0;
     }
     if (warp == 8 + LW)
         tc::tmem_alloc(smem_u32(&tmem_slot), 512);
@@ -598,12 +659,9 @@ __global__ void __launch_bounds__(Crew<FMT>::THREADS, 1) k_attn_tc(const __grid_
                     }
                 }
                 // a sum of weights that overflowed gives zeros above; it is not finite either
-                unsigned bad = __ballot_sync(0xffffffffu, on && !(fine && l < INFINITY));
-                while (bad) {                              // rows to be done on their own
-                    const int src = __ffs(bad) - 1;
-                    bad &= bad - 1;
-                    float o[N] = {};
-                    finish_row<kRows, DIM, FMT>(p, *pt, T * kM + (warp & 3) * 32 + src, o, __int_as_float(0x7fffffff));
+                if (on && !(fine && l < INFINITY)) {
+                    *dst = 0x7fff;
+                    whole.odd = 1;
                 }
             } else {
                 const int64_t at = (int64_t(blockIdx.x) * 2 + pt->begins) * kRows + T * kM + row;
@@ -624,14 +682,17 @@ __global__ void __launch_bounds__(Crew<FMT>::THREADS, 1) k_attn_tc(const __grid_
                     break;
                 if (warp == 0 && lane == 0) {
                     last_flag = atomicAdd(&p.part.arrived[pt->first], 1) == pt->last - pt->first;
-                    if (last_flag)
+                    if (last_flag) {
                         p.part.arrived[pt->first] = 0;
+                        whole.joined |= 1 << pt->begins;
+                    }
                 }
                 if (!meet())
                     break;
                 if (last_flag) {
                     __threadfence();
-                    join_unit<DIM, FMT>(p, *pt);
+                    if (join_unit<DIM, FMT>(p, *pt))
+                        whole.odd = 1;
                 }
                 if (!meet())                               // last_flag is free again
                     break;
@@ -639,6 +700,8 @@ __global__ void __launch_bounds__(Crew<FMT>::THREADS, 1) k_attn_tc(const __grid_
             tc::fence_before_sync();
             part_done();
         }
+        if (alive && meet() && whole.odd)
+            redo_rows<DIM, FMT>(p, whole);
     } else if (warp < 8 + LW) {
         // ------------------------------------------------------------ loads
         setmaxnreg_dec<Crew<FMT>::load>();
@@ -913,8 +976,11 @@ __global__ void __launch_bounds__(Crew<FMT>::THREADS, 1) k_attn_tc(const __grid_
         if (warp == 10 + LW && lane == 0) {
             int64_t x = piece * blockIdx.x;
             const int64_t x1 = min(x + piece, total);
-            if (x < x1)
+            if (x < x1) {
+                whole.x = x, whole.x1 = x1;
+                whole.s = cursor.s, whole.at = cursor.at;
                 Cut::locate(p, x, cursor);
+            }
             bool more = true;
             while (more) {
                 int t0 = 0, t1 = 0;
