@@ -1991,10 +1991,10 @@ int lora_sync_status(lora_ctx *ctx, void *stream)
     if (word != 0) {
         CUDA_TRY(ctx, zero_now(ctx->d_status, sizeof word));
         // an attention that gave up may have left arrivals behind
-        if (ctx->attn && word >= kDevTimeoutLoad && word <= kDevTimeoutPipe)
+        if (ctx->attn && (word & kDevGaveUp))
             CUDA_TRY(ctx, zero_now(ctx->attn, ctx->attn_bytes));
-        return word == kDevBadId ? LORA_E_ADAPTER : word == kDevBadBatch ? LORA_E_INVAL
-               : word == kDevBadPage ? LORA_E_PAGE : LORA_E_TIMEOUT;
+        return word & kDevGaveUp ? LORA_E_TIMEOUT : word & 1u << kDevBadId ? LORA_E_ADAPTER
+               : word & 1u << kDevBadBatch ? LORA_E_INVAL : LORA_E_PAGE;
     }
     return LORA_OK;
 }

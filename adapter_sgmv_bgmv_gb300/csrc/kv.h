@@ -5,6 +5,9 @@
 #include <cuda_runtime.h>
 
 #include "status.h"
+#ifdef __CUDACC__
+#include "ptx.cuh"
+#endif
 
 struct lora_ctx;
 
@@ -113,8 +116,7 @@ __device__ __forceinline__ SeqInfo seq_info(const BatchView &b, int s, unsigned 
     q.n_new = end - q.start;
     if (q.start < 0 || end < q.start || end > b.n_rows || q.n_new > b.max_new || q.len < 0 ||
         q.len > b.capacity) {
-        if (status)
-            atomicCAS(status, 0u, unsigned(kDevBadBatch));
+        raise_status(status, kDevBadBatch);
         q.start = q.n_new = q.len = 0;
     }
     return q;

@@ -20,11 +20,12 @@ __device__ __forceinline__ uint64_t globaltimer_ns()
     return t;
 }
 
-// Record a device-side failure (first writer wins) in the context's status word.
+// Record a device-side failure in the context's status word, beside what is there: bad
+// data found before a timeout must not hide it.
 __device__ __forceinline__ void raise_status(unsigned *status, unsigned code)
 {
     if (status)
-        atomicCAS(status, 0u, code);
+        atomicOr(status, 1u << code);
 }
 
 // ---------------------------------------------------------------- mbarrier

@@ -7,6 +7,8 @@ namespace lora {
 // A bounded device wait gives up after this long (nanoseconds of %globaltimer).
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
+// What a kernel found; the status word has bit 1 << code of every code raised since it was
+// last read.
 enum DeviceStatus : unsigned {
     kDevOk = 0,
     kDevTimeoutLoad = 1,   // a copy into shared memory did not complete in time
@@ -17,5 +19,8 @@ enum DeviceStatus : unsigned {
     kDevBadBatch = 6,      // a sequence's rows or length out of range (sequence skipped)
     kDevBadPage = 7        // a page id outside the cache's pools (its positions skipped)
 };
+
+// The codes after which a kernel has left work undone (bits of the status word).
+constexpr unsigned kDevGaveUp = 1u << kDevTimeoutLoad | 1u << kDevTimeoutMma | 1u << kDevTimeoutPipe | 1u << kDevBadShape;
 
 }  // namespace lora

@@ -345,8 +345,11 @@ int lora_tune_shape(lora_ctx *ctx, const lora_table *table, int kind,
                     int d_in, void *y, int64_t ldy, int d_out, int iters,
                     float *best_us, void *stream);
 
-/* Synchronize `stream`, then read and clear the device status word: LORA_OK or
- * LORA_E_TIMEOUT if a kernel's bounded wait expired since the last check. */
+/* Synchronize `stream`, then read and clear what kernels recorded since the last check:
+ * LORA_OK, or LORA_E_TIMEOUT if a bounded wait expired (the results of the calls since
+ * the last check are of no use), else LORA_E_ADAPTER (a device-resident id that its table cannot
+ * serve), else LORA_E_INVAL (a lora_kv_batch out of range), else LORA_E_PAGE (a page id in
+ * one). */
 int lora_sync_status(lora_ctx *ctx, void *stream);
 
 /* Context options:
