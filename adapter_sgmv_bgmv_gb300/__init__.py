@@ -485,9 +485,16 @@ class KvCache:
         d.n_pages, d.page_size, d.n_heads, d.head_dim = k_pool.shape
         d.page_stride, d.cell_stride, d.head_stride = k_pool.stride()[:3]
         if ctx.device is None:      # host-only context: pools are never dereferenced
+            self.device_index = None
             ptr = lambda t, nm: t.data_ptr()  # noqa: E731
         else:
-            ptr = _dev_ptr
+            self.device_index = ctx.device.index or 0
+
+            def ptr(t, nm):
+                p = _dev_ptr(t, nm)
+                if t.get_device() != self.device_index:
+                    raise ValueError(f"{nm} must be on the context's device")
+                return p
         d.k_pool, d.v_pool = ptr(k_pool, "k_pool"), ptr(v_pool, "v_pool")
         if d.format:
             d.k_scale, d.v_scale = ptr(k_scale, "k_scale"), ptr(v_scale, "v_scale")
@@ -530,6 +537,9 @@ class KvBatch:
         a.starts = _dev_ptr(starts, "starts")
         a.lens = _dev_ptr(lens, "lens")
         a.pages = _dev_ptr(pages, "pages")
+        self.device_index = starts.get_device()
+        if lens.get_device() != self.device_index or pages.get_device() != self.device_index:
+            raise ValueError("starts, lens and pages must be on one device")
         a.n_seqs, a.n_cols = pages.shape
         a.ld_pages = max(pages.stride(0), pages.shape[1]) if pages.shape[0] > 1 else pages.shape[1]
         if pages.shape[0] > 1 and pages.stride(0) < pages.shape[1]:
@@ -539,9 +549,10 @@ class KvBatch:
         self._ref = ctypes.addressof(a)
 
 
-def _head_rows(t: torch.Tensor, what: str, head_dim: int):
+def _head_rows(t: torch.Tensor, what: str, cache: KvCache):
     """(pointer, row stride, rows, heads) of bf16 rows [n, heads, head_dim] (the heads one
-    after another) or [n, heads * head_dim]."""
+    after another) or [n, heads * head_dim] on the cache's device."""
+    head_dim = cache.head_dim
     try:
         sh, st = t.shape, t.stride()
         if len(sh) == 3:
@@ -551,12 +562,14 @@ def _head_rows(t: torch.Tensor, what: str, head_dim: int):
             n, width = sh
             heads = width // head_dim
             ok = st[1] == 1 and heads * head_dim == width
-        ok = ok and t.is_cuda and t.element_size() == 2
+        ok = ok and t.dtype is torch.bfloat16 and t.get_device() == cache.device_index
     except (AttributeError, ValueError):
         ok = False
     if not ok:
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{what} must be a CUDA tensor")
+        if t.get_device() != cache.device_index:
+            raise ValueError(f"{what} must be on the context's device")
         raise ValueError(f"{what} must be bf16 [n, heads, {head_dim}] or [n, heads * {head_dim}] rows")
     # the stride of a single row says nothing
     return t.data_ptr(), st[0] if n > 1 else heads * head_dim, n, heads
@@ -571,8 +584,10 @@ def _raw_stream(stream, ctx: Context):
 
 
 def _kv_rows(ctx, cache, batch, k, v, stream, fn):
-    pk, ldk, n, hk = _head_rows(k, "k", cache.head_dim)
-    pv, ldv, nv, hv = _head_rows(v, "v", cache.head_dim)
+    pk, ldk, n, hk = _head_rows(k, "k", cache)
+    pv, ldv, nv, hv = _head_rows(v, "v", cache)
+    if batch.device_index != cache.device_index:
+        raise ValueError("the batch must be on the context's device")
     if nv != n or hk != cache.n_heads or hv != cache.n_heads:
         raise ValueError("k and v must have one row a token and the cache's heads")
     rc = fn(ctx.handle, cache.handle, batch._ref, n, pk, ldk, pv, ldv, _raw_stream(stream, ctx))
@@ -599,8 +614,10 @@ def lora_attention(ctx: Context, cache: KvCache, batch: KvBatch, q: torch.Tensor
     cache, which already holds their keys and values: causal by position, with a sliding
     window and `sinks` first tokens that stay visible when window > 0.  scale: None for
     head_dim ** -0.5."""
-    pq, ldq, n, hq = _head_rows(q, "q", cache.head_dim)
-    po, ldo, no, ho = _head_rows(out, "out", cache.head_dim)
+    pq, ldq, n, hq = _head_rows(q, "q", cache)
+    po, ldo, no, ho = _head_rows(out, "out", cache)
+    if batch.device_index != cache.device_index:
+        raise ValueError("the batch must be on the context's device")
     if no != n or ho != hq:
         raise ValueError("out must have the shape of q")
     if scale is None:
