@@ -622,6 +622,8 @@ def lora_attention(ctx: Context, cache: KvCache, batch: KvBatch, q: torch.Tensor
         raise ValueError("out must have the shape of q")
     if scale is None:
         scale = cache.head_dim ** -0.5
+    if (window | sinks) >> 31:      # beyond an int: no position is that far away; negative: refused
+        window, sinks = (max(-1, min(v, (1 << 31) - 1)) for v in (window, sinks))
     rc = _L.lora_attention(ctx.handle, cache.handle, batch._ref, n, pq, ldq, hq, scale, window, sinks,
                            po, ldo, _raw_stream(stream, ctx))
     if rc:
