@@ -18,6 +18,7 @@
 #include "../../include/lora.h"
 #include "ctx.h"
 #include "internal.h"
+#include "once.h"
 #include "status.h"
 #include "plan.h"
 #include "tiles.h"
@@ -197,6 +198,8 @@ cudaError_t zero_now(void *p, size_t bytes)
             return cuda_fail((ctx), _e);             \
     } while (0)
 
+thread_local int device_in_use = -1;
+
 int use_device(lora_ctx *ctx)
 {
     if (ctx->device < 0)
@@ -206,6 +209,7 @@ int use_device(lora_ctx *ctx)
     CUDA_TRY(ctx, cudaGetDevice(&cur));
     if (cur != ctx->device)
         CUDA_TRY(ctx, cudaSetDevice(ctx->device));
+    device_in_use = ctx->device;
     return LORA_OK;
 }
 
@@ -1130,6 +1134,8 @@ int ctx_begin(lora_ctx *ctx, cudaStream_t stream)
     begin_call(ctx, stream);
     return use_device(ctx);
 }
+
+int launch_device() { return device_in_use; }
 
 int ctx_cuda_fail(lora_ctx *ctx, cudaError_t e) { return cuda_fail(ctx, e); }
 

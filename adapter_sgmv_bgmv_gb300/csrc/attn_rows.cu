@@ -33,6 +33,7 @@
 #include <cuda_runtime.h>
 
 #include "attn.cuh"
+#include "once.h"
 #include "tc.cuh"
 
 namespace lora {
@@ -624,13 +625,12 @@ template <int DIM, int FMT, int NR>
 cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream)
 {
     using S = Shape<DIM, FMT, NR>;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(k_attn_rows<DIM, FMT, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-        if (e != cudaSuccess)
-            return e;
-        configured = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t e = once([] {
+        return cudaFuncSetAttribute(k_attn_rows<DIM, FMT, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    });
+    if (e != cudaSuccess)
+        return e;
     static_assert(S::CTAS <= kMaxCtas, "the scratch has room for every CTA");
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(S::CTAS * sms));

@@ -54,6 +54,7 @@
 #include <climits>
 
 #include "attn.cuh"
+#include "once.h"
 #include "tc.cuh"
 
 namespace lora {
@@ -1042,14 +1043,13 @@ __global__ void __launch_bounds__(Crew<FMT>::THREADS, 1) k_attn_tc(const __grid_
 template <int DIM, int FMT>
 cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream)
 {
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(k_attn_tc<DIM, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             TcShape<DIM>::SMEM);
-        if (e != cudaSuccess)
-            return e;
-        configured = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t e = once([] {
+        return cudaFuncSetAttribute(k_attn_tc<DIM, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    TcShape<DIM>::SMEM);
+    });
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(sms));
     cfg.blockDim = dim3(Crew<FMT>::THREADS);

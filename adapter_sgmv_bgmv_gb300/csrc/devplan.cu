@@ -18,6 +18,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "once.h"
 #include "ptx.cuh"
 
 namespace lora {
@@ -136,14 +137,13 @@ cudaError_t launch_plan_dev(const DevPlanArgs &a, cudaStream_t stream)
 {
     if (a.n_adapters <= 0 || a.n_adapters > kDevPlanMaxAdapters || a.n < 0 || a.rows_per_item < 1)
         return cudaErrorInvalidValue;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(k_plan_dev, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(dev_plan_smem_bytes(kDevPlanMaxAdapters)));
-        if (e != cudaSuccess)
-            return e;
-        configured = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t e = once([] {
+        return cudaFuncSetAttribute(k_plan_dev, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    int(dev_plan_smem_bytes(kDevPlanMaxAdapters)));
+    });
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(kPlanThreads);

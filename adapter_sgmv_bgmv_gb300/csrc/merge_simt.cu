@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "once.h"
 #include "ptx.cuh"
 
 namespace lora {
@@ -91,15 +92,12 @@ __global__ void __launch_bounds__(kThreads) k_merge_simt(const MergeParams p)
 cudaError_t launch_merge_simt(const MergeParams &p, cudaStream_t stream)
 {
     const size_t smem = size_t(kRowsTile) * p.rank * 4 + size_t(p.rank) * kColsTile * 2;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(k_merge_simt,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             200 * 1024);
-        if (e != cudaSuccess)
-            return e;
-        configured = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t e = once([] {
+        return cudaFuncSetAttribute(k_merge_simt, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    });
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((p.d_out + kColsTile - 1) / kColsTile, (p.d_in + kRowsTile - 1) / kRowsTile);
     cfg.blockDim = dim3(kThreads);

@@ -53,6 +53,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "once.h"
 #include "tc.cuh"
 #include "tmap.h"
 
@@ -524,14 +525,12 @@ cudaError_t launch_proj_tc(const ProjParams &p, cudaStream_t stream)
             m = CUtensorMap{};
         a.amap = CUtensorMap{};
     }
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(k_proj_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(proj_smem_bytes()));
-        if (e != cudaSuccess)
-            return e;
-        configured = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t e = once([] {
+        return cudaFuncSetAttribute(k_proj_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, int(proj_smem_bytes()));
+    });
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = proj_smem_bytes();

@@ -30,6 +30,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "once.h"
 #include "ptx.cuh"
 
 namespace lora {
@@ -528,17 +529,15 @@ cudaError_t configure(Kernel k)
 template <int MODE, bool INLINE, typename Arg, bool DIRECT, int OCC>
 cudaError_t launch_occ(const RowsParams &p, const Arg &arg, size_t smem, cudaStream_t stream)
 {
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e;
+    static OncePerDevice once;
+    const cudaError_t e = once([] {
         if constexpr (INLINE)
-            e = configure(k_rows_inline<MODE, Arg, OCC>);
+            return configure(k_rows_inline<MODE, Arg, OCC>);
         else
-            e = configure(k_rows<MODE, DIRECT, OCC>);
-        if (e != cudaSuccess)
-            return e;
-        configured = true;
-    }
+            return configure(k_rows<MODE, DIRECT, OCC>);
+    });
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(p.n_items) * unsigned(p.cluster), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);

@@ -47,6 +47,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "once.h"
 #include "tc.cuh"
 #include "tmap.h"
 
@@ -630,15 +631,17 @@ cudaError_t launch_stream(StreamArgs &a, const void *tensor, uint64_t inner, uin
                 a.nbuf = 2;
                 break;
             }
-    static bool configured = false;
-    if (!configured) {
+    static OncePerDevice once;
+    const cudaError_t e = once([] {
         for (auto *k : {k_stream_tc<false>, k_stream_tc<true>}) {
-            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-            if (e != cudaSuccess)
-                return e;
+            const cudaError_t one = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+            if (one != cudaSuccess)
+                return one;
         }
-        configured = true;
-    }
+        return cudaSuccess;
+    });
+    if (e != cudaSuccess)
+        return e;
     const bool wide = a.left == kLeftVParts && a.p.ksplit <= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(a.ctas));

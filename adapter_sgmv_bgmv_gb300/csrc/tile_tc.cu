@@ -28,6 +28,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "once.h"
 #include "tc.cuh"
 #include "tmap.h"
 
@@ -235,14 +236,12 @@ cudaError_t launch_shrink_tc(const TileParams &p, cudaStream_t stream)
                         kKB, kTM, true) ||
         !encode_row_maps(args.amap, p.a_rows, uint64_t(p.d_in), p.a_nrows, p.a_ld))
         return cudaErrorInvalidValue;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(k_shrink_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             227 * 1024);
-        if (e != cudaSuccess)
-            return e;
-        configured = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t e = once([] {
+        return cudaFuncSetAttribute(k_shrink_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    });
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(p.n_items) * unsigned(p.vmode == 0 ? p.ksplit : 1));
     cfg.blockDim = dim3(kShrinkThreads);
