@@ -152,7 +152,8 @@ class Context:
                self)
 
     def sync_status(self, stream=None) -> int:
-        """Synchronize and read back the device status word (raises on a timeout)."""
+        """Synchronize and read back what kernels recorded (see include/lora.h): raises on a
+        timeout, a device-resident id or a cache batch that could not be served."""
         return _check(_L.lora_sync_status(self.handle, _stream(stream, self.device)), self)
 
     def selftest_timeout(self, limit_us: int = 10000, stream=None):
@@ -186,7 +187,8 @@ class Context:
 
     def last_path(self):
         """(path bits, launches) of the last call: 1 row-gather, 2 tensor-core tile,
-        4 merge."""
+        4 merge, 8 page-in, 16 base projection, 32 cache write / read, 64 attention of few
+        rows, 128 attention of many."""
         n = ctypes.c_int()
         p = _L.lora_last_path(self.handle, ctypes.byref(n))
         return p, n.value

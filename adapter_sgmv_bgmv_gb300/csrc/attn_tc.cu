@@ -44,7 +44,7 @@
 // copy of each, and one warp for what all need to know of a unit).
 //
 // Measured (bf16, dim 128, 32 query heads on 8 key heads, one 8191-token prompt in pages of
-// one token): 547 us, 1.0 PFLOP/s, 0.53 of a cuBLAS bf16 product's rate; what bounds it is the
+// one token): 555 us, 0.99 PFLOP/s, 0.52 of a cuBLAS bf16 product's rate; what bounds it is the
 // chain of one row tile (scores, maximum, weights, products: 4,200 cycles for 1,024 of
 // products), of which two run side by side.  16 prompts of 1056 tokens, a key head for each
 // query head: 325 us, 0.45 PFLOP/s; a unit there is nine key tiles long at most, and its start

@@ -7,9 +7,9 @@
 //
 // 8-bit formats, per vector: scale = max |x| / T (T = 127 for int8, 448 for e4m3; one
 // fp32 division, rounded to nearest), code = x / scale rounded to nearest even and
-// limited to +-T.  x / scale means the true quotient: the code is the nearest one, not one
-// off next to a tie as with a rounded reciprocal.  A vector that holds an infinity or a
-// NaN gets a NaN scale and zero codes, so it reads back as NaN; a zero vector gets
+// limited to +-T.  x / scale is the quotient as one fp32 division gives it (rounded to
+// nearest), which a product with a rounded reciprocal may miss next to a tie.  A vector that
+// holds an infinity or a NaN gets a NaN scale and zero codes, so it reads back as NaN; a zero vector gets
 // scale 0.
 //
 // Bound: DRAM at prefill sizes (the vectors are read and written once), and one
@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const __grid_constant__ Kv
 template <typename F>
 cudaError_t launch(F kernel, KvRowsParams p, cudaStream_t stream)
 {
-    // As many rows a CTA as leave two CTAs for each SM (their look-ups then run side by
-    // side); a few rows of many vectors are cut instead, to spread over the SMs.
+    // As many rows a CTA as leave two CTAs for each of 152 SMs (their look-ups then run side
+    // by side); a few rows of many vectors are cut instead, to spread over the SMs.
     const int rows = int(std::min<int64_t>(kMaxRows, std::max<int64_t>(1, p.b.n_rows / 304)));
     const int per = kThreads / (p.kv.dim / 16) * 2;
     p.per_row = Divider(2 * p.kv.heads);

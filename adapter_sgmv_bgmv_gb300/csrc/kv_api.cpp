@@ -27,9 +27,11 @@ constexpr int64_t kMaxPosition = int64_t(1) << 30;
 bool aligned(const void *p, uintptr_t a) { return p && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Rows (new tokens times query heads per key head) up to which a sequence's attention
-// goes to the few-rows kernel: one unit of it.  Its second unit would read the keys again:
-// 20 rows over 2000 bf16 keys in 16 sequences took 76 us there and 46 us in the other (int8
-// 73 and 59).  12 rows of int8 take 50 us here and 58 there.
+// goes to the few-rows kernel: one unit of it.  Its second unit would read the keys again.
+// 16 sequences of 2000 keys, 32 query heads on 8: 20 rows take 76 us there and 46 us in the
+// other in bf16 (int8 72 and 58, e4m3 73 and 60); 12 rows 50 us here and 57 there in int8
+// (e4m3 50 and 60).  In bf16 12 rows take 55 us here and 45 there; they stay for the weights'
+// second term, so that the rule and the precision do not depend on the format.
 constexpr int kFewRows = 16;
 
 int log2_exact(int v)

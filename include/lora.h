@@ -37,9 +37,9 @@
  *    need not outlive it (lora_fused_device_ids excepted: its ids stay on the
  *    device and must stay valid until the stream has passed the call).  A context
  *    is not thread-safe, and its scratch (partial V, dense adapter rows, the
- *    device-side plan) is shared by its calls: calls of one context that could
- *    overlap on the GPU (different streams) must be ordered by events; page-in
- *    uses no scratch.
+ *    device-side plan, lora_attention's partial results) is shared by its calls:
+ *    calls of one context that could overlap on the GPU (different streams) must be
+ *    ordered by events; page-in and the cache's write and read use no scratch.
  *  - Ranks must be multiples of 8 in [8, LORA_MAX_RANK].
  */
 #ifndef LORA_H
@@ -347,9 +347,9 @@ int lora_tune_shape(lora_ctx *ctx, const lora_table *table, int kind,
 
 /* Synchronize `stream`, then read and clear what kernels recorded since the last check:
  * LORA_OK, or LORA_E_TIMEOUT if a bounded wait expired (the results of the calls since
- * the last check are of no use), else LORA_E_ADAPTER (a device-resident id that its table cannot
- * serve), else LORA_E_INVAL (a lora_kv_batch out of range), else LORA_E_PAGE (a page id in
- * one). */
+ * the last check are of no use), else LORA_E_ADAPTER (a device-resident id that its table
+ * cannot serve), else LORA_E_INVAL (a lora_kv_batch out of range), else LORA_E_PAGE (a
+ * page id in one). */
 int lora_sync_status(lora_ctx *ctx, void *stream);
 
 /* Context options:
@@ -370,8 +370,10 @@ int lora_sync_status(lora_ctx *ctx, void *stream);
  *                          not read, and still waits before it ends).  The caller then
  *                          guarantees that no kernel launched immediately before a
  *                          delta, merge or unmerge call in the same stream writes the
- *                          pools or page tables (this library's own kernels never do; a
- *                          copy or a host-side wait in between is enough).
+ *                          adapters' pages or the page tables (this library's own kernels
+ *                          never do, page-ins apart, which are waited for; lora_kv_write
+ *                          writes a unified pool's other pages; a copy or a host-side
+ *                          wait in between is enough).
  *                          For lora_fused_device_ids in its default mode the guarantee
  *                          covers the device ids as well: with 1 the kernel reads them
  *                          (and copies the pages they select) before the wait.
@@ -442,7 +444,7 @@ int lora_selftest_timeout(lora_ctx *ctx, int64_t limit_us, void *stream);
  * Formats: LORA_KV_BF16; LORA_KV_INT8 and LORA_KV_FP8 (e4m3), 8-bit codes with one fp32
  * scale for each (page, cell, head) in k_scale / v_scale, with strides of their own.  A
  * cached vector stands for scale * code.  Writing x takes scale = max |x| / T (T = 127 or
- * 448, one fp32 division) and code = x / scale to the nearest, ties to even; a vector
+ * 448) and code = x / scale (each one fp32 division) to the nearest, ties to even; a vector
  * with an infinity or a NaN gets a NaN scale and zero codes, and reads back as NaN.
  *
  * head_dim is 64 or 128.  Pool pointers and page, cell and head strides are multiples
@@ -480,8 +482,9 @@ typedef struct {
 } lora_kv_batch;
 
 /* Register a cache with a context.  The first one of a context allocates its attention
- * scratch; no later call allocates.  LORA_E_UNSUPPORTED: head_dim; LORA_E_CAPACITY: 2^31
- * pages or more, page_size above 2^20, more than 4096 heads. */
+ * scratch (56 MB on 152 SMs), kept until the context is destroyed; no later call
+ * allocates.  LORA_E_UNSUPPORTED: head_dim; LORA_E_CAPACITY: 2^31 pages or more, page_size
+ * above 2^20, more than 4096 heads. */
 int lora_kv_create(lora_ctx *ctx, const lora_kv_desc *desc, lora_kv **out);
 int lora_kv_destroy(lora_kv *kv);
 
@@ -490,9 +493,9 @@ int lora_kv_destroy(lora_kv *kv);
 int lora_kv_write(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch, int64_t n,
                   const void *k, int64_t ldk, const void *v, int64_t ldv, void *stream);
 
-/* The inverse: the cells of the rows' positions as bf16 rows (scale * code, rounded
- * once); rows without a position become zeros.  With n_new = lens it reads whole
- * sequences back. */
+/* The inverse: the cells of the rows' positions as bf16 rows (the fp32 product scale *
+ * code, rounded to bf16); rows without a position become zeros.  With n_new = lens it
+ * reads whole sequences back. */
 int lora_kv_read(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch, int64_t n,
                  void *k, int64_t ldk, void *v, int64_t ldv, void *stream);
 
@@ -503,9 +506,11 @@ int lora_kv_read(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch, i
  * out are [n][n_heads * head_dim] bf16 with row strides ldq / ldo; n_heads is a
  * multiple of the cache's heads, and query head h reads key head
  * h / (n_heads / cache heads).  A row without a position gets zeros.  Positions a row
- * does not see never reach its result, whatever they hold.  out may not overlap q.  (A
- * delta call right behind, with `out` as its x, must run without LORA_OPT_EARLY_INPUT,
- * which reads x ahead of the kernel before.)
+ * does not see never reach its result, whatever they hold.  A row that sees an infinity or
+ * a NaN, or has one among the values beside its own, is computed alone and slowly: 200
+ * rows of one head over 40,000 keys take 0.65 s then, 0.13 ms else.
+ * out may not overlap q.  (A delta call right behind, with `out` as its x, must run
+ * without LORA_OPT_EARLY_INPUT, which reads x ahead of the kernel before.)
  * Scores, weights' sums and outputs are kept in fp32.  For the product with v, weights
  * are taken as two bf16 terms (about 16 bits) for sequences of at most 16 rows
  * (n_new * query heads per key head), and rounded to bf16 for longer ones. */
