@@ -20,6 +20,9 @@ from . import _lib
 __all__ = ["LoraError", "Context", "AdapterTable", "lora_plan_build", "lora_shrink",
            "lora_expand", "lora_fused", "lora_fused_noalloc", "lora_base_fused", "PreparedFused", "PreparedFusedDeviceIds", "lora_merge", "lora_unmerge", "lora_page_in", "lora_fused_device_ids", "lora_tune_shape",
            "KvCache", "KvBatch", "lora_kv_write", "lora_kv_read", "lora_attention",
+           "HeadRope", "lora_head_rope", "lora_kv_write_rope",
+           "PageTable", "lora_pages_extend", "lora_pages_fork", "lora_pages_free", "lora_pages_compact", "lora_kv_copy",
+           "BlockSelection", "lora_kv_bounds", "lora_block_select", "lora_block_attention",
            "KIND_ROWS_FUSED", "KIND_SHRINK", "KIND_EXPAND", "KIND_TILE_FUSED", "KIND_MERGE",
            "OPT_TILE_PATH", "OPT_MERGE_KERNEL", "OPT_TILE_MIN_RUN", "OPT_EARLY_PAGES", "OPT_DEVICE_PLAN",
            "OPT_EARLY_INPUT", "OPT_ROWS_B_OVER_A",
@@ -188,7 +191,8 @@ class Context:
     def last_path(self):
         """(path bits, launches) of the last call: 1 row-gather, 2 tensor-core tile,
         4 merge, 8 page-in, 16 base projection, 32 cache write / read, 64 attention of few
-        rows, 128 attention of many."""
+        rows, 128 attention of many, 256 norms and rotation of heads, 512 page tables, 1024 page
+        copies, 2048 bounds and choice of pages."""
         n = ctypes.c_int()
         p = _L.lora_last_path(self.handle, ctypes.byref(n))
         return p, n.value
@@ -506,7 +510,25 @@ class KvCache:
         h = ctypes.c_void_p()
         _check(_L.lora_kv_create(ctx.handle, ctypes.byref(d), ctypes.byref(h)), ctx)
         self.handle = h.value
+        self.bounds = None
         ctx._tables.add(self)
+
+    def attach_bounds(self, codes: torch.Tensor | None, unit: torch.Tensor | None):
+        """The memory for each page's smallest and largest keys (see include/lora.h): codes int8
+        [n_pages, n_heads, 2, head_dim] and unit float32 [n_pages, n_heads], contiguous; both None
+        to detach.  lora_kv_bounds fills it, lora_block_select reads it, lora_kv_copy moves it."""
+        if (codes is None) != (unit is None):
+            raise ValueError("codes and unit come together")
+        if codes is not None:
+            for t, nm, dt, sh in ((codes, "codes", torch.int8, (self.n_pages, self.n_heads, 2, self.head_dim)),
+                                  (unit, "unit", torch.float32, (self.n_pages, self.n_heads))):
+                if not isinstance(t, torch.Tensor) or t.dtype != dt or tuple(t.shape) != sh or not t.is_contiguous():
+                    raise ValueError(f"{nm} must be a contiguous {dt} tensor of shape {list(sh)}")
+                if self.device_index is not None and (not t.is_cuda or t.get_device() != self.device_index):
+                    raise ValueError(f"{nm} must be on the context's device")
+        _check(_L.lora_kv_attach_bounds(self.handle, None if codes is None else codes.data_ptr(),
+                                        None if unit is None else unit.data_ptr()), self.ctx)
+        self.bounds = None if codes is None else (codes, unit)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -628,6 +650,287 @@ def lora_attention(ctx: Context, cache: KvCache, batch: KvBatch, q: torch.Tensor
         window, sinks = (max(-1, min(v, (1 << 31) - 1)) for v in (window, sinks))
     rc = _L.lora_attention(ctx.handle, cache.handle, batch._ref, n, pq, ldq, hq, scale, window, sinks,
                            po, ldo, _raw_stream(stream, ctx))
+    if rc:
+        _check(rc, ctx)
+
+
+class HeadRope:
+    """What lora_head_rope does to each head (see include/lora.h): freqs, float32 [pairs] on the
+    GPU, turns the first 2 * pairs elements (None: no rotation), as pairs (j, j + pairs) or, when
+    interleaved, (2j, 2j + 1); q_weight and k_weight [head_dim], where given, are the weights of
+    the norms (kept as float32: another type is converted here, once)."""
+
+    def __init__(self, freqs: torch.Tensor | None, head_dim: int, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False):
+        self.head_dim, self.device_index = int(head_dim), None
+        r = _lib.Rope()
+        r.eps, r.head_dim, r.interleaved = float(eps), self.head_dim, int(bool(interleaved))
+        if freqs is not None and freqs.numel() == 0:
+            freqs = None
+        kept = {}
+        for t, nm, field in ((freqs, "freqs", "freqs"), (q_weight, "q_weight", "q_weight"), (k_weight, "k_weight", "k_weight")):
+            if t is None:
+                continue
+            if not isinstance(t, torch.Tensor) or t.dim() != 1 or not t.is_floating_point():
+                raise ValueError(f"{nm} must be a 1-D tensor of floating point")
+            if nm == "freqs":
+                if t.dtype != torch.float32:
+                    raise ValueError("freqs must be float32")
+            elif t.shape[0] != self.head_dim:
+                raise ValueError(f"{nm} must have head_dim elements")
+            t = t.float().contiguous()
+            if t.data_ptr() % 16:
+                t = t.clone()
+            setattr(r, field, _dev_ptr(t, nm))
+            if self.device_index is not None and t.get_device() != self.device_index:
+                raise ValueError("freqs, q_weight and k_weight must be on one device")
+            self.device_index = t.get_device()
+            kept[nm] = t
+        r.rot_dim = 0 if freqs is None else 2 * freqs.shape[0]
+        self._kept, self._args = kept, r
+        self._ref = ctypes.addressof(r)
+
+
+class _HeadsOn:
+    """What _head_rows looks at, for rows that go with no cache."""
+
+    def __init__(self, head_dim, device_index):
+        self.head_dim, self.device_index = head_dim, device_index
+
+
+def _rope_side(x, out, what, where):
+    """(pointer, stride, rows, heads, pointer, stride) of a side and where it goes, which has its shape."""
+    px, ldx, n, heads = _head_rows(x, what, where)
+    po, ldo, no, ho = _head_rows(out, what + "_out", where)
+    if no != n or ho != heads:
+        raise ValueError(f"{what}_out must have the shape of {what}")
+    return px, ldx, n, heads, po, ldo
+
+
+def _rope_on(ctx, rope, batch, head_dim):
+    where = _HeadsOn(head_dim, batch.device_index)
+    if ctx.device is None or where.device_index != (ctx.device.index or 0):
+        raise ValueError("the batch must be on the context's device")
+    if rope.device_index is not None and rope.device_index != where.device_index:
+        raise ValueError("the rotation's tensors must be on the context's device")
+    if rope.head_dim != head_dim:
+        raise ValueError("the rotation is of another head_dim than the cache")
+    return where
+
+
+def lora_head_rope(ctx: Context, rope: HeadRope, batch: KvBatch, q: torch.Tensor | None, k: torch.Tensor | None,
+                   q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Norms and rotation of q and k (bf16 [n, heads, head_dim]; either may be None) by the
+    positions of the batch's new tokens, into q_out and k_out (None: in place)."""
+    if q is None and k is None:
+        raise ValueError("q or k has to be there")
+    where = _rope_on(ctx, rope, batch, rope.head_dim)
+    pq, ldq, nq, hq, pqo, ldqo = (0,) * 6 if q is None else _rope_side(q, q if q_out is None else q_out, "q", where)
+    pk, ldk, nk, hk, pko, ldko = (0,) * 6 if k is None else _rope_side(k, k if k_out is None else k_out, "k", where)
+    if q is not None and k is not None and nq != nk:
+        raise ValueError("q and k must have one row a token")
+    rc = _L.lora_head_rope(ctx.handle, rope._ref, batch._ref, nk if q is None else nq, pq, ldq, hq, pqo, ldqo,
+                           pk, ldk, hk, pko, ldko, _raw_stream(stream, ctx))
+    if rc:
+        _check(rc, ctx)
+
+
+def lora_kv_write_rope(ctx: Context, cache: KvCache, rope: HeadRope, batch: KvBatch, q: torch.Tensor | None,
+                       k: torch.Tensor, v: torch.Tensor, q_out: torch.Tensor | None = None, stream=None):
+    """lora_head_rope and lora_kv_write in one pass: q, normed and rotated, into q_out (None:
+    in place), k, normed and rotated, and v, as it is, into their cells."""
+    where = _rope_on(ctx, rope, batch, cache.head_dim)
+    if where.device_index != cache.device_index:
+        raise ValueError("the batch must be on the context's device")
+    pk, ldk, n, hk = _head_rows(k, "k", cache)
+    pv, ldv, nv, hv = _head_rows(v, "v", cache)
+    pq, ldq, nq, hq, pqo, ldqo = (0, 0, n, 0, 0, 0) if q is None else _rope_side(q, q if q_out is None else q_out, "q", where)
+    if nv != n or nq != n or hk != cache.n_heads or hv != cache.n_heads:
+        raise ValueError("q, k and v must have one row a token, k and v the cache's heads")
+    rc = _L.lora_kv_write_rope(ctx.handle, cache.handle, rope._ref, batch._ref, n, pq, ldq, hq, pqo, ldqo,
+                               pk, ldk, pv, ldv, _raw_stream(stream, ctx))
+    if rc:
+        _check(rc, ctx)
+
+
+def _ints(t: torch.Tensor, what: str, device: int, n: int | None = None) -> int:
+    """Pointer of a contiguous 1-D int32 tensor (of n elements) on a device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{what} must be a CUDA tensor")
+    if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{what} must be a contiguous int32 tensor [{'n' if n is None else n}]")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on the context's device")
+    return t.data_ptr()
+
+
+class PageTable:
+    """Which sequence holds which pages (see include/lora.h): lens [n_seqs], pages [n_seqs,
+    n_cols] and refs [n_pages], int32 CUDA tensors that the lora_pages_* calls change.  lens and
+    pages may be a KvBatch's."""
+
+    def __init__(self, lens: torch.Tensor, pages: torch.Tensor, refs: torch.Tensor, page_size: int):
+        for t, nm, dim in ((lens, "lens", 1), (pages, "pages", 2), (refs, "refs", 1)):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dim or \
+                    (t.numel() and t.stride(-1) != 1):
+                raise ValueError(f"{nm} must be a {dim}-D int32 tensor, contiguous in its last dimension")
+        if pages.shape[0] != lens.shape[0]:
+            raise ValueError("shapes: lens [n_seqs], pages [n_seqs, n_cols], refs [n_pages]")
+        if pages.shape[0] > 1 and pages.stride(0) < pages.shape[1]:
+            raise ValueError("the rows of pages overlap")
+        self.lens, self.pages, self.refs, self.page_size = lens, pages, refs, int(page_size)
+        a = _lib.PageTableArgs()
+        a.lens, a.pages, a.refs = _dev_ptr(lens, "lens"), _dev_ptr(pages, "pages"), _dev_ptr(refs, "refs")
+        self.device_index = lens.get_device()
+        if pages.get_device() != self.device_index or refs.get_device() != self.device_index:
+            raise ValueError("lens, pages and refs must be on one device")
+        a.n_seqs, a.n_cols = pages.shape
+        a.ld_pages = max(pages.stride(0), pages.shape[1]) if pages.shape[0] > 1 else pages.shape[1]
+        a.n_pages, a.page_size = refs.shape[0], self.page_size
+        self._args = a
+        self._ref = ctypes.addressof(a)
+
+
+def _table_on(ctx: Context, table: PageTable) -> int:
+    if ctx.device is None or table.device_index != (ctx.device.index or 0):
+        raise ValueError("the page table must be on the context's device")
+    return table.device_index
+
+
+def lora_pages_extend(ctx: Context, table: PageTable, grow: torch.Tensor, got: torch.Tensor, src: torch.Tensor,
+                      dst: torch.Tensor, cells: torch.Tensor, stream=None):
+    """Sequence s grows by grow[s] tokens, as far as the free pages go: got[s] is what it got.
+    src, dst and cells are the pages to copy (lora_kv_copy) before the new tokens are written.
+    All int32 [n_seqs]."""
+    dev, n = _table_on(ctx, table), table.lens.shape[0]
+    rc = _L.lora_pages_extend(ctx.handle, table._ref, *(_ints(t, nm, dev, n) for t, nm in (
+        (grow, "grow"), (got, "got"), (src, "src"), (dst, "dst"), (cells, "cells"))), _raw_stream(stream, ctx))
+    if rc:
+        _check(rc, ctx)
+
+
+def lora_pages_fork(ctx: Context, table: PageTable, parents: torch.Tensor, children: torch.Tensor, stream=None):
+    """Sequence children[i], empty so far, becomes a copy of parents[i] that shares its pages."""
+    dev = _table_on(ctx, table)
+    n = children.shape[0]
+    rc = _L.lora_pages_fork(ctx.handle, table._ref, _ints(parents, "parents", dev, n), _ints(children, "children", dev), n,
+                            _raw_stream(stream, ctx))
+    if rc:
+        _check(rc, ctx)
+
+
+def lora_pages_free(ctx: Context, table: PageTable, seqs: torch.Tensor, keep: torch.Tensor | None = None, stream=None):
+    """Sequence seqs[i] is cut to its first keep[i] tokens (None: none) and gives the other pages back."""
+    dev = _table_on(ctx, table)
+    n = seqs.shape[0]
+    rc = _L.lora_pages_free(ctx.handle, table._ref, _ints(seqs, "seqs", dev),
+                            None if keep is None else _ints(keep, "keep", dev, n), n, _raw_stream(stream, ctx))
+    if rc:
+        _check(rc, ctx)
+
+
+def lora_pages_compact(ctx: Context, table: PageTable, src: torch.Tensor, dst: torch.Tensor,
+                       top: torch.Tensor | None = None, stream=None):
+    """Moves held pages to the front of the pool, as many as src and dst (int32 [n]) list: the
+    moves for lora_kv_copy, -1 behind the last.  top (int32 [1]) becomes the end of the highest
+    held page."""
+    dev = _table_on(ctx, table)
+    n = src.shape[0]
+    rc = _L.lora_pages_compact(ctx.handle, table._ref, _ints(src, "src", dev), _ints(dst, "dst", dev, n), n,
+                               None if top is None else _ints(top, "top", dev, 1), _raw_stream(stream, ctx))
+    if rc:
+        _check(rc, ctx)
+
+
+def lora_kv_copy(ctx: Context, caches, src: torch.Tensor, dst: torch.Tensor, cells: torch.Tensor | None = None,
+                 stream=None):
+    """Page src[i] to page dst[i] in every one of `caches` (a KvCache or a sequence of them, alike in
+    page size, heads, head_dim and format): the first cells[i] cells, or all.  src[i] < 0: nothing."""
+    if isinstance(caches, KvCache):
+        caches = (caches,)
+    if not caches or ctx.device is None:
+        raise ValueError("no caches, or a context without a device")
+    dev, n = ctx.device.index or 0, src.shape[0]
+    handles = (ctypes.c_void_p * len(caches))(*[c.handle for c in caches])
+    rc = _L.lora_kv_copy(ctx.handle, handles, len(caches), _ints(src, "src", dev), _ints(dst, "dst", dev, n),
+                         None if cells is None else _ints(cells, "cells", dev, n), n, _raw_stream(stream, ctx))
+    if rc:
+        _check(rc, ctx)
+
+
+class BlockSelection:
+    """The pages chosen for each row and key head (see include/lora.h): lens int32 [rows] and pages
+    int32 [rows, key heads, blocks], contiguous CUDA tensors that lora_block_select writes and
+    lora_block_attention reads."""
+
+    def __init__(self, lens: torch.Tensor, pages: torch.Tensor):
+        for t, nm, dim in ((lens, "lens", 1), (pages, "pages", 3)):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+                raise ValueError(f"{nm} must be a contiguous {dim}-D int32 tensor")
+        if pages.shape[0] != lens.shape[0]:
+            raise ValueError("shapes: lens [rows], pages [rows, key heads, blocks]")
+        self.lens, self.pages = lens, pages
+        a = _lib.BlockSel()
+        a.lens, a.pages = _dev_ptr(lens, "lens"), _dev_ptr(pages, "pages")
+        self.device_index = lens.get_device()
+        if pages.get_device() != self.device_index:
+            raise ValueError("lens and pages must be on one device")
+        a.n_rows, self.heads, a.blocks = pages.shape
+        self._args = a
+        self._ref = ctypes.addressof(a)
+
+    @classmethod
+    def empty(cls, rows: int, cache: KvCache, blocks: int) -> "BlockSelection":
+        """A selection with new tensors for up to `rows` rows over a cache."""
+        dev = cache.k_pool.device
+        return cls(torch.empty(rows, dtype=torch.int32, device=dev),
+                   torch.empty((rows, cache.n_heads, blocks), dtype=torch.int32, device=dev))
+
+
+def lora_kv_bounds(ctx: Context, cache: KvCache, batch: KvBatch, rows: int, stream=None):
+    """Brings up to date the attached bounds of the pages in which the batch's new tokens (`rows`
+    of them, already written) lie."""
+    if batch.device_index != cache.device_index:
+        raise ValueError("the batch must be on the context's device")
+    rc = _L.lora_kv_bounds(ctx.handle, cache.handle, batch._ref, rows, _raw_stream(stream, ctx))
+    if rc:
+        _check(rc, ctx)
+
+
+def _selected(cache: KvCache, selection: BlockSelection, rows: int):
+    if selection.device_index != cache.device_index:
+        raise ValueError("the selection must be on the context's device")
+    if selection.heads != cache.n_heads or selection.lens.shape[0] < rows:
+        raise ValueError("the selection must have the cache's heads and a place for every row")
+
+
+def lora_block_select(ctx: Context, cache: KvCache, batch: KvBatch, q: torch.Tensor, selection: BlockSelection,
+                      first: int = 1, last: int = 1, stream=None):
+    """Chooses pages for the batch's new tokens (q, bf16 [n, heads, head_dim]): the first and the
+    last ones, and those whose bounds score highest."""
+    pq, ldq, n, hq = _head_rows(q, "q", cache)
+    if batch.device_index != cache.device_index:
+        raise ValueError("the batch must be on the context's device")
+    _selected(cache, selection, n)
+    rc = _L.lora_block_select(ctx.handle, cache.handle, batch._ref, n, pq, ldq, hq, first, last, selection._ref,
+                              _raw_stream(stream, ctx))
+    if rc:
+        _check(rc, ctx)
+
+
+def lora_block_attention(ctx: Context, cache: KvCache, selection: BlockSelection, q: torch.Tensor, out: torch.Tensor,
+                         scale: float | None = None, stream=None):
+    """out <- attention of q (bf16 [n, heads, head_dim]) over the pages chosen for each row.
+    scale: None for head_dim ** -0.5."""
+    pq, ldq, n, hq = _head_rows(q, "q", cache)
+    po, ldo, no, ho = _head_rows(out, "out", cache)
+    if no != n or ho != hq:
+        raise ValueError("out must have the shape of q")
+    _selected(cache, selection, n)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    rc = _L.lora_block_attention(ctx.handle, cache.handle, selection._ref, n, pq, ldq, hq, scale, po, ldo,
+                                 _raw_stream(stream, ctx))
     if rc:
         _check(rc, ctx)
 

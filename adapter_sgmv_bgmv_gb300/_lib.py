@@ -43,6 +43,23 @@ class KvBatchArgs(ctypes.Structure):
                 ("ld_pages", I64), ("max_new", I64)]
 
 
+class Rope(ctypes.Structure):
+    """lora_rope (include/lora.h)."""
+    _fields_ = [("q_weight", P), ("k_weight", P), ("freqs", P), ("eps", F), ("head_dim", I),
+                ("rot_dim", I), ("interleaved", I)]
+
+
+class PageTableArgs(ctypes.Structure):
+    """lora_page_table (include/lora.h)."""
+    _fields_ = [("lens", P), ("pages", P), ("refs", P), ("n_seqs", I64), ("n_cols", I64),
+                ("ld_pages", I64), ("n_pages", I64), ("page_size", I)]
+
+
+class BlockSel(ctypes.Structure):
+    """lora_block_sel (include/lora.h)."""
+    _fields_ = [("lens", P), ("pages", P), ("n_rows", I64), ("blocks", I)]
+
+
 SIGNATURES = {
     "lora_version": ([], I),
     "lora_strerror": ([I], ctypes.c_char_p),
@@ -69,6 +86,17 @@ SIGNATURES = {
     "lora_kv_write": ([P, P, P, I64, P, I64, P, I64, P], I),
     "lora_kv_read": ([P, P, P, I64, P, I64, P, I64, P], I),
     "lora_attention": ([P, P, P, I64, P, I64, I, F, I, I, P, I64, P], I),
+    "lora_head_rope": ([P, P, P, I64, P, I64, I, P, I64, P, I64, I, P, I64, P], I),
+    "lora_kv_write_rope": ([P, P, P, P, I64, P, I64, I, P, I64, P, I64, P, I64, P], I),
+    "lora_pages_extend": ([P, P, P, P, P, P, P, P], I),
+    "lora_pages_fork": ([P, P, P, P, I64, P], I),
+    "lora_pages_free": ([P, P, P, P, I64, P], I),
+    "lora_pages_compact": ([P, P, P, P, I64, P, P], I),
+    "lora_kv_copy": ([P, P, I, P, P, P, I64, P], I),
+    "lora_kv_attach_bounds": ([P, P, P], I),
+    "lora_kv_bounds": ([P, P, P, I64, P], I),
+    "lora_block_select": ([P, P, P, I64, P, I64, I, I, I, P, P], I),
+    "lora_block_attention": ([P, P, P, I64, P, I64, I, F, P, I64, P], I),
     "lora_selftest_timeout": ([P, I64, P], I),
     "lora_tiles_load": ([P, ctypes.c_char_p], I),
     "lora_tiles_save": ([P, ctypes.c_char_p], I),

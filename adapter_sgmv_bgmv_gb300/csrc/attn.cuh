@@ -261,7 +261,7 @@ __device__ __noinline__ void careful_row(const AttnParams &p, const SeqInfo &s, 
             const int j = j0 + b;
             bool there = j <= pos && sees(pos, j, p.window, p.sinks);
             const int jp = there ? page_of(p.kv, j) : 0;
-            const int page = there ? p.b.pages[int64_t(seq) * p.b.ld_pages + jp] : -1;
+            const int page = there ? p.b.pages[int64_t(seq) * p.b.ld_pages + head * p.b.head_pages + jp] : -1;
             there = page >= 0 && page < p.kv.n_pages;
             const int cell = j - jp * p.kv.page_size;
             const int64_t at = there ? page * p.kv.page_stride + cell * p.kv.cell_stride + head * p.kv.head_stride : 0;

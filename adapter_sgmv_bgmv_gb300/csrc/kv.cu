@@ -26,6 +26,7 @@
 #include "ptx.cuh"
 
 #include "kv.cuh"
+#include "kv_rows.cuh"
 
 namespace lora {
 
@@ -33,56 +34,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxRows = kThreads / 32;      // rows a CTA: a warp looks up each
-
-// Row `row`'s place in the cache, found by a whole warp: byte offset of the page's
-// cell in the pools (without the head) and element offset in the scales.
-struct Place {
-    bool live;                // the row belongs to a sequence of the batch
-    bool stored;              // ... and has a position and a valid page
-    int64_t at, s_at;
-};
-
-__device__ __forceinline__ Place find_row(const KvView &kv, const BatchView &b, int row,
-                                          unsigned *status)
-{
-    const int lane = threadIdx.x & 31;
-    Place pl{false, false, 0, 0};
-    // A decode batch has one row per sequence: row r is sequence r.  Otherwise a
-    // 32-way search for the last sequence that starts at or before the row.
-    int s = row;
-    bool hit = s < b.n_seqs && b.starts[s] == row && b.starts[s + 1] == row + 1;
-    if (!hit) {
-        int lo = 0, n = b.n_seqs;                    // starts[lo] <= row, answer in [lo, lo + n)
-        while (n > 1) {
-            const int step = (n + 31) / 32;
-            const int i = lo + lane * step;
-            const bool le = lane * step < n && b.starts[i] <= row;
-            const unsigned m = __ballot_sync(0xffffffffu, le);
-            const int last = m ? 31 - __clz(m) : 0;
-            n = min(step, n - last * step);
-            lo += last * step;
-        }
-        s = lo;
-    }
-    const SeqInfo q = seq_info(b, s, status);
-    if (row < q.start || row >= q.start + q.n_new)
-        return pl;
-    pl.live = true;
-    const int pos = q.len - q.n_new + (row - q.start);
-    if (pos < 0)
-        return pl;
-    const int j = page_of(kv, pos);
-    const int page = b.pages[int64_t(s) * b.ld_pages + j];
-    if (page < 0 || page >= kv.n_pages) {
-        raise_status(status, kDevBadPage);
-        return pl;
-    }
-    const int cell = pos - j * kv.page_size;
-    pl.stored = true;
-    pl.at = page * kv.page_stride + cell * kv.cell_stride;
-    pl.s_at = page * kv.s_page + cell * kv.s_cell;
-    return pl;
-}
 
 // `rows` rows from the CTA's first: their vectors one after another, kPer at a time.
 template <int DIM, int FMT>

@@ -30,6 +30,10 @@ struct KvView {
     int heads;
     int dim;
     int format;
+    // each page's smallest and largest keys, where the cache has them (bounds below): codes
+    // at bounds[((page * heads + head) * 2 + side) * dim + d], units at unit[page * heads + head]
+    int8_t *bounds;
+    float *unit;
 };
 
 // The sequences of one call: rows [starts[s], starts[s + 1]) of q / k / v are the last
@@ -42,6 +46,9 @@ struct BatchView {
     int n_rows;               // rows of q / k / v
     int max_new;              // upper bound on a sequence's new tokens
     int capacity;             // positions the page table has room for
+    // Without `starts`, row s is sequence s (none where lens[s] is negative), and each key head
+    // has a page list of its own, head_pages apart.
+    int64_t head_pages;
 };
 
 // i / d by a product, for 0 <= i and i * d < 2^32.
@@ -100,6 +107,70 @@ struct AttnParams {
 cudaError_t launch_attn_rows(const AttnParams &p, int sms, cudaStream_t stream);
 cudaError_t launch_attn_tc(const AttnParams &p, int sms, cudaStream_t stream);
 
+// Norm and rotation of heads (rope.cu), of a row's q_heads queries and k_heads keys; with
+// `kv.k`, keys and values go to their cells instead of k_out.
+struct RopeParams {
+    KvView kv;
+    BatchView b;
+    const uint16_t *q, *k, *v;
+    uint16_t *q_out, *k_out;
+    int64_t ldq, ldk, ldv, ldqo, ldko;
+    int q_heads, k_heads, dim, half, interleaved;
+    const float *q_weight, *k_weight, *freqs;
+    float eps;
+    Divider per_row;          // by a row's vectors
+    unsigned *status;
+};
+cudaError_t launch_rope(const RopeParams &p, bool store, cudaStream_t stream);
+
+// Page tables (pages.cu).
+struct TableView {
+    int32_t *lens, *pages, *refs;
+    int64_t ld_pages;
+    int n_seqs, n_cols, n_pages, page_size;
+    int capacity;             // positions a sequence's row has room for
+    unsigned *status;
+};
+constexpr int kMaxTableSeqs = 16384;
+cudaError_t launch_pages_extend(const TableView &t, const int32_t *grow, int32_t *got, int32_t *src,
+                                int32_t *dst, int32_t *cells, cudaStream_t stream);
+cudaError_t launch_pages_fork(const TableView &t, const int32_t *from, const int32_t *to, int n, cudaStream_t stream);
+cudaError_t launch_pages_free(const TableView &t, const int32_t *seqs, const int32_t *keep, int n, cudaStream_t stream);
+cudaError_t launch_pages_compact(const TableView &t, int32_t *src, int32_t *dst, int n, int32_t *top, int *launches,
+                                 cudaStream_t stream);
+
+// Copies of pages within each of some caches of one shape (copy.cu).
+constexpr int kMaxCopyCaches = 64;
+struct KvCopyParams {
+    KvView kv[kMaxCopyCaches];
+    const int32_t *src, *dst, *cells;
+    int n, n_kv;
+    unsigned *status;
+};
+cudaError_t launch_kv_copy(const KvCopyParams &p, int sms, cudaStream_t stream);
+
+// Bounds of pages, and the choice of pages by them (blocks.cu).
+struct BoundsParams {
+    KvView kv;
+    BatchView b;
+    unsigned *status;
+};
+cudaError_t launch_kv_bounds(const BoundsParams &p, cudaStream_t stream);
+
+constexpr int kMaxSelectCols = 1 << 18;
+constexpr int kMaxSelectGroup = 128;
+struct SelectParams {
+    KvView kv;
+    BatchView b;
+    int n_cols;
+    const uint16_t *q;
+    int64_t ldq;
+    int group, blocks, first, last;
+    int32_t *lens, *pages;    // of the selection: [n_rows], [n_rows][heads][blocks]
+    unsigned *status;
+};
+cudaError_t launch_block_select(const SelectParams &p, int sms, cudaStream_t stream);
+
 #ifdef __CUDACC__
 struct SeqInfo {
     int start, n_new, len;
@@ -110,6 +181,17 @@ struct SeqInfo {
 __device__ __forceinline__ SeqInfo seq_info(const BatchView &b, int s, unsigned *status)
 {
     SeqInfo q;
+    if (!b.starts) {
+        q.start = s;
+        q.len = b.lens[s];
+        q.n_new = q.len >= 0;
+        q.len = max(q.len, 0);
+        if (q.len > b.capacity) {
+            raise_status(status, kDevBadBatch);
+            q.n_new = q.len = 0;
+        }
+        return q;
+    }
     q.start = b.starts[s];
     const int end = b.starts[s + 1];
     q.len = b.lens[s];

@@ -518,14 +518,161 @@ int lora_attention(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch,
                    const void *q, int64_t ldq, int n_heads, float scale, int window,
                    int sinks, void *out, int64_t ldo, void *stream);
 
+/* ------------------------------------------------------------ norms and rotation of heads
+ *
+ * What lies between a projection and the cache: each head's vector x of head_dim elements is
+ * normed, where its side has a weight,
+ *     x_d <- x_d / sqrt(mean(x^2) + eps) * weight_d
+ * and the pairs of its first rot_dim elements are turned by the row's position p,
+ *     (a, b) <- (a cos t - b sin t, a sin t + b cos t),   t = p * freqs[j],  j < rot_dim / 2
+ * a, b = x_j, x_(j + rot_dim / 2), or x_2j, x_(2j + 1) when interleaved.  In fp32, rounded once
+ * at the end; t is exact to 2^-32 turns at any position.
+ *
+ * head_dim is a multiple of 8 up to 256, rot_dim one of 16 up to head_dim (0: no rotation).
+ * Weights are fp32 [head_dim] on 16-byte boundaries, or null: no norm on that side.  freqs are
+ * fp32 [rot_dim / 2], radians a token, of magnitude up to 2^20 (beyond: NaN).  All are device
+ * memory that stays the caller's. */
+typedef struct {
+    const float *q_weight, *k_weight, *freqs;
+    float eps;
+    int head_dim, rot_dim, interleaved;
+} lora_rope;
+
+/* Rows q [n][q_heads * head_dim] and k [n][k_heads * head_dim] (bf16) to q_out and k_out;
+ * positions are the batch's (its pages are not looked at).  Either side may have no heads.
+ * q_out may be q with the same stride, k_out k; other overlaps are not allowed.  A row without
+ * a position becomes zeros, rows past the last sequence are left alone. */
+int lora_head_rope(lora_ctx *ctx, const lora_rope *rope, const lora_kv_batch *batch, int64_t n,
+                   const void *q, int64_t ldq, int q_heads, void *q_out, int64_t ldqo,
+                   const void *k, int64_t ldk, int k_heads, void *k_out, int64_t ldko, void *stream);
+
+/* The same, with the keys and the values (as they are) stored in their cells: lora_head_rope
+ * and lora_kv_write in one pass.  In a bf16 cache the result is the same bits as theirs; 8-bit
+ * codes are taken from the fp32 keys, without a rounding to bf16 between.  q may have no heads. */
+int lora_kv_write_rope(lora_ctx *ctx, const lora_kv *kv, const lora_rope *rope,
+                       const lora_kv_batch *batch, int64_t n, const void *q, int64_t ldq, int q_heads,
+                       void *q_out, int64_t ldqo, const void *k, int64_t ldk, const void *v,
+                       int64_t ldv, void *stream);
+
+/* ------------------------------------------------------------ page tables
+ *
+ * Which sequence holds which pages, in device memory: lens and pages as in lora_kv_batch (the
+ * same arrays serve both), and refs [n_pages], the sequences that hold a page (0: free).  The
+ * calls below change all three; they run in stream order, never read them on the host, and can be
+ * captured.  The first ceil(lens[s] / page_size) entries of a row count; others are not looked
+ * at (the calls leave -1 behind).  A model's layers share one table: what has to be copied
+ * is listed, and lora_kv_copy does it in every layer's cache.  A page that something other than
+ * these sequences uses is kept out of the free ones by a count of its own in refs.
+ *
+ * Results do not depend on timing.  What is out of range is left as it was, and
+ * lora_sync_status returns LORA_E_INVAL (a sequence, a length, a list) or LORA_E_PAGE (a page
+ * id, or a count that would fall below 0).  LORA_E_CAPACITY: more than 16384 sequences (or
+ * entries of a list), 2^30 pages, page_size above 2^20. */
+typedef struct {
+    int32_t *lens;                 /* [n_seqs] */
+    int32_t *pages;                /* [n_seqs][ld_pages], n_cols of them used */
+    int32_t *refs;                 /* [n_pages] */
+    int64_t n_seqs, n_cols, ld_pages, n_pages;
+    int page_size;
+} lora_page_table;
+
+/* Sequence s grows by grow[s] tokens (<= 0: not), in order: lens[s] rises, missing pages are
+ * the lowest free ones.  Where its last page has room and others hold it too, the sequence gets
+ * a page of its own for it: src[s], dst[s], cells[s] say what lora_kv_copy has to copy before
+ * the next write (else -1, -1, 0); of sequences that write into one page in one call the last
+ * keeps it, if nobody else holds it.  got[s] is grow[s], or 0 for a sequence that stays as it
+ * is: the first for which the free pages do not suffice and all that grow after it, and one that
+ * would outgrow its row.  All arrays are [n_seqs]. */
+int lora_pages_extend(lora_ctx *ctx, const lora_page_table *table, const int32_t *grow, int32_t *got,
+                      int32_t *src, int32_t *dst, int32_t *cells, void *stream);
+
+/* Sequence to[i], empty so far (length 0), becomes a copy of sequence from[i]: the same length
+ * and pages, held once more.  A child listed twice takes the first; from[i] may not be in `to`. */
+int lora_pages_fork(lora_ctx *ctx, const lora_page_table *table, const int32_t *from,
+                    const int32_t *to, int64_t n, void *stream);
+
+/* Sequence seqs[i] is cut to its first keep[i] tokens (keep null: none), and gives back the
+ * pages behind them; one that is no longer stays as it is.  A sequence listed twice: the first. */
+int lora_pages_free(lora_ctx *ctx, const lora_page_table *table, const int32_t *seqs,
+                    const int32_t *keep, int64_t n, void *stream);
+
+/* Moves the held pages to the front of the pool: with L of them, the highest one goes to the
+ * lowest free page, and so on until all are below L, or n have moved.  src and dst [n] are the
+ * moves, for lora_kv_copy, then -1; the tables and refs already name the new places.  *top (or
+ * null) becomes the end of the highest held page: what is behind it can serve something else. */
+int lora_pages_compact(lora_ctx *ctx, const lora_page_table *table, int32_t *src, int32_t *dst,
+                       int64_t n, int32_t *top, void *stream);
+
+/* Copies page src[i] to page dst[i] (i < n, device memory; src[i] < 0: nothing) within each of
+ * n_kv caches of one page size, heads, head_dim and format: keys, values, scales and
+ * attached bounds, the first cells[i] cells of a page or, with cells null, all.  Destinations
+ * differ from one another and from every source, else the content of those pages is of no
+ * use.  A page id that a cache does not have is skipped (LORA_E_PAGE).  LORA_E_CAPACITY: page_size
+ * * n_heads above 2^24. */
+int lora_kv_copy(lora_ctx *ctx, const lora_kv *const *kvs, int n_kv, const int32_t *src,
+                 const int32_t *dst, const int32_t *cells, int64_t n, void *stream);
+
+/* ------------------------------------------------------------ attention over chosen pages
+ *
+ * For long contexts: every new token looks, for each key head, at `blocks` of its pages only:
+ * the first ones, the last ones, and those of the rest that score highest by the bounds of their
+ * keys.  Per step: lora_kv_write, lora_kv_bounds, lora_block_select, lora_block_attention.
+ * One pass over a row's pages for each row: for decoding and for a few tokens at once; a long
+ * prompt is sooner served whole by lora_attention.
+ *
+ * Bounds are caller-owned device memory attached to a cache: codes int8 [n_pages][n_heads][2]
+ * [head_dim] on a 16-byte boundary and unit fp32 [n_pages][n_heads].  lo and hi are the smallest and
+ * the largest value of each element among a page's keys (as fp32, scale * code in 8-bit caches);
+ * unit = 2^(e - 6) with 2^e <= max(|lo|, |hi|) < 2^(e + 1), e >= -100; codes are lo / unit and
+ * hi / unit to the nearest, ties to even, within +-127.  A page with a key that is not finite gets
+ * unit NaN and zero codes.  lora_kv_attach_bounds(kv, NULL, NULL) detaches.  Not while another
+ * thread's call uses the cache. */
+int lora_kv_attach_bounds(lora_kv *kv, void *codes, float *unit);
+
+/* Brings up to date the bounds of the pages in which the batch's new tokens (n rows) lie, over
+ * the tokens of the sequence that lie in them.  Call it once the tokens are written. */
+int lora_kv_bounds(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch, int64_t n,
+                   void *stream);
+
+/* What was chosen, caller-owned device memory: for row i < n_rows and key head h the page ids
+ * pages[(i * n_heads + h) * blocks ...] in the order of the sequence, -1 behind the last, and
+ * lens[i], the tokens in them that the row sees (the same for every head): 0 for a row without
+ * a position, -1 for one of no sequence. */
+typedef struct {
+    int32_t *lens, *pages;
+    int64_t n_rows;
+    int blocks;
+} lora_block_sel;
+
+/* The choice for the batch's n new tokens.  A row at position p sees pages 0 .. p / page_size; if
+ * they are more than sel->blocks, it takes the first `first`, the last `last` (at least 1: its
+ * own), and of the others those with the highest score, equal ones in the order of the sequence:
+ *     max over the query heads g of the key head of unit_page * unit_g * sum_d max(c_d lo_d, c_d hi_d)
+ * with c, unit_g of query head g taken like the bounds' codes, in integers and fp32 products
+ * with powers of two: the choice is the same in any order of summation.  A page whose unit is NaN
+ * comes first, one the cache does not have last (and LORA_E_PAGE); a query head with an infinity or a NaN
+ * has no say.  LORA_E_CAPACITY: more than 2^18 columns, 128 query heads a key head, or
+ * blocks * page_size above 2^30. */
+int lora_block_select(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch, int64_t n,
+                      const void *q, int64_t ldq, int n_heads, int first, int last,
+                      const lora_block_sel *sel, void *stream);
+
+/* lora_attention of n rows over the pages chosen for them (the fp32 and two-term weights of its
+ * few-rows form): row i sees the first lens[i] tokens of its lists.  Rows with lens[i] < 0 are
+ * left alone.  The selection may also be the caller's own. */
+int lora_block_attention(lora_ctx *ctx, const lora_kv *kv, const lora_block_sel *sel, int64_t n,
+                         const void *q, int64_t ldq, int n_heads, float scale, void *out,
+                         int64_t ldo, void *stream);
+
 /* Kernels launched by this context since it was created. */
 int64_t lora_launch_count(const lora_ctx *ctx);
 
 /* Which kernel the last call launched: 0 none, 1 row-gather, 2 tensor-core tile,
  * 3 both (delta calls), 4 merge / unmerge, 8 page-in, 16 base projection GEMM (with
  * the bits of the shrink kernels lora_base_fused launched before it), 32 cache write /
- * read, 64 attention of few rows, 128 attention of many rows; and how many
- * kernels it launched. */
+ * read, 64 attention of few rows, 128 attention of many rows, 256 norms and rotation of heads,
+ * 512 page tables, 1024 page copies, 2048 bounds and choice of pages; and how many kernels it
+ * launched. */
 int lora_last_path(const lora_ctx *ctx, int *n_launches);
 
 const char *lora_strerror(int code);

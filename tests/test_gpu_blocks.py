@@ -1,0 +1,300 @@
+"""Bounds of pages, the choice of pages by them and attention over what is chosen, against the models
+in integers and 64 bits."""
+import math
+import random
+
+import pytest
+import torch
+
+from tests._kv_ref import Case, assert_attention, raw
+from tests._step_ref import bounds, chosen_attention, select
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    import adapter_sgmv_bgmv_gb300 as L
+    c = L.Context(0, max_rows=1024)
+    yield c
+    c.close()
+
+
+class Step:
+    """A Case with its cache and bounds, those of every page filled as earlier steps would have."""
+
+    def __init__(self, ctx, case, max_new=None):
+        import adapter_sgmv_bgmv_gb300 as L
+        self.L, self.ctx, self.c = L, ctx, case
+        self.cache = L.KvCache(ctx, case.k_pool, case.v_pool, case.k_scale, case.v_scale)
+        n = case.k_pool.shape[0]
+        self.codes = torch.full((n, case.kv_heads, 2, case.dim), 55, dtype=torch.int8, device="cuda")
+        self.unit = torch.full((n, case.kv_heads), 3.0, device="cuda")
+        self.cache.attach_bounds(self.codes, self.unit)
+        self.batch = L.KvBatch(case.starts, case.lens_t, case.pages, max_new=max_new)
+
+    def fill(self):
+        """Bounds of all pages, by calls in which every token is new."""
+        c = self.c
+        starts = torch.tensor([0] + c.lens, dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+        if sum(c.lens):
+            self.L.lora_kv_bounds(self.ctx, self.cache, self.L.KvBatch(starts, c.lens_t, c.pages), sum(c.lens))
+
+    def choose(self, blocks, first, last):
+        sel = self.L.BlockSelection.empty(self.c.n + 2, self.cache, blocks)
+        sel.lens.fill_(-7)
+        sel.pages.fill_(-7)
+        self.L.lora_block_select(self.ctx, self.cache, self.batch, self.c.q, sel, first, last)
+        return sel
+
+    def close(self):
+        self.cache.close()
+
+
+def draw(seed):
+    rng = random.Random(seed)
+    kv_heads = rng.choice([1, 1, 2, 3, 4, 8])
+    seqs, hi = rng.choice([(1, 1), (1, 5), (3, 1), (5, 3), (17, 1), (2, 40)])
+    page = rng.choice([1, 3, 16, 16, 24, 64])
+    longest = rng.choice([20, 300, 1200]) * (1 if page < 16 else 2)
+    new = [rng.randint(0 if seqs > 1 else 1, hi) for _ in range(seqs)]
+    lens = [max(n, rng.randint(1, longest)) for n in new]
+    for s in rng.sample(range(seqs), rng.choice([0, seqs // 3])):
+        lens[s], new[s] = 0, 1
+    if sum(new) == 0:
+        new[0] = 1
+        lens[0] = max(1, lens[0])
+    blocks = rng.choice([1, 2, 5, 16, 40])
+    first = rng.randint(0, min(3, blocks - 1))
+    last = rng.randint(1, min(3, blocks - first))
+    return dict(new=new, lens=lens, heads=kv_heads * rng.choice([1, 2, 3, 5, 8, 16, 20]), kv_heads=kv_heads, dim=rng.choice([64, 128]), page=page,
+                fmt=rng.choice(["bf16", "int8", "fp8"]), layout=rng.choice(["split", "joint", "heads", "gaps"])), (blocks, first, last)
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_random_steps(ctx, seed):
+    shape, how = draw(seed)
+    c = Case(seed, **shape)
+    st = Step(ctx, c)
+    was = st.codes.clone(), st.unit.clone()
+    st.L.lora_kv_bounds(ctx, st.cache, st.batch, c.n)
+    ctx.sync_status()
+    assert ctx.last_path() == (2048, 1)
+    want = bounds(c, *was)
+    assert torch.equal(st.codes, want[0]) and torch.equal(st.unit, want[1])
+    st.fill()
+    sel = st.choose(*how)
+    ctx.sync_status()
+    lens, pages = select(c, st.codes, st.unit, *how)
+    assert torch.equal(sel.lens[:c.n].cpu(), lens) and torch.equal(sel.pages[:c.n].cpu(), pages)
+    assert bool((sel.lens[c.n:] == -7).all()) and bool((sel.pages[c.n:] == -7).all())
+    st.L.lora_block_attention(ctx, st.cache, sel, c.q, c.out)
+    ctx.sync_status()
+    assert ctx.last_path() == (64, 1)
+    assert_attention(c.out, *chosen_attention(c, lens, pages))
+    st.close()
+
+
+@pytest.mark.parametrize("n_cols,page,heads,kv_heads", [(2000, 1, 4, 1), (9000, 1, 1, 1), (40000, 1, 2, 2), (1500, 16, 28, 4)])
+def test_long_lists(ctx, n_cols, page, heads, kv_heads):
+    """One (row, head) over a cluster of CTAs."""
+    c = Case(n_cols, [2], [n_cols * page - page // 2], heads, kv_heads, 64, page)
+    st = Step(ctx, c)
+    st.fill()
+    for how in ((7, 2, 3), (300, 0, 1)):
+        sel = st.choose(*how)
+        ctx.sync_status()
+        lens, pages = select(c, st.codes, st.unit, *how)
+        assert torch.equal(sel.lens[:2].cpu(), lens) and torch.equal(sel.pages[:2].cpu(), pages)
+        st.L.lora_block_attention(ctx, st.cache, sel, c.q, c.out)
+        ctx.sync_status()
+        assert_attention(c.out, *chosen_attention(c, lens, pages))
+    st.close()
+
+
+def test_ties_go_to_the_first_pages(ctx):
+    """Equal keys everywhere, queries of zero, and scores of either sign of zero."""
+    c = Case(3, [1, 1], [1000, 900], 4, 2, 64, 4)
+    raw(c.k_pool).copy_(raw(c.k_pool[:1, :1]).expand_as(c.k_pool))
+    c.q[1] = 0
+    st = Step(ctx, c)
+    st.fill()
+    sel = st.choose(9, 2, 3)
+    ctx.sync_status()
+    for s, cols in ((0, 250), (1, 225)):
+        want = c.pages[s][list(range(6)) + list(range(cols - 3, cols))]
+        assert torch.equal(sel.pages[s], want.expand(2, -1))
+    st.close()
+
+
+def test_keys_that_are_not_finite(ctx):
+    """A page with one is chosen ahead of all others; NaNs behind a sequence's end are nobody's."""
+    c = Case(4, [1], [64 * 16 + 3], 2, 1, 64, 16)
+    k, v = c.rand(1, 1, 64), c.rand(1, 1, 64)
+    k[0, 0, 5] = -math.inf
+    c.put(0, [16 * 20 + 7], k, v)
+    k[0, 0, 5] = math.nan
+    c.put(0, [16 * 40 + 2], k, v)
+    st = Step(ctx, c)
+    was = st.codes.clone(), st.unit.clone()
+    st.fill()
+    ctx.sync_status()
+    full = Case.__new__(Case)
+    full.__dict__.update(c.__dict__, new=c.lens)
+    want = bounds(full, *was)
+    assert torch.equal(st.codes, want[0]) and torch.equal(st.unit.nan_to_num(-1), want[1].nan_to_num(-1))
+    sel = st.choose(4, 1, 1)
+    lens, pages = select(c, st.codes, st.unit, 4, 1, 1)
+    assert torch.equal(sel.pages[:1].cpu(), pages)
+    assert sel.pages[0, 0].tolist()[1:3] == [int(c.table[0, 20]), int(c.table[0, 40])]
+    st.L.lora_block_attention(ctx, st.cache, sel, c.q, c.out)
+    ctx.sync_status()
+    assert bool(torch.isnan(c.out[0]).all())
+    # a query head that is not finite has no say; alone, the first pages are as good as any
+    c.q[0, 0, 1] = math.inf
+    sel = st.choose(4, 1, 1)
+    lens, pages = select(c, st.codes, st.unit, 4, 1, 1)
+    ctx.sync_status()
+    assert torch.equal(sel.pages[:1].cpu(), pages)
+    st.close()
+
+
+def test_values_of_chosen_pages_only(ctx):
+    """NaNs in the pages that were not chosen, and behind the row's position, never reach the result."""
+    c = Case(5, [1, 1], [50 * 16 + 5, 30 * 16], 8, 2, 128, 16)
+    st = Step(ctx, c)
+    st.fill()
+    sel = st.choose(6, 1, 2)
+    ctx.sync_status()
+    lens, pages = sel.lens[:2].cpu(), sel.pages[:2].cpu()
+    want = chosen_attention(c, lens, pages)
+    for h in range(2):
+        lost = torch.ones(c.k_pool.shape[0], dtype=torch.bool)
+        lost[pages[:, h].flatten().long()] = False
+        for pool in (c.k_pool, c.v_pool):
+            pool[lost.cuda(), :, h] = math.nan
+    st.L.lora_block_attention(ctx, st.cache, sel, c.q, c.out)
+    ctx.sync_status()
+    assert_attention(c.out, *want)
+    st.close()
+
+
+@pytest.mark.parametrize("gain", [1e-37, 1e-20, 1e18])
+def test_extreme_sizes(ctx, gain):
+    c = Case(6, [1], [500], 4, 2, 64, 8, gain=gain if gain > 1 else 1.0)
+    if gain < 1:
+        c.k_pool.mul_(gain)
+    st = Step(ctx, c)
+    was = st.codes.clone(), st.unit.clone()
+    st.fill()
+    ctx.sync_status()
+    full = Case.__new__(Case)
+    full.__dict__.update(c.__dict__, new=c.lens)
+    want = bounds(full, *was)
+    assert torch.equal(st.codes, want[0]) and torch.equal(st.unit, want[1])
+    sel = st.choose(10, 1, 1)
+    lens, pages = select(c, st.codes, st.unit, 10, 1, 1)
+    ctx.sync_status()
+    assert torch.equal(sel.pages[:1].cpu(), pages)
+    st.close()
+
+
+def test_rows_of_no_sequence_bad_pages_and_bad_sequences(ctx):
+    import adapter_sgmv_bgmv_gb300 as L
+    from adapter_sgmv_bgmv_gb300 import LoraError
+    c = Case(7, [1, 2, 1], [400, 300, 200], 4, 2, 64, 16)
+    st = Step(ctx, c)
+    st.fill()
+    ctx.sync_status()
+    q = torch.cat([c.q, c.rand(2, 4, 64)])
+    out = torch.full_like(q, 7)
+    c.lens_t[1] = 10 ** 6
+    sel = L.BlockSelection.empty(6, st.cache, 5)
+    for call in (lambda: L.lora_kv_bounds(ctx, st.cache, st.batch, 4),
+                 lambda: L.lora_block_select(ctx, st.cache, st.batch, q, sel)):
+        call()
+        with pytest.raises(LoraError) as e:
+            ctx.sync_status()
+        assert e.value.name == "LORA_E_INVAL"
+    assert sel.lens.tolist() == [(4 * 16) + (399 % 16) + 1, -1, -1, 4 * 16 + 199 % 16 + 1, -1, -1]
+    L.lora_block_attention(ctx, st.cache, sel, q, out)
+    ctx.sync_status()
+    assert bool((out[[1, 2, 4, 5]] == 7).all()) and bool((out[[0, 3]] != 7).any(-1).all())
+    c.lens_t[1] = 300
+    c.pages[0, 3], c.pages[2, 12] = -1, 10 ** 6
+    L.lora_kv_bounds(ctx, st.cache, st.batch, 4)
+    with pytest.raises(LoraError) as e:
+        ctx.sync_status()
+    assert e.value.name == "LORA_E_PAGE"
+    L.lora_block_select(ctx, st.cache, st.batch, q, sel)
+    with pytest.raises(LoraError) as e:
+        ctx.sync_status()
+    assert e.value.name == "LORA_E_PAGE"
+    assert -1 not in sel.pages[0].tolist()[0]              # chosen last
+    L.lora_block_attention(ctx, st.cache, sel, q, out)     # the last row's own page is not there
+    with pytest.raises(LoraError) as e:
+        ctx.sync_status()
+    assert e.value.name == "LORA_E_PAGE"
+    st.close()
+
+
+def test_all_pages_chosen_is_attention(ctx):
+    import adapter_sgmv_bgmv_gb300 as L
+    c = Case(8, [1, 3, 1], [100, 77, 0], 8, 2, 128, 16, fmt="int8")
+    st = Step(ctx, c)
+    sel = st.choose(7, 3, 2)
+    L.lora_block_attention(ctx, st.cache, sel, c.q, c.out)
+    ctx.sync_status()
+    want, bound = c.reference()
+    assert_attention(c.out, want, bound)
+    st.close()
+
+
+def test_scale_and_many_heads(ctx):
+    """More query heads than one unit has rows, and a scale of one's own."""
+    c = Case(9, [2], [700], 128, 1, 64, 16, fmt="fp8")
+    st = Step(ctx, c)
+    st.fill()
+    sel = st.choose(12, 1, 1)
+    lens, pages = select(c, st.codes, st.unit, 12, 1, 1)
+    assert torch.equal(sel.pages[:2].cpu(), pages)
+    st.L.lora_block_attention(ctx, st.cache, sel, c.q, c.out, scale=0.31)
+    ctx.sync_status()
+    assert_attention(c.out, *chosen_attention(c, lens, pages, scale=0.31))
+    st.close()
+
+
+def test_results_repeat_and_replay(ctx):
+    """The same bits on every run, on a stream and in replays that follow the lengths; two graphs in turn."""
+    import adapter_sgmv_bgmv_gb300 as L
+    c = Case(10, [1] * 4, [5000, 3000, 40, 2500], 8, 2, 128, 16)
+    st = Step(ctx, c, max_new=1)
+    st.fill()
+    ctx.sync_status()
+    sels = [L.BlockSelection.empty(4, st.cache, b) for b in (20, 6)]
+    outs = [torch.empty_like(c.out) for _ in sels]
+
+    def step(i):
+        L.lora_kv_bounds(ctx, st.cache, st.batch, 4)
+        L.lora_block_select(ctx, st.cache, st.batch, c.q, sels[i], 1, 1)
+        L.lora_block_attention(ctx, st.cache, sels[i], c.q, outs[i])
+    graphs = [torch.cuda.CUDAGraph() for _ in sels]
+    for i, g in enumerate(graphs):
+        step(i)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            step(i)
+    for lens in ([5000, 3000, 40, 2500], [4800, 0, 33, 17], [4801, 1, 34, 18]):
+        c.lens_t.copy_(torch.tensor(lens, dtype=torch.int32))
+        want = []
+        for i in range(2):
+            step(i)
+            ctx.sync_status()
+            want.append((outs[i].clone(), sels[i].pages.clone(), sels[i].lens.clone()))
+        for _ in range(3):
+            for g in graphs:
+                g.replay()
+        ctx.sync_status()
+        for i in range(2):
+            assert torch.equal(outs[i], want[i][0]) and torch.equal(sels[i].pages, want[i][1]) and torch.equal(sels[i].lens, want[i][2])
+    st.close()
