@@ -118,7 +118,7 @@ struct RopeParams {
     int q_heads, k_heads, dim, half, interleaved;
     const float *q_weight, *k_weight, *freqs;
     float eps;
-    Divider per_row;          // by a row's vectors
+    Divider per_row;          // by a row's items (rope.cu)
     unsigned *status;
 };
 cudaError_t launch_rope(const RopeParams &p, bool store, cudaStream_t stream);

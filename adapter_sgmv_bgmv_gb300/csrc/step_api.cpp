@@ -14,7 +14,7 @@ using namespace lora;
 
 namespace {
 
-// Vectors of a row, so that a CTA's rows of them can be numbered and divided in 32 bits.
+// Vectors of a row, so that a CTA's items can be numbered and divided in 32 bits.
 constexpr int64_t kMaxRowVectors = 16384;
 // Cells times heads of a page that is copied: its parts are numbered in 32 bits.
 constexpr int64_t kMaxCopyVectors = 1 << 24;
