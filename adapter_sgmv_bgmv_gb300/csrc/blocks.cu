@@ -74,7 +74,10 @@ __global__ void __launch_bounds__(kThreads) k_kv_bounds(const __grid_constant__ 
     const int row = blockIdx.x * rows + int(threadIdx.x);
     if (int(threadIdx.x) < rows && row < p.b.n_rows) {
         int s = row;
-        if (!(s < p.b.n_seqs && p.b.starts[s] == row && p.b.starts[s + 1] == row + 1)) {
+        const bool may = row < p.b.n_seqs;
+        const int start = may ? p.b.starts[row] : -1, end = may ? p.b.starts[row + 1] : -1, len = may ? p.b.lens[row] : 0;
+        const bool hit = start == row && end == row + 1;
+        if (!hit) {
             int lo = 0, hi = p.b.n_seqs - 1;         // the last sequence that starts at or before the row
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
@@ -85,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_bounds(const __grid_constant__ 
             }
             s = lo;
         }
-        const SeqInfo q = seq_info(p.b, s, p.status);
+        const SeqInfo q = hit ? checked_seq(p.b, start, end, len, p.status) : seq_info(p.b, s, p.status);
         const int pos = q.len - q.n_new + (row - q.start);
         if (row >= q.start && row < q.start + q.n_new && pos >= 0) {
             const int col = page_of(kv, pos), cell = pos - col * kv.page_size;
@@ -213,9 +216,11 @@ cudaError_t launch(const BoundsParams &p, cudaStream_t stream)
 // ---------------------------------------------------------------- select
 
 constexpr int kMaxCluster = 8;
-constexpr int kPassBits[3] = {11, 11, 10};
-constexpr int kBins = 1 << 11;
-constexpr int kMaxShare = 1 << 15;           // columns of a CTA: four bytes of shared memory each
+constexpr int kSelThreads = 256;
+constexpr int kSelCtas = 3;                  // a SM
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 256;                   // of a pass over eight bits of the keys
+constexpr int kTile = 16;                    // pages a warp scores at once
 
 // An order-preserving integer of a score; no zero is negative.
 __device__ __forceinline__ uint32_t key_of(float score)
@@ -224,58 +229,76 @@ __device__ __forceinline__ uint32_t key_of(float score)
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ int ld_cluster(const int *local, int rank)
+// 16 pages' bounds by 8 query heads' codes, 32 of the 2 * DIM products at once.
+__device__ __forceinline__ void mma_s8(int c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_cluster(smem_u32(local), uint32_t(rank))) : "memory");
-    return v;
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Exclusive prefix of one small value a thread over the block, and the sum.
-__device__ __forceinline__ int block_prefix(int v, int *sums, int &total)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d)
-            x += y;
-    }
-    __syncthreads();
-    if (lane == 31)
-        sums[warp] = x;
-    __syncthreads();
-    int before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp)
-            before += sums[w];
-        total += sums[w];
-    }
-    return before + x - v;
-}
-
-// One (row, key head) a cluster of n_cta CTAs, which share its pages' columns.
+// A query head's codes in shared memory: 16 bytes more than they need, so that two heads' pieces
+// lie in different banks.
 template <int DIM>
-__global__ void __launch_bounds__(kThreads) k_block_select(const __grid_constant__ SelectParams p, int n_cta)
+constexpr int kQueryBytes = 2 * DIM + 16;
+
+// 32 bytes (on a boundary of as many) at once: four lanes have a 128-byte line of a page.
+__device__ __forceinline__ void load32(const void *src, uint32_t x[8])
 {
-    constexpr int L = DIM / 16, PW = 32 / L;         // lanes of a page, pages a warp's load
-    constexpr int U = 4;
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+                 : "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster(uint32_t *local, int rank, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_cluster(smem_u32(local), uint32_t(rank))), "r"(v) : "memory");
+}
+
+// One (row, key head) a cluster of n_cta CTAs: they share the scoring of its pages, and the first
+// one, which gets all scores in its shared memory, chooses.
+//
+// Scores: the 2 * DIM bytes of a page's bounds (lo, then hi) are one row of the products' left side,
+// the codes of a query head (those below zero, then those above) one column of the right.  The
+// order of the 2 * DIM is free as long as both sides have the same, so a lane takes 32-byte pieces
+// of its two pages straight from memory.
+template <int DIM>
+__global__ void __launch_bounds__(kSelThreads, kSelCtas) k_block_select(const __grid_constant__ SelectParams p, int n_cta)
+{
+    constexpr int J = 2 * DIM / 128;                 // 128-byte lines of a page: a 32-byte piece for each of four lanes
     extern __shared__ __align__(16) uint8_t smem[];
-    uint32_t *qpos = reinterpret_cast<uint32_t *>(smem), *qneg = qpos + p.group * DIM / 4;   // codes above and below zero
-    float *q_unit = reinterpret_cast<float *>(qneg + p.group * DIM / 4);
-    int *hist = reinterpret_cast<int *>(q_unit + ((p.group + 3) & ~3));                       // one for each pass
-    uint32_t *keys = reinterpret_cast<uint32_t *>(hist + 3 * kBins);
-    __shared__ int sums[kWarps], counts[2], found[2];
+    const int heads8 = (p.group + 7) & ~7;
+    uint8_t *q_codes = smem;
+    float *q_unit = reinterpret_cast<float *>(smem + heads8 * kQueryBytes<DIM>);  // [heads8]
+    int *hist = reinterpret_cast<int *>(q_unit + heads8);                         // one for each of four passes
+    uint32_t *keys = reinterpret_cast<uint32_t *>(hist + 4 * kBins);
+    __shared__ int sums[2 * kSelWarps];
     const KvView &kv = p.kv;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = int(cluster_ctarank());
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = int(cluster_ctarank()), c = lane & 3, g = lane >> 2;
     const int64_t work = int64_t(blockIdx.x) / n_cta;
     const int row = int(work / kv.heads), head = int(work - int64_t(row) * kv.heads);
     grid_dep_wait();
     grid_dep_launch();
 
+    // the queries are on their way while the row's place is looked up, and so are the first pages
+    // of the sequence that a decode batch's row belongs to
+    constexpr int N = DIM / 32;
+    constexpr int kStep = kSelWarps * kTile;
+    const uint16_t *q = p.q + row * p.ldq + int64_t(head) * p.group * DIM + lane * N;
+    uint2 mine = make_uint2(0, 0);
+    auto query = [&](int h) {
+        return N == 4 ? *reinterpret_cast<const uint2 *>(q + h * DIM) : make_uint2(*reinterpret_cast<const uint32_t *>(q + h * DIM), 0u);
+    };
+    if (warp < p.group)
+        mine = query(warp);
+    int base = warp * kTile, page[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int col = p.first + base + 8 * r + g;
+        page[r] = row < p.b.n_seqs && col < p.n_cols ? p.b.pages[row * p.b.ld_pages + col] : -1;
+    }
+    for (int i = threadIdx.x; i < 4 * kBins; i += kSelThreads)
+        hist[i] = 0;
     const RowAt at = find_pos(p.b, row, head == 0 && rank == 0 ? p.status : nullptr);
     const int pos = at.live ? at.pos : -1;
     const int cols = pos >= 0 ? page_of(kv, pos) + 1 : 0;    // pages the row sees
@@ -287,183 +310,208 @@ __global__ void __launch_bounds__(kThreads) k_block_select(const __grid_constant
     if (cols <= p.blocks || choose == 0) {
         // all of them, or no choice: the first and the last
         if (rank == 0)
-            for (int i = threadIdx.x; i < p.blocks; i += kThreads)
+            for (int i = threadIdx.x; i < p.blocks; i += kSelThreads)
                 out[i] = i >= cols ? -1 : cols <= p.blocks || i < p.first ? table[i] : table[cols - p.blocks + i];
         return;
     }
-    // the columns to choose from, this CTA's share of them
-    const int n_cand = cols - p.first - p.last, share = (n_cand + n_cta - 1) / n_cta;
-    const int c_lo = p.first + min(n_cand, rank * share), n = min(n_cand, (rank + 1) * share) - min(n_cand, rank * share);
+    // the columns to choose from, [lo, hi) of them this CTA's
+    const int n = cols - p.first - p.last, share = (n + n_cta - 1) / n_cta;
+    const int lo = min(n, rank * share), hi = min(n, lo + share);
+    table += p.first;
 
-    for (int g = warp; g < p.group; g += kWarps) {
-        constexpr int N = DIM / 32;
-        const uint16_t *src = p.q + row * p.ldq + int64_t(head * p.group + g) * DIM + lane * N;
-        float f[N], top = 0.f, inverse;
+    // Two pages of a tile a lane: the first tile's bounds too are on their way while the queries become codes.
+    uint32_t a[2][J][8];
+    float unit[2];
+    auto load = [&]() {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            f[e] = __uint_as_float(uint32_t(src[e]) << 16);
-            top = max_nan(top, fabsf(f[e]));
+        for (int r = 0; r < 2; ++r) {
+            const bool there = page[r] >= 0 && page[r] < kv.n_pages;
+            const int64_t where = int64_t(there ? page[r] : 0) * kv.heads + head;
+            const int8_t *src = kv.bounds + where * 2 * DIM + c * 32;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                load32(src + 128 * j, a[r][j]);
+            unit[r] = there ? kv.unit[where] : -1.f;
         }
+    };
+    auto look_up = [&]() {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            page[r] = base + 8 * r + g < hi ? table[base + 8 * r + g] : 0;
+    };
+    base += lo;
+    if (base < hi) {
+        if (at.s != row || lo != 0)
+            look_up();
+        load();
+    }
+    for (int h = warp; h < heads8; h += kSelWarps) {
+        const bool on = h < p.group;
+        const uint2 x = !on ? make_uint2(0, 0) : h == warp ? mine : query(h);
+        const float f[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u)};
+        float top = 0.f, inverse;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            top = max_nan(top, fabsf(f[e]));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float unit = unit_for(top, inverse);
+        const float u = unit_for(top, inverse);
+        uint32_t above = 0, below = 0;               // the lane's N codes
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            const int c = unit == unit ? code_of(f[e], inverse) : 0;
-            reinterpret_cast<int8_t *>(qpos)[g * DIM + lane * N + e] = int8_t(max(c, 0));
-            reinterpret_cast<int8_t *>(qneg)[g * DIM + lane * N + e] = int8_t(min(c, 0));
+            const int code = u == u ? code_of(f[e], inverse) : 0;
+            above |= uint32_t(max(code, 0) & 0xff) << (8 * e);
+            below |= uint32_t(min(code, 0) & 0xff) << (8 * e);
+        }
+        uint8_t *dst = q_codes + h * kQueryBytes<DIM> + lane * N;
+        if (N == 4) {
+            *reinterpret_cast<uint32_t *>(dst) = below;
+            *reinterpret_cast<uint32_t *>(dst + DIM) = above;
+        } else {
+            *reinterpret_cast<uint16_t *>(dst) = uint16_t(below);
+            *reinterpret_cast<uint16_t *>(dst + DIM) = uint16_t(above);
         }
         if (lane == 0)
-            q_unit[g] = unit;
+            q_unit[h] = on ? u : __int_as_float(0x7fffffff);     // no head: no say
     }
-    for (int i = threadIdx.x; i < 3 * kBins; i += kThreads)
-        hist[i] = 0;
     __syncthreads();
 
-    // Scores: L lanes a page, 16 elements of both bounds each.
-    const int sub = lane % L, off = lane / L;
-    for (int base = warp * PW * U; base < n; base += kWarps * PW * U) {
-        uint4 lo[U], hi[U];
-        float unit[U], best[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = base + u * PW + off;
-            int page = i < n ? table[c_lo + i] : 0;
-            if (page < 0 || page >= kv.n_pages) {
-                raise_status(p.status, kDevBadPage);
-                page = -1;
-            }
-            const int64_t at = int64_t(max(page, 0)) * kv.heads + head;
-            const uint8_t *src = reinterpret_cast<const uint8_t *>(kv.bounds) + at * 2 * DIM + sub * 16;
-            lo[u] = *reinterpret_cast<const uint4 *>(src);
-            hi[u] = *reinterpret_cast<const uint4 *>(src + DIM);
-            unit[u] = kv.unit[at];
-            best[u] = -INFINITY;
-            if (page < 0)
-                unit[u] = -1.f;                      // chosen last
-        }
+    while (base < hi) {
+        float best[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
-        for (int g = 0; g < p.group; ++g) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(qpos + (g * DIM + sub * 16) / 4);
-            const uint4 b = *reinterpret_cast<const uint4 *>(qneg + (g * DIM + sub * 16) / 4);
-            const float ug = q_unit[g];
+        for (int h = 0; h < heads8; h += 8) {
+            const uint4 *b = reinterpret_cast<const uint4 *>(q_codes + (h + g) * kQueryBytes<DIM>) + 2 * c;
+            int s[2][4] = {};                        // two chains of products
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                int d = __dp4a(int(hi[u].x), int(a.x), __dp4a(int(lo[u].x), int(b.x), 0));
-                d = __dp4a(int(hi[u].y), int(a.y), __dp4a(int(lo[u].y), int(b.y), d));
-                d = __dp4a(int(hi[u].z), int(a.z), __dp4a(int(lo[u].z), int(b.z), d));
-                d = __dp4a(int(hi[u].w), int(a.w), __dp4a(int(lo[u].w), int(b.w), d));
+            for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int o = 1; o < L; o <<= 1)
-                    d += __shfl_xor_sync(0xffffffffu, d, o);
-                best[u] = fmaxf(best[u], float(d) * unit[u] * ug);       // a query that is not finite has no say
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = base + u * PW + off;
-            if (sub == 0 && i < n)
-                // a page that is not finite is looked at: its keys reach the result as they would
-                keys[i] = unit[u] < 0.f ? 0u : unit[u] != unit[u] ? key_of(INFINITY) : key_of(best[u]);
-        }
-    }
-
-    // The choose-th largest key over the cluster, digit by digit.
-    uint32_t prefix = 0;
-    int want = choose, shift = 32;
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        int *h = hist + pass * kBins;
-        const int bits = pass < 2 ? 11 : 10;
-        const uint32_t above = pass == 0 ? 0u : ~0u << shift;
-        shift -= bits;
-        __syncthreads();
-        for (int i = threadIdx.x; i < n; i += kThreads)
-            if ((keys[i] & above) == prefix)
-                atomicAdd(&h[keys[i] >> shift & ((1u << bits) - 1)], 1);
-        if (n_cta > 1) {
-            __syncwarp();
-            cluster_sync();
-        } else
-            __syncthreads();
-        // thread t has bins of falling keys: eight (four) from the top down
-        constexpr int B = kBins / kThreads;
-        const int per = (1 << bits) / kThreads, top_bin = (1 << bits) - 1 - int(threadIdx.x) * per;
-        int bin[B], mine = 0;
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-            bin[b] = 0;
-            if (b < per) {
-                if (n_cta > 1)
-                    for (int c = 0; c < n_cta; ++c)
-                        bin[b] += ld_cluster(h + top_bin - b, c);
-                else
-                    bin[b] = h[top_bin - b];
-            }
-            mine += bin[b];
-        }
-        int total;
-        int before = block_prefix(mine, sums, total);
-        if (before < want && before + mine >= want) {
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                if (before < want && before + bin[b] >= want) {
-                    found[0] = top_bin - b;
-                    found[1] = want - before;
+                for (int e = 0; e < 2; ++e) {
+                    const uint4 y = b[8 * j + e];
+                    const uint32_t *x0 = a[0][j] + 4 * e, *x1 = a[1][j] + 4 * e;
+                    mma_s8(s[0], x0[0], x1[0], x0[1], x1[1], y.x, y.y);
+                    mma_s8(s[1], x0[2], x1[2], x0[3], x1[3], y.z, y.w);
                 }
-                before += bin[b];
+            // pages g and g + 8, heads 2c and 2c + 1; a query that is not finite has no say
+            const float2 u = *reinterpret_cast<const float2 *>(q_unit + h + 2 * c);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                best[r] = fmaxf(best[r], fmaxf(float(s[0][2 * r] + s[1][2 * r]) * unit[r] * u.x, float(s[0][2 * r + 1] + s[1][2 * r + 1]) * unit[r] * u.y));
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+            best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+            const int i = base + 8 * r + g;
+            if (c == 0 && i < hi) {
+                // a page that is not there comes last; one that is not finite is looked at: its keys
+                // reach the result as they would
+                if (unit[r] < 0.f)
+                    raise_status(p.status, kDevBadPage);
+                keys[i] = unit[r] < 0.f ? 0u : unit[r] != unit[r] ? key_of(INFINITY) : key_of(best[r]);
             }
         }
-        __syncthreads();
-        prefix |= uint32_t(found[0]) << shift;
-        want = found[1];                             // of the keys equal so far
-    }
-    // prefix is the key itself: all above it, and the first `want` equal ones by column
-
-    int gt = 0, eq = 0;                              // ahead of this CTA's columns
-    if (n_cta > 1) {
-        int a = 0, b = 0;
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            a += keys[i] > prefix;
-            b += keys[i] == prefix;
+        base += kStep;
+        if (base < hi) {
+            look_up();
+            load();
         }
-        int t;
-        block_prefix(a, sums, t);
-        if (threadIdx.x == 0)
-            counts[0] = t;
-        block_prefix(b, sums, t);
-        if (threadIdx.x == 0)
-            counts[1] = t;
+    }
+    __syncthreads();
+    if (n_cta > 1) {
+        if (rank != 0)
+            for (int i = lo + int(threadIdx.x); i < hi; i += kSelThreads)
+                st_cluster(keys + i, 0, keys[i]);
         __syncwarp();
         cluster_sync();
-        for (int c = 0; c < rank; ++c) {
-            gt += ld_cluster(&counts[0], c);
-            eq += ld_cluster(&counts[1], c);
+        if (rank != 0)
+            return;
+    }
+
+    // The choose-th largest key, eight bits at a time.  Every warp looks through the counts itself:
+    // one barrier a pass.
+    uint32_t prefix = 0;
+    int want = choose;
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+        int *h = hist + pass * kBins;
+        const int shift = 24 - 8 * pass;
+        const uint32_t above = pass == 0 ? 0u : ~0u << (shift + 8);
+        for (int i0 = warp * 32; i0 < n; i0 += kSelThreads) {
+            const uint32_t key = i0 + lane < n ? keys[i0 + lane] : 0u;
+            const bool in = i0 + lane < n && (key & above) == prefix;
+            const int digit = in ? int(key >> shift & (kBins - 1)) : -1;
+            // most keys have the same first digit: one addition for each digit of a warp
+            const unsigned same = pass == 0 ? __match_any_sync(0xffffffffu, digit) : 1u << lane;
+            if (in && __ffs(same) - 1 == lane)
+                atomicAdd(&h[digit], __popc(same));
+        }
+        __syncthreads();
+        // lane l has eight bins, from 255 - 8 l down
+        const int low = kBins - 8 - 8 * lane;
+        const int4 x = *reinterpret_cast<const int4 *>(h + low), y = *reinterpret_cast<const int4 *>(h + low + 4);
+        const int bin[8] = {y.w, y.z, y.y, y.x, x.w, x.z, x.y, x.x};
+        int all = 0;
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+            all += bin[b];
+        int upto = all;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d)
+                upto += y;
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, upto >= want)) - 1;
+        int rest = want - (upto - all), digit = 0, count = 0;
+        bool done = false;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+            if (!done) {
+                digit = low + 7 - b;
+                count = bin[b];
+                done = rest <= bin[b];
+                rest -= done ? 0 : bin[b];
+            }
+        }
+        prefix |= uint32_t(__shfl_sync(0xffffffffu, digit, src)) << shift;
+        want = __shfl_sync(0xffffffffu, rest, src);  // of the keys equal so far
+        if (want == __shfl_sync(0xffffffffu, count, src) && prefix) {
+            prefix -= 1;                             // all of them: no need to tell them apart
+            want = 0;
+            break;
         }
     }
-    for (int base = 0; base < n; base += kThreads) {
-        const int i = base + int(threadIdx.x);
-        const uint32_t key = i < n ? keys[i] : 0u;
-        const bool more = i < n && key > prefix, same = i < n && key == prefix;
-        int total;
-        const int before = block_prefix(int(more) | int(same) << 16, sums, total);
-        const int g = gt + (before & 0xffff), e = eq + (before >> 16);
+
+    // All keys above prefix, and the first `want` of those equal to it, in the order of their
+    // columns: a warp has a run of them.
+    const int run = (n + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32, i1 = min(n, (warp + 1) * run);
+    int gt = 0, eq = 0;
+    for (int i0 = warp * run; i0 < i1; i0 += 32) {
+        const uint32_t key = i0 + lane < i1 ? keys[i0 + lane] : 0u;
+        gt += __popc(__ballot_sync(0xffffffffu, i0 + lane < i1 && key > prefix));
+        eq += __popc(__ballot_sync(0xffffffffu, i0 + lane < i1 && key == prefix));
+    }
+    if (lane == 0)
+        sums[warp] = gt, sums[kSelWarps + warp] = eq;
+    __syncthreads();
+    gt = __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0);
+    eq = __reduce_add_sync(0xffffffffu, lane < warp ? sums[kSelWarps + lane] : 0);
+    const unsigned below = (1u << lane) - 1;
+    for (int i0 = warp * run; i0 < i1; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t key = i < i1 ? keys[i] : 0u;
+        const bool more = i < i1 && key > prefix, same = i < i1 && key == prefix;
+        const unsigned mg = __ballot_sync(0xffffffffu, more), me = __ballot_sync(0xffffffffu, same);
+        const int ahead = gt + __popc(mg & below), e = eq + __popc(me & below);
         if (more || (same && e < want))
-            out[p.first + g + min(e, want)] = table[c_lo + i];
-        gt += total & 0xffff;
-        eq += total >> 16;
+            out[p.first + ahead + min(e, want)] = table[i];
+        gt += __popc(mg);
+        eq += __popc(me);
     }
-    if (rank == 0)
-        for (int i = threadIdx.x; i < p.first; i += kThreads)
-            out[i] = table[i];
-    if (rank == n_cta - 1)
-        for (int i = threadIdx.x; i < p.last; i += kThreads)
-            out[p.blocks - p.last + i] = table[cols - p.last + i];
-    if (n_cta > 1) {
-        __syncwarp();
-        cluster_sync();                              // others may still read this CTA's counts
-    }
+    // the first ones, and the last ones behind the n to choose from
+    for (int i = threadIdx.x; i < p.first + p.last; i += kSelThreads)
+        out[i < p.first ? i : i + choose] = table[i < p.first ? i - p.first : i - p.first + n];
 }
 
 template <int DIM>
@@ -473,14 +521,15 @@ cudaError_t launch(const SelectParams &p, int sms, cudaStream_t stream)
     const cudaError_t e = allow_shared(once, k_block_select<DIM>, 226 * 1024);
     if (e != cudaSuccess)
         return e;
-    // Few rows over many pages are cut over more SMs, not below 256 pages a CTA.
+    // A CTA scores 128 pages in about 2 us: more are shared, as far as the GPU has room for the
+    // CTAs at once.
     const int64_t units = int64_t(p.b.n_rows) * p.kv.heads;
     int c = 1;
-    while (c < kMaxCluster && ((p.n_cols + c - 1) / c > kMaxShare || (units * c < 2 * sms && p.n_cols / c > 256)))
+    while (c < kMaxCluster && units * c * 2 <= kSelCtas * sms && p.n_cols / c > 256)
         c *= 2;
-    const size_t codes = size_t(p.group) * DIM * 2 + size_t((p.group + 3) & ~3) * 4;
-    return start(k_block_select<DIM>, dim3(unsigned(units * c)), kThreads,
-                 codes + (3 * kBins + size_t((p.n_cols + c - 1) / c)) * 4, c, stream, p, c);
+    const size_t heads8 = size_t((p.group + 7) & ~7);
+    return start(k_block_select<DIM>, dim3(unsigned(units * c)), kSelThreads,
+                 heads8 * (kQueryBytes<DIM> + 4) + (4 * kBins + size_t(p.n_cols)) * 4, c, stream, p, c);
 }
 
 }  // namespace

@@ -157,12 +157,12 @@ struct BoundsParams {
 };
 cudaError_t launch_kv_bounds(const BoundsParams &p, cudaStream_t stream);
 
-constexpr int kMaxSelectCols = 1 << 18;
+constexpr int kMaxSelectCols = 44 << 10;
 constexpr int kMaxSelectGroup = 128;
 struct SelectParams {
     KvView kv;
     BatchView b;
-    int n_cols;
+    int n_cols;               // of the page table
     const uint16_t *q;
     int64_t ldq;
     int group, blocks, first, last;
@@ -176,12 +176,27 @@ struct SeqInfo {
     int start, n_new, len;
 };
 
-// Sequence s of the batch; one whose rows or length are out of range counts as having
-// no rows and raises the status.
-__device__ __forceinline__ SeqInfo seq_info(const BatchView &b, int s, unsigned *status)
+// A sequence with rows [start, end) and length len; one whose rows or length are out of range
+// counts as having no rows and raises the status.
+__device__ __forceinline__ SeqInfo checked_seq(const BatchView &b, int start, int end, int len, unsigned *status)
 {
     SeqInfo q;
+    q.start = start;
+    q.len = len;
+    q.n_new = end - start;
+    if (q.start < 0 || end < q.start || end > b.n_rows || q.n_new > b.max_new || q.len < 0 ||
+        q.len > b.capacity) {
+        raise_status(status, kDevBadBatch);
+        q.start = q.n_new = q.len = 0;
+    }
+    return q;
+}
+
+// Sequence s of the batch.
+__device__ __forceinline__ SeqInfo seq_info(const BatchView &b, int s, unsigned *status)
+{
     if (!b.starts) {
+        SeqInfo q;
         q.start = s;
         q.len = b.lens[s];
         q.n_new = q.len >= 0;
@@ -192,16 +207,7 @@ __device__ __forceinline__ SeqInfo seq_info(const BatchView &b, int s, unsigned 
         }
         return q;
     }
-    q.start = b.starts[s];
-    const int end = b.starts[s + 1];
-    q.len = b.lens[s];
-    q.n_new = end - q.start;
-    if (q.start < 0 || end < q.start || end > b.n_rows || q.n_new > b.max_new || q.len < 0 ||
-        q.len > b.capacity) {
-        raise_status(status, kDevBadBatch);
-        q.start = q.n_new = q.len = 0;
-    }
-    return q;
+    return checked_seq(b, b.starts[s], b.starts[s + 1], b.lens[s], status);
 }
 
 __device__ __forceinline__ int page_of(const KvView &kv, int pos)

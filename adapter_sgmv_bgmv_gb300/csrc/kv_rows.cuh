@@ -18,11 +18,14 @@ struct RowAt {
 __device__ __forceinline__ RowAt find_pos(const BatchView &b, int row, unsigned *status)
 {
     const int lane = threadIdx.x & 31;
-    // A decode batch has one row per sequence: row r is sequence r.  Otherwise a
-    // 32-way search for the last sequence that starts at or before the row.
-    int s = row;
-    bool hit = s < b.n_seqs && b.starts[s] == row && b.starts[s + 1] == row + 1;
-    if (!hit) {
+    // A decode batch has one row per sequence: row r is sequence r (its length is on its way with
+    // its rows).  Otherwise a 32-way search for the last sequence that starts at or before the row.
+    const bool may = row < b.n_seqs;
+    const int start = may ? b.starts[row] : -1, end = may ? b.starts[row + 1] : -1, len = may ? b.lens[row] : 0;
+    RowAt r{false, row, -1, {}};
+    if (start == row && end == row + 1) {
+        r.q = checked_seq(b, start, end, len, status);
+    } else {
         int lo = 0, n = b.n_seqs;                    // starts[lo] <= row, answer in [lo, lo + n)
         while (n > 1) {
             const int step = (n + 31) / 32;
@@ -33,9 +36,9 @@ __device__ __forceinline__ RowAt find_pos(const BatchView &b, int row, unsigned 
             n = min(step, n - last * step);
             lo += last * step;
         }
-        s = lo;
+        r.s = lo;
+        r.q = seq_info(b, lo, status);
     }
-    RowAt r{false, s, -1, seq_info(b, s, status)};
     if (row < r.q.start || row >= r.q.start + r.q.n_new)
         return r;
     r.live = true;

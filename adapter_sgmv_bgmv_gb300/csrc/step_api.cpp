@@ -262,7 +262,7 @@ int lora_kv_copy(lora_ctx *ctx, const lora_kv *const *kvs, int n_kv, const int32
 
 int lora_kv_attach_bounds(lora_kv *kv, void *codes, float *unit)
 {
-    if (!kv || !codes != !unit || (codes && (!aligned(codes, 16) || !aligned(unit, 4))))
+    if (!kv || !codes != !unit || (codes && (!aligned(codes, 32) || !aligned(unit, 4))))
         return LORA_E_INVAL;
     kv->view.bounds = static_cast<int8_t *>(codes);
     kv->view.unit = unit;

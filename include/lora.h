@@ -621,7 +621,7 @@ int lora_kv_copy(lora_ctx *ctx, const lora_kv *const *kvs, int n_kv, const int32
  * prompt is sooner served whole by lora_attention.
  *
  * Bounds are caller-owned device memory attached to a cache: codes int8 [n_pages][n_heads][2]
- * [head_dim] on a 16-byte boundary and unit fp32 [n_pages][n_heads].  lo and hi are the smallest and
+ * [head_dim] on a 32-byte boundary and unit fp32 [n_pages][n_heads].  lo and hi are the smallest and
  * the largest value of each element among a page's keys (as fp32, scale * code in 8-bit caches);
  * unit = 2^(e - 6) with 2^e <= max(|lo|, |hi|) < 2^(e + 1), e >= -100; codes are lo / unit and
  * hi / unit to the nearest, ties to even, within +-127.  A page with a key that is not finite gets
@@ -651,7 +651,7 @@ typedef struct {
  * with c, unit_g of query head g taken like the bounds' codes, in integers and fp32 products
  * with powers of two: the choice is the same in any order of summation.  A page whose unit is NaN
  * comes first, one the cache does not have last (and LORA_E_PAGE); a query head with an infinity or a NaN
- * has no say.  LORA_E_CAPACITY: more than 2^18 columns, 128 query heads a key head, or
+ * has no say.  LORA_E_CAPACITY: more than 45,056 columns, 128 query heads a key head, or
  * blocks * page_size above 2^30. */
 int lora_block_select(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch, int64_t n,
                       const void *q, int64_t ldq, int n_heads, int first, int last,

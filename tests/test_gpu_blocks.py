@@ -95,7 +95,7 @@ def test_random_steps(ctx, seed):
     st.close()
 
 
-@pytest.mark.parametrize("n_cols,page,heads,kv_heads", [(2000, 1, 4, 1), (9000, 1, 1, 1), (40000, 1, 2, 2), (1500, 16, 28, 4)])
+@pytest.mark.parametrize("n_cols,page,heads,kv_heads", [(2000, 1, 4, 1), (9000, 1, 1, 1), (45056, 1, 2, 2), (1500, 16, 28, 4)])
 def test_long_lists(ctx, n_cols, page, heads, kv_heads):
     """One (row, head) over a cluster of CTAs."""
     c = Case(n_cols, [2], [n_cols * page - page // 2], heads, kv_heads, 64, page)

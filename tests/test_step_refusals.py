@@ -178,7 +178,7 @@ def test_bounds_and_choice(ctx, kv):
         return L._L.lora_block_select(ctx.handle, kv, batch, 3, A, ldq, heads, first, last, s, None)
     assert L._L.lora_kv_bounds(ctx.handle, kv, b, 3, None) == INVAL and choose() == INVAL        # none attached
     assert L._L.lora_kv_attach_bounds(kv, 1 << 22, None) == INVAL and L._L.lora_kv_attach_bounds(kv, None, 1 << 22) == INVAL
-    assert L._L.lora_kv_attach_bounds(kv, (1 << 22) + 8, 1 << 22) == INVAL and L._L.lora_kv_attach_bounds(kv, 1 << 22, 2) == INVAL
+    assert L._L.lora_kv_attach_bounds(kv, (1 << 22) + 16, 1 << 22) == INVAL and L._L.lora_kv_attach_bounds(kv, 1 << 22, 2) == INVAL
     assert L._L.lora_kv_attach_bounds(None, 1 << 22, 1 << 22) == INVAL
     assert L._L.lora_kv_attach_bounds(kv, 1 << 22, 1 << 23) == 0
     assert L._L.lora_kv_bounds(ctx.handle, kv, b, 3, None) == UNSUPPORTED
@@ -187,7 +187,7 @@ def test_bounds_and_choice(ctx, kv):
     assert choose(first=-1) == INVAL and choose(last=0) == INVAL and choose(first=4, last=3) == INVAL and choose(first=6) == INVAL
     assert choose(first=5) == UNSUPPORTED and choose(first=3, last=3) == UNSUPPORTED
     assert choose(first=(1 << 31) - 1, last=(1 << 31) - 1) == INVAL
-    assert choose(batch=ctypes.byref(batch(n_cols=(1 << 18) + 1, ld_pages=1 << 19))) == CAPACITY
+    assert choose(batch=ctypes.byref(batch(n_cols=45057, ld_pages=1 << 19))) == CAPACITY
     assert choose(heads=4 * 129, ldq=4 * 129 * 128) == CAPACITY
     assert L._L.lora_kv_attach_bounds(kv, None, None) == 0
     assert choose() == INVAL
