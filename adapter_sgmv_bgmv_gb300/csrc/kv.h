@@ -106,6 +106,8 @@ struct AttnParams {
 };
 cudaError_t launch_attn_rows(const AttnParams &p, int sms, cudaStream_t stream);
 cudaError_t launch_attn_tc(const AttnParams &p, int sms, cudaStream_t stream);
+// Rows over page lists of their own (no `starts`).
+cudaError_t launch_attn_blocks(const AttnParams &p, int sms, cudaStream_t stream);
 
 // Norm and rotation of heads (rope.cu), of a row's q_heads queries and k_heads keys; with
 // `kv.k`, keys and values go to their cells instead of k_out.

@@ -126,8 +126,7 @@ int take_selection(const lora_ctx *ctx, const lora_kv *kv, const lora_block_sel 
     if (!ctx || !kv || kv->ctx != ctx || !sel || n < 0 || sel->n_rows < n || sel->blocks < 1 || n_heads < 1 ||
         n_heads % kv->view.heads || (n > 0 && (!aligned(sel->lens, 4) || !aligned(sel->pages, 4))))
         return LORA_E_INVAL;
-    if (int64_t(sel->blocks) * kv->view.page_size > kMaxPosition || n * kv->view.heads >= (int64_t(1) << 28) ||
-        n * n_heads >= (int64_t(1) << 31))
+    if (int64_t(sel->blocks) * kv->view.page_size > kMaxPosition || n * n_heads >= (int64_t(1) << 28))
         return LORA_E_CAPACITY;
     return LORA_OK;
 }
@@ -349,11 +348,8 @@ int lora_block_attention(lora_ctx *ctx, const lora_kv *kv, const lora_block_sel 
     p.heads = n_heads;
     p.group = n_heads / p.kv.heads;
     p.scale = scale;
-    p.min_rows = 1;
-    p.max_rows = int64_t(1) << 40;
-    p.part = kv->few;
     p.status = ctx_status(ctx);
-    return done(ctx, stream, launch_attn_rows(p, ctx_sms(ctx), stream), 64);
+    return done(ctx, stream, launch_attn_blocks(p, ctx_sms(ctx), stream), 64);
 }
 
 }  // extern "C"
