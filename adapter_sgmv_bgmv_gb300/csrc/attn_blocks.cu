@@ -35,10 +35,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxCluster = 8;
-constexpr int kCtas8 = 2;
-template <int FMT>
-constexpr int kSub = FMT == kKvBf16 ? 1 : 2;
+constexpr int kMaxCluster = 8;               // with a lane for each warp's part
+static_assert(kMaxCluster * kWarps <= 32);
 
 __device__ __forceinline__ void mma(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
@@ -99,13 +97,13 @@ __device__ __forceinline__ void widen(uint32_t r, uint32_t &even, uint32_t &odd)
 template <int DIM, int FMT, int NR>
 struct Shape {
     static constexpr int ES = FMT == kKvBf16 ? 2 : 1;
-    static constexpr int SUB = kSub<FMT>;                  // tiles of 16 keys at once
+    static constexpr int SUB = FMT == kKvBf16 ? 1 : 2;     // tiles of 16 keys at once
     static constexpr int KEYS = 16 * SUB;
     static constexpr int J = DIM * ES / 64;                // 16-byte pieces of a key a lane
     static constexpr int MT = DIM / 16;                    // 16-element tiles of values
     static constexpr int ROWS = 8 * NR;
     static constexpr int LD = DIM + 4;                     // floats of a part's row
-    static constexpr int CTAS = NR == 1 ? (FMT == kKvBf16 ? 3 : kCtas8) : 2;
+    static constexpr int CTAS = NR == 1 && FMT == kKvBf16 ? 3 : 2;       // a SM
 };
 
 template <int DIM, int FMT, int NR, bool EVEN>
@@ -455,27 +453,61 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_bl
 #pragma unroll 1
     for (int row = w; row < n_rows; row += workers) {
         // lane i has the i-th part's maximum and sum
-        const bool on = lane < workers;
-        const float4 ml = on ? ld_cluster(reinterpret_cast<const float *>(&part_ml[lane % kWarps][row]), lane / kWarps) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        if (lane < workers)
+            ml = n_cta > 1 ? ld_cluster(&part_ml[lane % kWarps][row].x, lane / kWarps) : part_ml[lane][row];
         float top = ml.x;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float a = exp2_fast(ml.x - (top == -INFINITY ? 0.f : top)), al = a * ml.y;
-        float sum = 0.f, acc[N] = {};
-#pragma unroll 4
-        for (int i = 0; i < workers; ++i) {
-            const float f = __shfl_sync(0xffffffffu, a, i);
-            sum += __shfl_sync(0xffffffffu, al, i);
-            const float4 v = ld_cluster(&part[i % kWarps][row * S::LD + (lane * N & ~3)], i / kWarps);
+        const float a = exp2_fast(ml.x - (top == -INFINITY ? 0.f : top));
+        const float sum = warp_sum(a * ml.y);
+        float f[N] = {};
+        auto add = [&](int i, float4 v) {
+            const float x = __shfl_sync(0xffffffffu, a, i);
             if (N == 4) {
-                acc[0] = fmaf(f, v.x, acc[0]), acc[1] = fmaf(f, v.y, acc[1]);
-                acc[N - 2] = fmaf(f, v.z, acc[N - 2]), acc[N - 1] = fmaf(f, v.w, acc[N - 1]);
+                f[0] = fmaf(x, v.x, f[0]), f[1] = fmaf(x, v.y, f[1]);
+                f[N - 2] = fmaf(x, v.z, f[N - 2]), f[N - 1] = fmaf(x, v.w, f[N - 1]);
             } else {
-                acc[0] = fmaf(f, lane & 1 ? v.z : v.x, acc[0]), acc[1] = fmaf(f, lane & 1 ? v.w : v.y, acc[1]);
+                f[0] = fmaf(x, lane & 1 ? v.z : v.x, f[0]), f[1] = fmaf(x, lane & 1 ? v.w : v.y, f[1]);
+            }
+        };
+        const int piece = row * S::LD + (lane * N & ~3);
+        if (n_cta == 1) {
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i)
+                add(i, *reinterpret_cast<const float4 *>(&part[i][piece]));
+        } else {
+            // eight parts' loads under way at once
+#pragma unroll 1
+            for (int i0 = 0; i0 < workers; i0 += 8) {
+                float4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int k = min(i0 + i, workers - 1);
+                    v[i] = ld_cluster(&part[k % kWarps][piece], k / kWarps);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i0 + i < workers)
+                        add(i0 + i, v[i]);
             }
         }
-        finish_row<S::ROWS, DIM, FMT>(p, u, row, acc, sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;    // no key: zeros
+        bool ok = true;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            f[e] *= inv;
+            ok = ok && fabsf(f[e]) < INFINITY;
+        }
+        const int64_t col = int64_t(u.h * p.group + u.r * S::ROWS + row) * DIM;
+        if (!__all_sync(0xffffffffu, ok))
+            careful_row<DIM, FMT>(p, u.q, u.s, u.h, n - 1, p.q + u.s * p.ldq + col, f);
+        uint16_t *dst = p.out + u.s * p.ldo + col + lane * N;
+        if (N == 4)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(bf2(f[0], f[1]), bf2(f[N - 2], f[N - 1]));
+        else
+            *reinterpret_cast<uint32_t *>(dst) = bf2(f[0], f[1]);
     }
     if (n_cta > 1) {
         __syncwarp();
