@@ -102,10 +102,10 @@ class Context:
     def __init__(self, device: int = 0, max_rows: int = 1 << 16, max_rank: int = 64):
         """device = -1: host-only context (plans and tile tables, no launches)."""
         if isinstance(device, int) and device < 0:
-            self.device, idx = None, -1
+            self.device, idx, self.device_index = None, -1, None
         else:
             self.device = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
-            idx = self.device.index or 0
+            self.device_index = idx = self.device.index or 0
         h = ctypes.c_void_p()
         self.handle = None
         self._tables = weakref.WeakSet()
@@ -603,7 +603,7 @@ def _raw_stream(stream, ctx: Context):
     """_stream for the calls of a decode loop: the current stream's handle without a
     Stream object around it."""
     if stream is None and _current_raw_stream is not None and ctx.device is not None:
-        return _current_raw_stream(ctx.device.index or 0)
+        return _current_raw_stream(ctx.device_index)
     return _stream(stream, ctx.device)
 
 
@@ -708,14 +708,17 @@ def _rope_side(x, out, what, where):
 
 
 def _rope_on(ctx, rope, batch, head_dim):
-    where = _HeadsOn(head_dim, batch.device_index)
-    if ctx.device is None or where.device_index != (ctx.device.index or 0):
+    """What the rows have to be like: head_dim elements a head, on the context's device."""
+    dev = batch.device_index
+    if dev != ctx.device_index:
         raise ValueError("the batch must be on the context's device")
-    if rope.device_index is not None and rope.device_index != where.device_index:
-        raise ValueError("the rotation's tensors must be on the context's device")
     if rope.head_dim != head_dim:
         raise ValueError("the rotation is of another head_dim than the cache")
-    return where
+    if rope.device_index == dev:
+        return rope
+    if rope.device_index is not None:
+        raise ValueError("the rotation's tensors must be on the context's device")
+    return _HeadsOn(head_dim, dev)
 
 
 def lora_head_rope(ctx: Context, rope: HeadRope, batch: KvBatch, q: torch.Tensor | None, k: torch.Tensor | None,
@@ -755,13 +758,18 @@ def lora_kv_write_rope(ctx: Context, cache: KvCache, rope: HeadRope, batch: KvBa
 
 def _ints(t: torch.Tensor, what: str, device: int, n: int | None = None) -> int:
     """Pointer of a contiguous 1-D int32 tensor (of n elements) on a device."""
+    try:
+        sh = t.shape
+        if t.dtype is torch.int32 and t.get_device() == device and len(sh) == 1 and (n is None or sh[0] == n) and \
+                (sh[0] <= 1 or t.stride()[0] == 1):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{what} must be a CUDA tensor")
-    if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{what} must be a contiguous int32 tensor [{'n' if n is None else n}]")
     if t.get_device() != device:
         raise ValueError(f"{what} must be on the context's device")
-    return t.data_ptr()
+    raise ValueError(f"{what} must be a contiguous int32 tensor [{'n' if n is None else n}]")
 
 
 class PageTable:
@@ -792,7 +800,7 @@ class PageTable:
 
 
 def _table_on(ctx: Context, table: PageTable) -> int:
-    if ctx.device is None or table.device_index != (ctx.device.index or 0):
+    if table.device_index != ctx.device_index:
         raise ValueError("the page table must be on the context's device")
     return table.device_index
 
@@ -803,8 +811,9 @@ def lora_pages_extend(ctx: Context, table: PageTable, grow: torch.Tensor, got: t
     src, dst and cells are the pages to copy (lora_kv_copy) before the new tokens are written.
     All int32 [n_seqs]."""
     dev, n = _table_on(ctx, table), table.lens.shape[0]
-    rc = _L.lora_pages_extend(ctx.handle, table._ref, *(_ints(t, nm, dev, n) for t, nm in (
-        (grow, "grow"), (got, "got"), (src, "src"), (dst, "dst"), (cells, "cells"))), _raw_stream(stream, ctx))
+    rc = _L.lora_pages_extend(ctx.handle, table._ref, _ints(grow, "grow", dev, n), _ints(got, "got", dev, n),
+                              _ints(src, "src", dev, n), _ints(dst, "dst", dev, n), _ints(cells, "cells", dev, n),
+                              _raw_stream(stream, ctx))
     if rc:
         _check(rc, ctx)
 
@@ -850,7 +859,7 @@ def lora_kv_copy(ctx: Context, caches, src: torch.Tensor, dst: torch.Tensor, cel
         caches = (caches,)
     if not caches or ctx.device is None:
         raise ValueError("no caches, or a context without a device")
-    dev, n = ctx.device.index or 0, src.shape[0]
+    dev, n = ctx.device_index, src.shape[0]
     handles = (ctypes.c_void_p * len(caches))(*[c.handle for c in caches])
     rc = _L.lora_kv_copy(ctx.handle, handles, len(caches), _ints(src, "src", dev), _ints(dst, "dst", dev, n),
                          None if cells is None else _ints(cells, "cells", dev, n), n, _raw_stream(stream, ctx))

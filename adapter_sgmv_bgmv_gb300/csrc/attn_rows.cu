@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_ro
         const int n_rows = min(kRows, u.q.n_new * p.group - u.r * kRows);
         const int base = u.q.len - u.q.n_new;
         const uint8_t *kp = kv.k + u.h * kv.head_stride, *vp = kv.v + u.h * kv.head_stride;
-        const int32_t *pages = b.pages + int64_t(u.s) * b.ld_pages + u.h * b.head_pages;
+        const int32_t *pages = b.pages + int64_t(u.s) * b.ld_pages;
 
         // first position of tile t's keys, and the end of the keys to read
         auto keys = [&](int t, int &j0, int &j1) {

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_bounds(const __grid_constant__ 
 {
     constexpr int E = FMT == kKvBf16 ? 8 : 16;       // elements of a lane's 16 bytes
     constexpr int L = DIM / E, CW = 32 / L;          // lanes of a cell, cells a warp's load
-    constexpr int U = 8;
+    constexpr int U = FMT == kKvBf16 ? 4 : 8;
     __shared__ int pages[kThreads], filled[kThreads], n_pages;
     const KvView &kv = p.kv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -209,7 +209,10 @@ cudaError_t launch(const BoundsParams &p, cudaStream_t stream)
     // A CTA has about one page: its rows of a prompt, one row where sequences have few each.
     const int64_t n = p.b.n_rows, touched = n / p.kv.page_size + p.b.n_seqs;
     const int rows = int(std::max<int64_t>(1, std::min<int64_t>(kThreads, n / std::max<int64_t>(1, touched))));
-    const dim3 grid(unsigned((n + rows - 1) / rows), unsigned(std::min((p.kv.heads + kWarps - 1) / kWarps, 64)));
+    // The heads too are dealt out to CTAs while these are fewer than twelve a SM (of 152).
+    const int64_t ctas = (n + rows - 1) / rows;
+    const int parts = int(std::max<int64_t>(1, std::min<int64_t>((p.kv.heads + kWarps - 1) / kWarps, 1824 / ctas)));
+    const dim3 grid{unsigned(ctas), unsigned(parts)};
     return start(k_kv_bounds<DIM, FMT>, grid, kThreads, 0, 0, stream, p, rows);
 }
 

@@ -98,6 +98,13 @@ __device__ __forceinline__ void rank_warps(int mine, int *counts, int n_cta, int
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = int(cluster_ctarank());
     if (lane == 0)
         counts[warp] = mine;
+    if (n_cta == 1) {
+        __syncthreads();
+        const int v = counts[lane];
+        total = __reduce_add_sync(0xffffffffu, v);
+        before = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
+        return;
+    }
     cluster_barrier();
     before = total = 0;
     for (int c = 0; c < n_cta; ++c) {
@@ -134,6 +141,9 @@ __global__ void __launch_bounds__(kThreads) k_pages_extend(const __grid_constant
     unsigned *status = rank == 0 ? t.status : nullptr;
     grid_dep_wait();
     grid_dep_launch();
+
+    const Run run = my_run(t.n_pages, n_cta);
+    const int held = count_held(t.refs, run);
 
     // What each sequence wants: every CTA works it out for itself.
     int any = 0;
@@ -196,8 +206,6 @@ __global__ void __launch_bounds__(kThreads) k_pages_extend(const __grid_constant
         }
     }
 
-    const Run run = my_run(t.n_pages, n_cta);
-    const int held = count_held(t.refs, run);
     int held_before, held_all;
     rank_warps(held, counts, n_cta, held_before, held_all);      // behind it nobody reads lens or another's refs
     const int free_all = t.n_pages - held_all;
@@ -246,7 +254,8 @@ __global__ void __launch_bounds__(kThreads) k_pages_extend(const __grid_constant
             *at = id;
             t.refs[id] = 1;
         }
-    cluster_barrier();                                  // others may still read this CTA's counts
+    if (n_cta > 1)
+        cluster_barrier();                           // others may still read this CTA's counts
 }
 
 // ---------------------------------------------------------------- fork, free
