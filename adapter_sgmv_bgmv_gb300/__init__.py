@@ -658,7 +658,7 @@ class HeadRope:
     """What lora_head_rope does to each head (see include/lora.h): freqs, float32 [pairs] on the
     GPU, turns the first 2 * pairs elements (None: no rotation), as pairs (j, j + pairs) or, when
     interleaved, (2j, 2j + 1); q_weight and k_weight [head_dim], where given, are the weights of
-    the norms (kept as float32: another type is converted here, once)."""
+    the norms (kept as float32: another type is converted here, once, on the current stream)."""
 
     def __init__(self, freqs: torch.Tensor | None, head_dim: int, q_weight: torch.Tensor | None = None,
                  k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False):

@@ -23,6 +23,8 @@ __device__ __forceinline__ RowAt find_pos(const BatchView &b, int row, unsigned 
     const bool may = row < b.n_seqs;
     const int start = may ? b.starts[row] : -1, end = may ? b.starts[row + 1] : -1, len = may ? b.lens[row] : 0;
     RowAt r{false, row, -1, {}};
+    if (b.n_seqs == 0)
+        return r;
     if (start == row && end == row + 1) {
         r.q = checked_seq(b, start, end, len, status);
     } else {

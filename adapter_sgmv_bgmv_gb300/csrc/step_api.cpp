@@ -303,8 +303,8 @@ int lora_block_select(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *b, 
     if (b->n_cols > kMaxSelectCols || n_heads / p.kv.heads > kMaxSelectGroup)
         return LORA_E_CAPACITY;
     rc = ctx_begin(ctx, stream);
-    if (rc != LORA_OK || n == 0 || b->n_seqs == 0)
-        return rc;
+    if (rc != LORA_OK || n == 0)
+        return rc;                             // without sequences too every row gets its length of -1
     p.n_cols = int(b->n_cols);
     p.q = static_cast<const uint16_t *>(q);
     p.ldq = ldq;

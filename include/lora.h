@@ -659,7 +659,7 @@ int lora_block_select(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *bat
 
 /* lora_attention of n rows over the pages chosen for them (the fp32 and two-term weights of its
  * few-rows form): row i sees the first lens[i] tokens of its lists.  Rows with lens[i] < 0 are
- * left alone.  The selection may also be the caller's own. */
+ * left alone.  The selection may also be the caller's own.  out may not overlap q. */
 int lora_block_attention(lora_ctx *ctx, const lora_kv *kv, const lora_block_sel *sel, int64_t n,
                          const void *q, int64_t ldq, int n_heads, float scale, void *out,
                          int64_t ldo, void *stream);

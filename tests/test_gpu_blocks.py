@@ -298,3 +298,54 @@ def test_results_repeat_and_replay(ctx):
         for i in range(2):
             assert torch.equal(outs[i], want[i][0]) and torch.equal(sels[i].pages, want[i][1]) and torch.equal(sels[i].lens, want[i][2])
     st.close()
+
+
+def test_batches_without_rows_or_sequences(ctx):
+    """Every row of a call without sequences belongs to none: its length is -1, and attention leaves it alone."""
+    import adapter_sgmv_bgmv_gb300 as L
+    c = Case(11, [1], [40], 4, 2, 64, 16)
+    st = Step(ctx, c)
+    none = torch.zeros(1, dtype=torch.int32, device="cuda")
+    empty = L.KvBatch(none, none[:0], torch.zeros((0, 3), dtype=torch.int32, device="cuda"))
+    q = c.rand(3, 4, 64)
+    out = torch.full_like(q, 7)
+    sel = L.BlockSelection.empty(3, st.cache, 2)
+    sel.lens.fill_(5)
+    L.lora_kv_bounds(ctx, st.cache, empty, 3)
+    L.lora_block_select(ctx, st.cache, empty, q, sel)
+    L.lora_block_attention(ctx, st.cache, sel, q, out)
+    ctx.sync_status()
+    assert sel.lens.tolist() == [-1] * 3 and bool((out == 7).all())
+    L.lora_kv_bounds(ctx, st.cache, st.batch, 0)
+    L.lora_block_select(ctx, st.cache, st.batch, q[:0], sel)
+    L.lora_block_attention(ctx, st.cache, sel, q[:0], out[:0])
+    ctx.sync_status()
+    assert ctx.last_path() == (0, 0)
+    st.close()
+
+
+def test_a_selection_of_ones_own(ctx):
+    """Any pages in any order, one of them twice, lengths that end inside a page; one too long is refused."""
+    import adapter_sgmv_bgmv_gb300 as L
+    from adapter_sgmv_bgmv_gb300 import LoraError
+    c = Case(12, [1, 1, 1], [200, 90, 40], 4, 2, 64, 16)
+    st = Step(ctx, c)
+    ids = [[[5, 0, 3], [0, 5, 5]], [[1, 2, 4], [2, 1, 0]], [[2, -1, -1], [0, -1, -1]]]
+    sel = L.BlockSelection(torch.tensor([37, 48, 1], dtype=torch.int32, device="cuda"), torch.tensor(ids, dtype=torch.int32, device="cuda"))
+    # pages of the table: those have been written
+    for s in range(3):
+        for h in range(2):
+            for i in range(3):
+                if ids[s][h][i] >= 0:
+                    sel.pages[s, h, i] = int(c.table[0, ids[s][h][i]])
+    L.lora_block_attention(ctx, st.cache, sel, c.q, c.out)
+    ctx.sync_status()
+    assert_attention(c.out, *chosen_attention(c, sel.lens.cpu(), sel.pages.cpu()))
+    before = c.out.clone()
+    sel.lens[1] = 49
+    L.lora_block_attention(ctx, st.cache, sel, c.q, c.out.fill_(3))
+    with pytest.raises(LoraError) as e:
+        ctx.sync_status()
+    assert e.value.name == "LORA_E_INVAL"
+    assert torch.equal(c.out[[0, 2]], before[[0, 2]]) and bool((c.out[1] == 3).all())
+    st.close()

@@ -249,3 +249,39 @@ def test_captured_and_on_a_stream(ctx):
         pos = c.lens_t.long() - 1
         check(c.out, c.q, w["q"], pos, f, 1e-6, False)
     cache.close()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_in_place_in_a_wider_buffer(ctx, interleaved):
+    """Queries and keys of one projection's rows, turned where they are: nothing else of the rows changes."""
+    import adapter_sgmv_bgmv_gb300 as L
+    c = Case(9, [700, 1, 33], [700, 50, 40], 5, 2, 128, 16, fill=False)
+    r, w, f = make(ctx, c, 64, "qk", interleaved)
+    rows = c.rand(c.n, 5 + 2 + 2, 128)
+    was = rows.clone()
+    L.lora_head_rope(ctx, r, L.KvBatch(c.starts, c.lens_t, c.pages), rows[:, :5], rows[:, 5:7])
+    ctx.sync_status()
+    check(rows[:, :5], was[:, :5], w["q"], positions(c), f, 1e-6, interleaved)
+    check(rows[:, 5:7], was[:, 5:7], w["k"], positions(c), f, 1e-6, interleaved)
+    assert torch.equal(rows[:, 7:], was[:, 7:])
+
+
+def test_calls_without_rows_or_heads(ctx):
+    import adapter_sgmv_bgmv_gb300 as L
+    c = Case(10, [2], [9], 2, 2, 64, 16, fill=False)
+    r, _, _ = make(ctx, c, 64)
+    batch = L.KvBatch(c.starts, c.lens_t, c.pages)
+    L.lora_head_rope(ctx, r, batch, c.q[:0], None)
+    assert ctx.last_path() == (0, 0)
+    none = torch.zeros(1, dtype=torch.int32, device="cuda")
+    was = c.q.clone()
+    L.lora_head_rope(ctx, r, L.KvBatch(none, none[:0], torch.zeros((0, 3), dtype=torch.int32, device="cuda")), c.q, None)
+    ctx.sync_status()
+    assert torch.equal(c.q, was)
+    for bad in (lambda: L.lora_head_rope(ctx, r, batch, None, None), lambda: L.lora_head_rope(ctx, r, batch, c.q, None, c.q[:1]),
+                lambda: L.lora_head_rope(ctx, r, batch, c.q[..., :32], None), lambda: L.lora_head_rope(ctx, r, batch, c.q.float(), None),
+                lambda: L.lora_kv_write_rope(ctx, L.KvCache(ctx, c.k_pool, c.v_pool), L.HeadRope(None, 128), batch, None, c.q, c.q)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        L.lora_head_rope(ctx, r, batch, c.q.cpu(), None)
