@@ -354,7 +354,8 @@ cudaError_t launch(RopeParams p, cudaStream_t stream)
     const int rows = int(std::max<int64_t>(1, n / kWave < 1 ? 1 : (n + kWave * waves - 1) / (kWave * waves)));
     const int nvec = p.q_heads + (FMT != kNone ? 2 : 1) * p.k_heads, row_items = (nvec + 32 / G - 1) / (32 / G);
     p.per_row = Divider(row_items);
-    const dim3 grid(unsigned((n + rows - 1) / rows), unsigned(rows == 1 ? (row_items + kWarps - 1) / kWarps : 1));
+    const int64_t parts = rows > 1 ? 1 : std::max<int64_t>(1, std::min<int64_t>((row_items + kWarps - 1) / kWarps, kWave / std::max<int64_t>(n, 1)));
+    const dim3 grid{unsigned((n + rows - 1) / rows), unsigned(parts)};
     return start(k_rope<G, FMT>, grid, kThreads, 0, 0, stream, p, rows);
 }
 
