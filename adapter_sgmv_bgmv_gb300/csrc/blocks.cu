@@ -528,7 +528,7 @@ cudaError_t launch(const SelectParams &p, int sms, cudaStream_t stream)
     // CTAs at once.
     const int64_t units = int64_t(p.b.n_rows) * p.kv.heads;
     int c = 1;
-    while (c < kMaxCluster && units * c * 2 <= kSelCtas * sms && p.n_cols / c > 256)
+    while (c < kMaxCluster && units * c * 2 <= kSelCtas * sms && p.n_cols / c > 128)
         c *= 2;
     const size_t heads8 = size_t((p.group + 7) & ~7);
     return start(k_block_select<DIM>, dim3(unsigned(units * c)), kSelThreads,
