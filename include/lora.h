@@ -371,8 +371,9 @@ int lora_sync_status(lora_ctx *ctx, void *stream);
  *                          guarantees that no kernel launched immediately before a
  *                          delta, merge or unmerge call in the same stream writes the
  *                          adapters' pages or the page tables (this library's own kernels
- *                          never do, page-ins apart, which are waited for; lora_kv_write
- *                          writes a unified pool's other pages; a copy or a host-side
+ *                          never do, page-ins apart, which are waited for; lora_kv_write,
+ *                          lora_kv_write_rope and lora_kv_copy write a unified pool's
+ *                          other pages; a copy or a host-side
  *                          wait in between is enough).
  *                          For lora_fused_device_ids in its default mode the guarantee
  *                          covers the device ids as well: with 1 the kernel reads them
@@ -659,7 +660,9 @@ int lora_block_select(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *bat
 
 /* lora_attention of n rows over the pages chosen for them (the fp32 and two-term weights of its
  * few-rows form): row i sees the first lens[i] tokens of its lists.  Rows with lens[i] < 0 are
- * left alone.  The selection may also be the caller's own.  out may not overlap q. */
+ * left alone.  The selection may also be the caller's own.  out may not overlap q,
+ * and a delta call right behind with it as its x must run without LORA_OPT_EARLY_INPUT, as behind
+ * lora_attention. */
 int lora_block_attention(lora_ctx *ctx, const lora_kv *kv, const lora_block_sel *sel, int64_t n,
                          const void *q, int64_t ldq, int n_heads, float scale, void *out,
                          int64_t ldo, void *stream);
