@@ -531,11 +531,12 @@ cudaError_t launch(const SelectParams &p, int sms, cudaStream_t stream)
     const cudaError_t e = allow_shared(once, k_block_select<DIM>, 226 * 1024);
     if (e != cudaSuccess)
         return e;
-    // A CTA scores 128 pages in about 2 us: more are shared, as far as the GPU has room for the
-    // CTAs at once.
+    // A CTA scores 128 pages in about 2 us: more are shared as far as the GPU has room for the CTAs at
+    // once, and more than a thousand in any case, for their balance (32 rows of up to 4125 pages, 8 key heads, 60 us
+    // with a CTA each and 47 with shares of a thousand).
     const int64_t units = int64_t(p.b.n_rows) * p.kv.heads;
     int c = 1;
-    while (c < kMaxCluster && units * c * 2 <= kSelCtas * sms && p.n_cols / c > 128)
+    while (c < kMaxCluster && ((units * c * 2 <= kSelCtas * sms && p.n_cols / c > 128) || p.n_cols / c > 1024))
         c *= 2;
     const size_t heads8 = size_t((p.group + 7) & ~7);
     return start(k_block_select<DIM>, dim3(unsigned(units * c)), kSelThreads,
