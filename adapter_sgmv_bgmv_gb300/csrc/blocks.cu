@@ -332,7 +332,12 @@ __global__ void __launch_bounds__(kSelThreads, kSelCtas) k_block_select(const __
     // Two pages of a tile a lane: the first tile's bounds too are on their way while the queries become codes.
     uint32_t a[2][J][8];
     float unit[2];
-    auto load = [&]() {
+    auto look_up = [&](int at) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            page[r] = at + 8 * r + g < hi ? table[at + 8 * r + g] : 0;
+    };
+    auto load = [&]() {                              // and the next tile's pages
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const bool there = page[r] >= 0 && page[r] < kv.n_pages;
@@ -343,16 +348,12 @@ __global__ void __launch_bounds__(kSelThreads, kSelCtas) k_block_select(const __
                 load32(src + 128 * j, a[r][j]);
             unit[r] = there ? kv.unit[where] : -1.f;
         }
-    };
-    auto look_up = [&]() {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-            page[r] = base + 8 * r + g < hi ? table[base + 8 * r + g] : 0;
+        look_up(base + kStep);
     };
     base += lo;
     if (base < hi) {
         if (at.s != row || lo != 0)
-            look_up();
+            look_up(base);
         load();
     }
     for (int h = warp; h < heads8; h += kSelWarps) {
@@ -422,10 +423,8 @@ __global__ void __launch_bounds__(kSelThreads, kSelCtas) k_block_select(const __
             }
         }
         base += kStep;
-        if (base < hi) {
-            look_up();
+        if (base < hi)
             load();
-        }
     }
     __syncthreads();
     if (n_cta > 1) {
