@@ -349,3 +349,60 @@ def test_a_selection_of_ones_own(ctx):
     assert e.value.name == "LORA_E_INVAL"
     assert torch.equal(c.out[[0, 2]], before[[0, 2]]) and bool((c.out[1] == 3).all())
     st.close()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+def test_values_that_are_not_finite(ctx, fmt):
+    """An infinity among the values of a token that a row sees reaches its own element only; a NaN, as an
+    8-bit vector keeps it, the whole vector's elements; tokens behind the row's length neither."""
+    import adapter_sgmv_bgmv_gb300 as L
+    c = Case(13, [1, 1], [200, 100], 12, 2, 128, 16, fmt=fmt)
+    k, v = c.rand(1, 2, 128), c.rand(1, 2, 128)
+    v[0, 1, 7] = math.inf
+    c.put(0, [50], k, v)                                    # its page is listed for both heads
+    c.put(1, [99], *(x.clone() for x in (k, v)))            # behind the second row's length
+    st = Step(ctx, c)
+    ids = c.pages[:, [0, 1, 3, 6]].clone()
+    sel = L.BlockSelection(torch.tensor([61, 51], dtype=torch.int32, device="cuda"), ids[:, None].expand(2, 2, 4).contiguous())
+    L.lora_block_attention(ctx, st.cache, sel, c.q, c.out)
+    ctx.sync_status()
+    lost = ~torch.isfinite(c.out)
+    want = torch.zeros_like(lost)
+    if fmt == "bf16":
+        want[0, 6:, 7] = True
+        assert bool((c.out[0, 6:, 7] == math.inf).all())
+    else:
+        want[0, 6:] = True
+    assert torch.equal(lost, want)
+    st.close()
+
+
+def test_offsets_beyond_32_bits(ctx):
+    """Pages beyond 2^32 bytes of a 6 GB pool, for the store, the bounds, the choice and the attention."""
+    import adapter_sgmv_bgmv_gb300 as L
+    n_pages, page, kv, dim = 24000, 16, 64, 128
+    pool = torch.empty((n_pages, page, kv, dim), dtype=torch.bfloat16, device="cuda")
+    cache = L.KvCache(ctx, pool, torch.empty_like(pool))
+    cache.attach_bounds(torch.zeros((n_pages, kv, 2, dim), dtype=torch.int8, device="cuda"), torch.zeros((n_pages, kv), device="cuda"))
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    m = 16 * 9 + 5
+    rows = [torch.randn((m, kv, dim), generator=gen, device="cuda").bfloat16() for _ in range(3)]
+    outs = []
+    rope = L.HeadRope((1e4 ** (-torch.arange(64) / 64)).cuda(), dim)
+    for first in (0, 23990):                                # the same tokens at both ends of the pool
+        pages = torch.arange(first, first + 10, dtype=torch.int32, device="cuda")[None]
+        lens = torch.tensor([m], dtype=torch.int32, device="cuda")
+        batch = L.KvBatch(torch.tensor([0, m], dtype=torch.int32, device="cuda"), lens, pages)
+        q = torch.empty_like(rows[0])
+        L.lora_kv_write_rope(ctx, cache, rope, batch, rows[0], rows[1], rows[2], q)
+        L.lora_kv_bounds(ctx, cache, batch, m)
+        sel = L.BlockSelection.empty(m, cache, 4)
+        L.lora_block_select(ctx, cache, batch, q, sel)
+        out = torch.empty_like(q)
+        L.lora_block_attention(ctx, cache, sel, q, out)
+        ctx.sync_status()
+        chosen = torch.where(sel.pages >= 0, sel.pages - first, -1)
+        outs.append((q, chosen, sel.lens, out, pool[first:first + 9].clone(), cache.bounds[0][first:first + 10].clone()))
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+    cache.close()
