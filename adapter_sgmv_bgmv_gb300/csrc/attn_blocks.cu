@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DIM, FMT, NR>::CTAS) k_attn_bl
             qf[r][j] = row < n_rows ? x : make_uint4(0, 0, 0, 0);
         }
     }
-    u.q = seq_info(p.b, u.s, rank == 0 && u.h == 0 && u.r == 0 ? p.status : nullptr);
+    u.q = row_info(p.b, u.s, rank == 0 && u.h == 0 && u.r == 0 ? p.status : nullptr);
     if (u.q.n_new == 0)
         return;                                            // a row of no sequence; the whole cluster
     const int n = u.q.len;

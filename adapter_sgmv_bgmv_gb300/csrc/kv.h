@@ -197,19 +197,19 @@ __device__ __forceinline__ SeqInfo checked_seq(const BatchView &b, int start, in
 // Sequence s of the batch.
 __device__ __forceinline__ SeqInfo seq_info(const BatchView &b, int s, unsigned *status)
 {
-    if (!b.starts) {
-        SeqInfo q;
-        q.start = s;
-        q.len = b.lens[s];
-        q.n_new = q.len >= 0;
-        q.len = max(q.len, 0);
-        if (q.len > b.capacity) {
-            raise_status(status, kDevBadBatch);
-            q.n_new = q.len = 0;
-        }
-        return q;
-    }
     return checked_seq(b, b.starts[s], b.starts[s + 1], b.lens[s], status);
+}
+
+// Sequence s of a batch without `starts`.
+__device__ __forceinline__ SeqInfo row_info(const BatchView &b, int s, unsigned *status)
+{
+    SeqInfo q{s, 0, 0};
+    const int len = b.lens[s];
+    if (len > b.capacity)
+        raise_status(status, kDevBadBatch);
+    else if (len >= 0)
+        q = SeqInfo{s, 1, len};
+    return q;
 }
 
 __device__ __forceinline__ int page_of(const KvView &kv, int pos)
