@@ -698,22 +698,31 @@ class _HeadsOn:
         self.head_dim, self.device_index = head_dim, device_index
 
 
-def _rope_side(x, out, what, where):
-    """(pointer, stride, rows, heads, pointer, stride) of a side and where it goes, which has its shape."""
+def _alike(x, y, where):
+    """(pointer, stride, rows, heads, pointer, stride) of two tensors of bf16 rows [n, heads, head_dim] of
+    the same shape, or None where they are not that: _head_rows says what is wrong."""
     try:
-        sh, st, so, dev = x.shape, x.stride(), out.stride(), where.device_index
+        sh, st, so, dev = x.shape, x.stride(), y.stride(), where.device_index
         n, heads, width = sh
-        if x.dtype is torch.bfloat16 and out.dtype is torch.bfloat16 and width == where.head_dim and \
-                st[1] == so[1] == width and st[2] == so[2] == 1 and out.shape == sh and x.get_device() == out.get_device() == dev:
+        if x.dtype is torch.bfloat16 and y.dtype is torch.bfloat16 and width == where.head_dim and \
+                st[1] == so[1] == width and st[2] == so[2] == 1 and y.shape == sh and x.get_device() == y.get_device() == dev:
             # the stride of a single row says nothing
-            return x.data_ptr(), st[0] if n > 1 else heads * width, n, heads, out.data_ptr(), so[0] if n > 1 else heads * width
+            return x.data_ptr(), st[0] if n > 1 else heads * width, n, heads, y.data_ptr(), so[0] if n > 1 else heads * width
     except (AttributeError, ValueError):
         pass
-    px, ldx, n, heads = _head_rows(x, what, where)
-    po, ldo, no, ho = _head_rows(out, what + "_out", where)
-    if no != n or ho != heads:
-        raise ValueError(f"{what}_out must have the shape of {what}")
-    return px, ldx, n, heads, po, ldo
+    return None
+
+
+def _rope_side(x, out, what, where):
+    """The same of a side and where it goes, which has its shape."""
+    both = _alike(x, out, where)
+    if both is None:
+        px, ldx, n, heads = _head_rows(x, what, where)
+        po, ldo, no, ho = _head_rows(out, what + "_out", where)
+        if no != n or ho != heads:
+            raise ValueError(f"{what}_out must have the shape of {what}")
+        both = px, ldx, n, heads, po, ldo
+    return both
 
 
 def _rope_on(ctx, rope, batch, head_dim):
@@ -754,8 +763,13 @@ def lora_kv_write_rope(ctx: Context, cache: KvCache, rope: HeadRope, batch: KvBa
     where = _rope_on(ctx, rope, batch, cache.head_dim)
     if where.device_index != cache.device_index:
         raise ValueError("the batch must be on the context's device")
-    pk, ldk, n, hk = _head_rows(k, "k", cache)
-    pv, ldv, nv, hv = _head_rows(v, "v", cache)
+    both = _alike(k, v, cache)
+    if both is not None:
+        pk, ldk, n, hk, pv, ldv = both
+        nv, hv = n, hk
+    else:
+        pk, ldk, n, hk = _head_rows(k, "k", cache)
+        pv, ldv, nv, hv = _head_rows(v, "v", cache)
     pq, ldq, nq, hq, pqo, ldqo = (0, 0, n, 0, 0, 0) if q is None else _rope_side(q, q if q_out is None else q_out, "q", where)
     if nv != n or nq != n or hk != cache.n_heads or hv != cache.n_heads:
         raise ValueError("q, k and v must have one row a token, k and v the cache's heads")
@@ -940,10 +954,14 @@ def lora_block_attention(ctx: Context, cache: KvCache, selection: BlockSelection
                          scale: float | None = None, stream=None):
     """out <- attention of q (bf16 [n, heads, head_dim]) over the pages chosen for each row.
     scale: None for head_dim ** -0.5."""
-    pq, ldq, n, hq = _head_rows(q, "q", cache)
-    po, ldo, no, ho = _head_rows(out, "out", cache)
-    if no != n or ho != hq:
-        raise ValueError("out must have the shape of q")
+    both = _alike(q, out, cache)
+    if both is not None:
+        pq, ldq, n, hq, po, ldo = both
+    else:
+        pq, ldq, n, hq = _head_rows(q, "q", cache)
+        po, ldo, no, ho = _head_rows(out, "out", cache)
+        if no != n or ho != hq:
+            raise ValueError("out must have the shape of q")
     _selected(cache, selection, n)
     if scale is None:
         scale = cache.head_dim ** -0.5

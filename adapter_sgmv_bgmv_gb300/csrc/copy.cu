@@ -34,7 +34,17 @@ struct Shape {
     int unit_shift;                          // log2 of a vector's 16-byte units
 };
 
-__global__ void __launch_bounds__(kThreads, kCtas) k_kv_copy(const __grid_constant__ KvCopyParams p, Shape sh)
+// The caches travel in the launch's parameters: up to eight in an eighth of the bytes that 64 take, half a
+// microsecond less on the host.
+template <int CACHES>
+struct Params : KvCopyLists {
+    KvView kv[CACHES];
+    int n_kv;
+    unsigned *status;
+};
+
+template <int CACHES>
+__global__ void __launch_bounds__(kThreads, kCtas) k_kv_copy(const __grid_constant__ Params<CACHES> p, Shape sh)
 {
     __shared__ int pairs[kList];
     __shared__ int counts[kWarps];
@@ -126,19 +136,31 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_kv_copy(const __grid_consta
     }
 }
 
+template <int CACHES>
+cudaError_t launch(const KvView *kv, int n_kv, const KvCopyLists &lists, unsigned *status, const Shape &sh, unsigned ctas, cudaStream_t stream)
+{
+    Params<CACHES> p;
+    static_cast<KvCopyLists &>(p) = lists;
+    std::copy(kv, kv + n_kv, p.kv);
+    p.n_kv = n_kv;
+    p.status = status;
+    return start(k_kv_copy<CACHES>, dim3(ctas), kThreads, 0, 0, stream, p, sh);
+}
+
 }  // namespace
 
-cudaError_t launch_kv_copy(const KvCopyParams &p, int sms, cudaStream_t stream)
+cudaError_t launch_kv_copy(const KvView *kv, int n_kv, const KvCopyLists &lists, unsigned *status, int sms, cudaStream_t stream)
 {
-    const KvView &kv = p.kv[0];
-    const int bytes = kv.dim * (kv.format == kKvBf16 ? 2 : 1);
+    const int bytes = kv->dim * (kv->format == kKvBf16 ? 2 : 1);
     Shape sh;
-    sh.per_cell = Divider(kv.heads);
+    sh.per_cell = Divider(kv->heads);
     sh.unit_shift = bytes == 256 ? 4 : bytes == 128 ? 3 : 2;
-    const int64_t vecs = int64_t(kv.page_size) * kv.heads;
+    const int64_t vecs = int64_t(kv->page_size) * kv->heads;
     sh.parts = int((vecs * bytes + kItem - 1) / kItem);
-    const int64_t items = int64_t(p.n) * p.n_kv * 2 * sh.parts;
-    return start(k_kv_copy, dim3(unsigned(std::min<int64_t>(int64_t(kCtas) * sms, items))), kThreads, 0, 0, stream, p, sh);
+    const int64_t items = int64_t(lists.n) * n_kv * 2 * sh.parts;
+    const unsigned ctas = unsigned(std::min<int64_t>(int64_t(kCtas) * sms, items));
+    return n_kv <= 8 ? launch<8>(kv, n_kv, lists, status, sh, ctas, stream)
+                     : launch<kMaxCopyCaches>(kv, n_kv, lists, status, sh, ctas, stream);
 }
 
 }  // namespace lora

@@ -143,13 +143,11 @@ cudaError_t launch_pages_compact(const TableView &t, int32_t *src, int32_t *dst,
 
 // Copies of pages within each of some caches of one shape (copy.cu).
 constexpr int kMaxCopyCaches = 64;
-struct KvCopyParams {
-    KvView kv[kMaxCopyCaches];
+struct KvCopyLists {
     const int32_t *src, *dst, *cells;
-    int n, n_kv;
-    unsigned *status;
+    int n;
 };
-cudaError_t launch_kv_copy(const KvCopyParams &p, int sms, cudaStream_t stream);
+cudaError_t launch_kv_copy(const KvView *kv, int n_kv, const KvCopyLists &lists, unsigned *status, int sms, cudaStream_t stream);
 
 // Bounds of pages, and the choice of pages by them (blocks.cu).
 struct BoundsParams {

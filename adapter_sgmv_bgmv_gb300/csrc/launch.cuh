@@ -24,7 +24,7 @@ cudaError_t start(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = cluster ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<const P &>(args)...);
 }
 
 template <typename K>

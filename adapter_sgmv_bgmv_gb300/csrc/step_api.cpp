@@ -241,17 +241,12 @@ int lora_kv_copy(lora_ctx *ctx, const lora_kv *const *kvs, int n_kv, const int32
     const int rc = ctx_begin(ctx, stream);
     if (rc != LORA_OK || n == 0)
         return rc;
-    KvCopyParams p{};
-    p.src = src;
-    p.dst = dst;
-    p.cells = cells;
-    p.n = int(n);
-    p.status = ctx_status(ctx);
+    KvView views[kMaxCopyCaches];
     for (int at = 0; at < n_kv; at += kMaxCopyCaches) {
-        p.n_kv = std::min(n_kv - at, kMaxCopyCaches);
-        for (int i = 0; i < p.n_kv; ++i)
-            p.kv[i] = kvs[at + i]->view;
-        const cudaError_t e = launch_kv_copy(p, ctx_sms(ctx), stream);
+        const int some = std::min(n_kv - at, kMaxCopyCaches);
+        for (int i = 0; i < some; ++i)
+            views[i] = kvs[at + i]->view;
+        const cudaError_t e = launch_kv_copy(views, some, KvCopyLists{src, dst, cells, int(n)}, ctx_status(ctx), ctx_sms(ctx), stream);
         if (e != cudaSuccess)
             return ctx_cuda_fail(ctx, e);
         ctx_launched(ctx, stream, 1024);
