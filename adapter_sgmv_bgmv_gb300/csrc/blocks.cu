@@ -14,7 +14,7 @@
 //
 // Measured (heads of 128).  Bounds: 16 prompts of 1056 tokens, 32 heads, bf16 24.6 us, 5.8 TB/s (0.86
 // of a copy's rate); one decode's page of 64 tokens of 8 heads 4 us.  Choice: one row of 512 pages 6.2 us, 32
-// rows of up to 409 pages, 64 heads on 8, 11.9 us, 39 rows of up to 1504 pages, 28 heads on 4, 19 us: chains of
+// rows of up to 409 pages, 64 heads on 8, 11.6 us, 39 rows of up to 1504 pages, 28 heads on 4, 19 us: chains of
 // latencies (lengths, pages, bounds, products, three passes over the scores, output).
 #include <cuda_runtime.h>
 

@@ -19,7 +19,7 @@
 // once; norms add an exchange over the vector's lanes to each item's chain), the chain launch,
 // lengths, angles for a decode batch.
 //
-// Measured: 16,896 rows of 32 + 32 heads of 128 without norms 87 us, 6.4 TB/s (0.94 of a copy's
+// Measured: 16,896 rows of 32 + 32 heads of 128 without norms 86 us, 6.4 TB/s (0.95 of a copy's
 // rate); 8191 rows of 32 + 8 heads with norms and the store into a bf16 cache 41 us (36 without the
 // norms), 4.9 TB/s.  Eight elements a lane, pairs in two lanes and exchanged, took 173 and 58 us, bound by
 // instructions; three CTAs a SM instead of four 89 and 41, five 91 and 53.
