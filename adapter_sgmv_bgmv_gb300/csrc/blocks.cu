@@ -1,6 +1,6 @@
 // Attention over a part of the cache: bounds of each page's keys, and the choice of pages for
 // every new token and key head by a cheap score (the attention over what is chosen is
-// attn_rows.cu's, each row a sequence with a page list for each key head).
+// attn_blocks.cu's).
 //
 // Bounds: the smallest and largest key of a page for each element, as 8-bit codes with one
 // power-of-two unit for a page and head.  Score of a page for a row:
@@ -8,7 +8,7 @@
 //   max over the group's query heads g of  unit_page unit_g sum_d max(c_d lo_d, c_d hi_d)
 //
 // with c the codes of query head g, taken the same way.  Units that are powers of two make
-// every step exact: codes are x / unit rounded once, the sum is of integers below 2^21 (dp4a),
+// every step exact: codes are x / unit rounded once, the sum is of integers below 2^21,
 // the products with the units only move the exponent.  The choice so depends on the inputs
 // alone, not on the order of sums, and equal scores go to the lower page.
 //
@@ -324,6 +324,11 @@ __global__ void __launch_bounds__(kSelThreads, kSelCtas) k_block_select(const __
                 out[i] = i >= cols ? -1 : cols <= p.blocks || i < p.first ? table[i] : table[cols - p.blocks + i];
         return;
     }
+    // the scores go to the first CTA's shared memory, which has to have started by then
+    if (n_cta > 1) {
+        __syncwarp();
+        cluster_arrive_relaxed();
+    }
     // the columns to choose from, [lo, hi) of them this CTA's
     const int n = cols - p.first - p.last, share = (n + n_cta - 1) / n_cta;
     const int lo = min(n, rank * share), hi = min(n, lo + share);
@@ -428,6 +433,8 @@ __global__ void __launch_bounds__(kSelThreads, kSelCtas) k_block_select(const __
     }
     __syncthreads();
     if (n_cta > 1) {
+        __syncwarp();
+        cluster_wait_acquire();
         if (rank != 0)
             for (int i = lo + int(threadIdx.x); i < hi; i += kSelThreads)
                 st_cluster(keys + i, 0, keys[i]);
