@@ -13,7 +13,7 @@
 // alone, not on the order of sums, and equal scores go to the lower page.
 //
 // Measured (heads of 128).  Bounds: 16 prompts of 1056 tokens, 32 heads, bf16 24.6 us, 5.8 TB/s (0.86
-// of a copy's rate); one decode's page of 64 tokens of 8 heads 4 us.  Choice: one row of 512 pages 6.2 us, 32
+// of a copy's rate); one decode's page of 64 tokens of 8 heads 3 us.  Choice: one row of 512 pages 6.2 us, 32
 // rows of up to 409 pages, 64 heads on 8, 11.6 us, 39 rows of up to 1504 pages, 28 heads on 4, 19 us: chains of
 // latencies (lengths, pages, bounds, products, three passes over the scores, output).
 #include <cuda_runtime.h>
@@ -46,6 +46,20 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return y;
 }
 
+__device__ __forceinline__ float min3_nan(float a, float b, float c)
+{
+    float y;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+__device__ __forceinline__ float max3_nan(float a, float b, float c)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 // The unit for numbers up to `top`: 2^(e - 6) with 2^e <= top < 2^(e + 1), e at least -100; and
 // its reciprocal.  NaN where top is not finite.
 __device__ __forceinline__ float unit_for(float top, float &inverse)
@@ -60,14 +74,15 @@ __device__ __forceinline__ int code_of(float x, float inverse) { return max(-127
 // ---------------------------------------------------------------- bounds
 
 // A CTA looks at `rows` rows of the call: each that is its sequence's first in a page stands for
-// the page, and the page's vectors [cells][dim] of each head are a warp's, four loads a lane (eight in
-// 8 bits) under way.  Every page touched is read once; DRAM bounds it.
+// the page, and the page's vectors [cells][dim] of each head are a warp's, four loads a lane (two in
+// 8 bits) under way.  Every page touched is read once: DRAM bounds it in bf16, in 8 bits the conversions and
+// the registers they take (with eight loads under way 45 us for 16 prompts of 1056 tokens, 32 heads, now 31).
 template <int DIM, int FMT>
 __global__ void __launch_bounds__(kThreads) k_kv_bounds(const __grid_constant__ BoundsParams p, int rows)
 {
     constexpr int E = FMT == kKvBf16 ? 8 : 16;       // elements of a lane's 16 bytes
     constexpr int L = DIM / E, CW = 32 / L;          // lanes of a cell, cells a warp's load
-    constexpr int U = FMT == kKvBf16 ? 4 : 8;
+    constexpr int U = FMT == kKvBf16 ? 4 : 2;
     __shared__ int pages[kThreads], filled[kThreads], n_pages;
     const KvView &kv = p.kv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -138,73 +153,117 @@ __global__ void __launch_bounds__(kThreads) k_kv_bounds(const __grid_constant__ 
                 sc[u] = FMT == kKvBf16 ? 1.f : scales[c * kv.s_cell];
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < U; u += 2) {
                 if (FMT == kKvBf16) {
-                    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&x[u]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        lo2[e] = __hmin2_nan(lo2[e], h[e]);
-                        hi2[e] = __hmax2_nan(hi2[e], h[e]);
-                    }
-                } else {
-                    const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint2 v = widen4<FMT == kKvFp8 ? kKvFp8 : kKvInt8>(w[i]);
-                        const float f[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
-                                            __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)};
+                    for (int v = 0; v < 2; ++v) {
+                        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&x[u + v]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            lo[(4 * i + e) % E] = min_nan(lo[(4 * i + e) % E], f[e] * sc[u]);
-                            hi[(4 * i + e) % E] = max_nan(hi[(4 * i + e) % E], f[e] * sc[u]);
+                            lo2[e] = __hmin2_nan(lo2[e], h[e]);
+                            hi2[e] = __hmax2_nan(hi2[e], h[e]);
                         }
+                    }
+                } else {
+                    // two cells at once: instructions that take the least of three
+                    float f[2][E];
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        const uint32_t w[4] = {x[u + v].x, x[u + v].y, x[u + v].z, x[u + v].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint2 y = widen4<FMT == kKvFp8 ? kKvFp8 : kKvInt8>(w[i]);
+                            float *at = f[v] + 4 * i % E;
+                            at[0] = __uint_as_float(y.x << 16) * sc[u + v], at[1] = __uint_as_float(y.x & 0xffff0000u) * sc[u + v];
+                            at[2] = __uint_as_float(y.y << 16) * sc[u + v], at[3] = __uint_as_float(y.y & 0xffff0000u) * sc[u + v];
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        lo[e] = min3_nan(lo[e], f[0][e], f[1][e]);
+                        hi[e] = max3_nan(hi[e], f[0][e], f[1][e]);
                     }
                 }
             }
         }
-        if (FMT == kKvBf16)
+        int8_t *dst = kv.bounds + (page * kv.heads + head) * 2 * DIM;
+        float top = 0.f, inverse, unit;
+        if constexpr (FMT == kKvBf16) {
+            // every lane has all lanes' bounds of its elements, the first ones of each write them
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 lo[2 * e] = __low2float(lo2[e]), lo[2 * e + 1] = __high2float(lo2[e]);
                 hi[2 * e] = __low2float(hi2[e]), hi[2 * e + 1] = __high2float(hi2[e]);
             }
-        float top = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
+            for (int e = 0; e < E; ++e) {
 #pragma unroll
-            for (int o = L; o < 32; o <<= 1) {
-                lo[e] = min_nan(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
-                hi[e] = max_nan(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
+                for (int o = L; o < 32; o <<= 1) {
+                    lo[e] = min_nan(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
+                    hi[e] = max_nan(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
+                }
+                top = max_nan(top, max_nan(fabsf(lo[e]), fabsf(hi[e])));
             }
-            top = max_nan(top, max_nan(fabsf(lo[e]), fabsf(hi[e])));
-        }
 #pragma unroll
-        for (int o = 1; o < L; o <<= 1)
-            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float inverse;
-        const float unit = unit_for(top, inverse);
-        if (off == 0) {
-            uint32_t c[2][E / 4];
+            for (int o = 1; o < L; o <<= 1)
+                top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+            unit = unit_for(top, inverse);
+            if (off == 0) {
+                uint32_t c[2][2] = {};
+                if (unit == unit)
 #pragma unroll
-            for (int w = 0; w < E / 4; ++w) {
-                c[0][w] = c[1][w] = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (unit == unit) {
-                        c[0][w] |= uint32_t(code_of(lo[4 * w + e], inverse) & 0xff) << (8 * e);
-                        c[1][w] |= uint32_t(code_of(hi[4 * w + e], inverse) & 0xff) << (8 * e);
+                    for (int e = 0; e < E; ++e) {
+                        c[0][e / 4] |= uint32_t(code_of(lo[e], inverse) & 0xff) << (e % 4 * 8);
+                        c[1][e / 4] |= uint32_t(code_of(hi[e], inverse) & 0xff) << (e % 4 * 8);
                     }
+                dst += sub * E;
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(c[0][0], c[0][1]);
+                *reinterpret_cast<uint2 *>(dst + DIM) = make_uint2(c[1][0], c[1][1]);
             }
-            int8_t *dst = kv.bounds + (page * kv.heads + head) * 2 * DIM + sub * E;
+        } else {
+            // Lanes with the same 16 elements join by halves: at each step a lane keeps one half of what
+            // it has, its partner the other, until each has N of them.  (In bf16, where there is
+            // less to join, this takes a quarter longer.)
+            constexpr int N = DIM / 32;
+            int first = sub * E;
 #pragma unroll
-            for (int side = 0; side < 2; ++side)
-                if (E == 16)
-                    *reinterpret_cast<uint4 *>(dst + side * DIM) = make_uint4(c[side][0], c[side][1], c[side][E / 4 - 2], c[side][E / 4 - 1]);
-                else
-                    *reinterpret_cast<uint2 *>(dst + side * DIM) = make_uint2(c[side][0], c[side][1]);
-            if (sub == 0)
-                kv.unit[page * kv.heads + head] = unit;
+            for (int o = L, half = E / 2; o < 32; o <<= 1, half >>= 1) {
+                const bool upper = lane & o;
+                first += upper ? half : 0;
+#pragma unroll
+                for (int e = 0; e < half; ++e) {
+                    const float lo_give = upper ? lo[e] : lo[e + half], hi_give = upper ? hi[e] : hi[e + half];
+                    lo[e] = min_nan(upper ? lo[e + half] : lo[e], __shfl_xor_sync(0xffffffffu, lo_give, o));
+                    hi[e] = max_nan(upper ? hi[e + half] : hi[e], __shfl_xor_sync(0xffffffffu, hi_give, o));
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                top = max_nan(top, max_nan(fabsf(lo[e]), fabsf(hi[e])));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+            unit = unit_for(top, inverse);
+            uint32_t below = 0, above = 0;
+            if (unit == unit)
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    below |= uint32_t(code_of(lo[e], inverse) & 0xff) << (8 * e);
+                    above |= uint32_t(code_of(hi[e], inverse) & 0xff) << (8 * e);
+                }
+            dst += first;
+            if (N == 4) {
+                *reinterpret_cast<uint32_t *>(dst) = below;
+                *reinterpret_cast<uint32_t *>(dst + DIM) = above;
+            } else {
+                *reinterpret_cast<uint16_t *>(dst) = uint16_t(below);
+                *reinterpret_cast<uint16_t *>(dst + DIM) = uint16_t(above);
+            }
         }
+        // (asked for as `lane == 0`, this leaves the compiler at 32 registers in bf16 instead of 40, with
+        // fewer loads under way, and 16 prompts' bounds take a fifth longer)
+        if (off == 0 && sub == 0)
+            kv.unit[page * kv.heads + head] = unit;
     }
 }
 
