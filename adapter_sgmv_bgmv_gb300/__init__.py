@@ -832,7 +832,8 @@ def lora_pages_extend(ctx: Context, table: PageTable, grow: torch.Tensor, got: t
                       dst: torch.Tensor, cells: torch.Tensor, stream=None):
     """Sequence s grows by grow[s] tokens, as far as the free pages go: got[s] is what it got.
     src, dst and cells are the pages to copy (lora_kv_copy) before the new tokens are written.
-    All int32 [n_seqs]."""
+    All int32 [n_seqs].  A batch that has rows for sequences that got none takes the lengths
+    torch.where(got == grow, table.lens, 0): table.lens would have them replace tokens that are there."""
     dev, n = _table_on(ctx, table), table.lens.shape[0]
     rc = _L.lora_pages_extend(ctx.handle, table._ref, _ints(grow, "grow", dev, n), _ints(got, "got", dev, n),
                               _ints(src, "src", dev, n), _ints(dst, "dst", dev, n), _ints(cells, "cells", dev, n),

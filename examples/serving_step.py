@@ -104,11 +104,15 @@ class PagedRequests:
         self.got, self.src, self.dst, self.cells = new(n), new(n), new(n), new(n)
 
     def grow(self, new):
-        """The batch in which request s gets new[s] tokens (as many as `got` says there was room for)."""
+        """The batch in which request s gets new[s] tokens.  One that there is no room for stays as it was
+        (got[s] is 0): the batch has a length of 0 for it, so that its rows have no position, nothing
+        of them is stored and their attention is zeros; they can be offered again.  Nothing here waits for the GPU."""
         to = lambda a: torch.from_numpy(np.asarray(a, np.int32)).to(self.got.device)  # noqa: E731
-        L.lora_pages_extend(self.ctx, self.table, to(new), self.got, self.src, self.dst, self.cells)
+        asked = to(new)
+        L.lora_pages_extend(self.ctx, self.table, asked, self.got, self.src, self.dst, self.cells)
         L.lora_kv_copy(self.ctx, self.caches, self.src, self.dst, self.cells)
-        return L.KvBatch(to(np.concatenate([[0], np.cumsum(new)])), self.table.lens, self.table.pages, max_new=int(max(new)))
+        lens = torch.where(self.got == asked, self.table.lens, 0)
+        return L.KvBatch(to(np.concatenate([[0], np.cumsum(new)])), lens, self.table.pages, max_new=int(max(new)))
 
     def fork(self, parents, children):
         to = lambda a: torch.tensor(a, dtype=torch.int32, device=self.got.device)  # noqa: E731

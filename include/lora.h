@@ -583,7 +583,12 @@ typedef struct {
  * the next write (else -1, -1, 0); of sequences that write into one page in one call the last
  * keeps it, if nobody else holds it.  got[s] is grow[s], or 0 for a sequence that stays as it
  * is: the first for which the free pages do not suffice and all that grow after it, and one that
- * would outgrow its row.  All arrays are [n_seqs]. */
+ * would outgrow its row.  All arrays are [n_seqs].
+ *
+ * A batch of the step has to follow got.  Rows of a sequence that got none would be taken for the
+ * last tokens that it already has, which a write replaces, for whoever shares them too.  Either
+ * starts leaves them out, or, where the rows are fixed (a captured step), the batch has lens of its
+ * own, lens[s] where got[s] == grow[s] and else 0, made on the device: rows without a position. */
 int lora_pages_extend(lora_ctx *ctx, const lora_page_table *table, const int32_t *grow, int32_t *got,
                       int32_t *src, int32_t *dst, int32_t *cells, void *stream);
 
