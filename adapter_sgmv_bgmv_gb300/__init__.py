@@ -21,7 +21,7 @@ __all__ = ["LoraError", "Context", "AdapterTable", "lora_plan_build", "lora_shri
            "lora_expand", "lora_fused", "lora_fused_noalloc", "lora_base_fused", "PreparedFused", "PreparedFusedDeviceIds", "lora_merge", "lora_unmerge", "lora_page_in", "lora_fused_device_ids", "lora_tune_shape",
            "KvCache", "KvBatch", "lora_kv_write", "lora_kv_read", "lora_attention",
            "HeadRope", "lora_head_rope", "lora_kv_write_rope",
-           "PageTable", "lora_pages_extend", "lora_pages_fork", "lora_pages_free", "lora_pages_compact", "lora_kv_copy",
+           "PageTable", "PAGE_PINNED", "lora_pages_extend", "lora_pages_fork", "lora_pages_free", "lora_pages_compact", "lora_kv_copy",
            "BlockSelection", "lora_kv_bounds", "lora_block_select", "lora_block_attention",
            "KIND_ROWS_FUSED", "KIND_SHRINK", "KIND_EXPAND", "KIND_TILE_FUSED", "KIND_MERGE",
            "OPT_TILE_PATH", "OPT_MERGE_KERNEL", "OPT_TILE_MIN_RUN", "OPT_EARLY_PAGES", "OPT_DEVICE_PLAN",
@@ -795,10 +795,14 @@ def _ints(t: torch.Tensor, what: str, device: int, n: int | None = None) -> int:
     raise ValueError(f"{what} must be a contiguous int32 tensor [{'n' if n is None else n}]")
 
 
+PAGE_PINNED = 1 << 30
+
+
 class PageTable:
     """Which sequence holds which pages (see include/lora.h): lens [n_seqs], pages [n_seqs,
     n_cols] and refs [n_pages], int32 CUDA tensors that the lora_pages_* calls change.  lens and
-    pages may be a KvBatch's."""
+    pages may be a KvBatch's.  refs[page] += PAGE_PINNED keeps a page that something else uses,
+    an adapter's in a unified pool for instance, where it is."""
 
     def __init__(self, lens: torch.Tensor, pages: torch.Tensor, refs: torch.Tensor, page_size: int):
         for t, nm, dim in ((lens, "lens", 1), (pages, "pages", 2), (refs, "refs", 1)):
@@ -864,8 +868,8 @@ def lora_pages_free(ctx: Context, table: PageTable, seqs: torch.Tensor, keep: to
 
 def lora_pages_compact(ctx: Context, table: PageTable, src: torch.Tensor, dst: torch.Tensor,
                        top: torch.Tensor | None = None, stream=None):
-    """Moves held pages to the front of the pool, as many as src and dst (int32 [n]) list: the
-    moves for lora_kv_copy, -1 behind the last.  top (int32 [1]) becomes the end of the highest
+    """Moves held pages to the front of the pool, pinned ones apart, as many as src and dst (int32
+    [n]) list: the moves for lora_kv_copy, -1 behind the last.  top (int32 [1]) becomes the end of the highest
     held page."""
     dev = _table_on(ctx, table)
     n = src.shape[0]

@@ -2,7 +2,8 @@
 // that are held move to the front of the pool.  Integers only; every result is determined by
 // the inputs (the lowest free page first, lists in order), not by who comes first.
 //
-// refs[page] counts the sequences that hold a page; 0 is free.  Extend and compact have to
+// refs[page] counts the sequences that hold a page; 0 is free, LORA_PAGE_PINNED and more stays where it
+// is.  Extend and compact have to
 // rank the free (or held) pages of the whole pool: one cluster of up to eight CTAs, each warp
 // a run of pages, counts first, exchanges the counts through shared memory and walks its run
 // again with its rank at hand.  Every wait in between is a hardware barrier of the block or the cluster.
@@ -17,6 +18,7 @@
 
 #include <algorithm>
 
+#include "../../include/lora.h"
 #include "kv.h"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -77,11 +79,14 @@ __device__ __forceinline__ Run my_run(int n_pages, int n_cta)
     return {int(min(w * chunk, int64_t(n_pages))), int(min((w + 1) * chunk, int64_t(n_pages)))};
 }
 
-// Pages of the run with refs > 0; the same in all lanes.
-__device__ __forceinline__ int count_held(const int32_t *refs, const Run &r)
+// Pages of the run with refs of `least` and more; the same in all lanes.
+template <int K>
+__device__ __forceinline__ void count_pages(const int32_t *refs, const Run &r, const int (&least)[K], int (&n)[K])
 {
     const int lane = threadIdx.x & 31;
-    int n = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        n[k] = 0;
     for (int base = r.lo; base < r.hi; base += 32 * kUnroll) {
         int v[kUnroll];
 #pragma unroll
@@ -89,34 +94,41 @@ __device__ __forceinline__ int count_held(const int32_t *refs, const Run &r)
             v[u] = base + u * 32 + lane < r.hi ? refs[base + u * 32 + lane] : 0;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-            n += v[u] > 0;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                n[k] += v[u] >= least[k];
     }
-    return __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        n[k] = __reduce_add_sync(0xffffffffu, n[k]);
 }
 
-// What all warps counted: the sum ahead of this warp's and over the cluster.  `counts` is one
-// entry a warp in every CTA's shared memory; ends behind a cluster barrier, and the caller has
+// What all warps counted, K numbers each: the sums ahead of this warp's and over the cluster.  `counts`
+// is K entries a warp in every CTA's shared memory; ends behind a cluster barrier, and the caller has
 // to pass another before it leaves.
-__device__ __forceinline__ void rank_warps(int mine, int *counts, int n_cta, int &before, int &total)
+template <int K>
+__device__ __forceinline__ void rank_warps(const int (&mine)[K], int (*counts)[kWarps], int n_cta, int (&before)[K], int (&total)[K])
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = int(cluster_ctarank());
-    if (lane == 0)
-        counts[warp] = mine;
-    if (n_cta == 1) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (lane == 0)
+            counts[k][warp] = mine[k];
+        before[k] = total[k] = 0;
+    }
+    if (n_cta == 1)
         __syncthreads();
-        const int v = counts[lane];
-        total = __reduce_add_sync(0xffffffffu, v);
-        before = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
-        return;
-    }
-    cluster_barrier();
-    before = total = 0;
-    for (int c = 0; c < n_cta; ++c) {
-        int v;
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_cluster(smem_u32(counts + lane), c)) : "memory");
-        total += __reduce_add_sync(0xffffffffu, v);
-        before += __reduce_add_sync(0xffffffffu, c < rank || (c == rank && lane < warp) ? v : 0);
-    }
+    else
+        cluster_barrier();
+    for (int c = 0; c < n_cta; ++c)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            int v = counts[k][lane];
+            if (n_cta > 1)
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_cluster(smem_u32(&counts[k][lane]), c)) : "memory");
+            total[k] += __reduce_add_sync(0xffffffffu, v);
+            before[k] += __reduce_add_sync(0xffffffffu, c < rank || (c == rank && lane < warp) ? v : 0);
+        }
 }
 
 // ---------------------------------------------------------------- extend
@@ -140,14 +152,15 @@ __global__ void __launch_bounds__(kThreads) k_pages_extend(const __grid_constant
     Want *want = reinterpret_cast<Want *>(smem);
     int *mark = reinterpret_cast<int *>(want + t.n_seqs);        // the shared page a sequence would write into, or -1
     __shared__ long long sums[kWarps];
-    __shared__ int counts[kWarps];
+    __shared__ int counts[1][kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = int(cluster_ctarank());
     unsigned *status = rank == 0 ? t.status : nullptr;
     grid_dep_wait();
     grid_dep_launch();
 
     const Run run = my_run(t.n_pages, n_cta);
-    const int held = count_held(t.refs, run);
+    int held[1];
+    count_pages(t.refs, run, {1}, held);
 
     // What each sequence wants: every CTA works it out for itself.
     int any = 0;
@@ -210,9 +223,9 @@ __global__ void __launch_bounds__(kThreads) k_pages_extend(const __grid_constant
         }
     }
 
-    int held_before, held_all;
+    int held_before[1], held_all[1];
     rank_warps(held, counts, n_cta, held_before, held_all);      // behind it nobody reads lens or another's refs
-    const int free_all = t.n_pages - held_all;
+    const int free_all = t.n_pages - held_all[0];
 
     if (rank == 0)
         for (int s = threadIdx.x; s < t.n_seqs; s += kThreads) {
@@ -227,8 +240,8 @@ __global__ void __launch_bounds__(kThreads) k_pages_extend(const __grid_constant
         }
     // The free pages in order, each to whoever wants one of its rank.
     const int wanted = t.n_seqs ? want[t.n_seqs - 1].upto : 0;
-    int next = run.lo - held_before;
-    if (held < run.hi - run.lo)
+    int next = run.lo - held_before[0];
+    if (held[0] < run.hi - run.lo)
         for (int base = run.lo; base < run.hi && next < wanted; base += 32) {
             const int id = base + lane;
             const bool is_free = id < run.hi && t.refs[id] <= 0;
@@ -359,9 +372,13 @@ __global__ void __launch_bounds__(kThreads) k_pages_free(const __grid_constant__
                 continue;
             if (page[b] < 0 || page[b] >= t.n_pages) {
                 raise_status(t.status, kDevBadPage);
-            } else if (atomicSub(&t.refs[page[b]], 1) <= 0) {
-                atomicAdd(&t.refs[page[b]], 1);      // nobody holds it: the table is wrong
-                raise_status(t.status, kDevBadPage);
+            } else {
+                const int was = atomicSub(&t.refs[page[b]], 1);
+                // no sequence holds it (others may just be finding out the same): the table is wrong
+                if (was <= 0 || (was <= LORA_PAGE_PINNED && was > LORA_PAGE_PINNED - kMaxTableSeqs)) {
+                    atomicAdd(&t.refs[page[b]], 1);
+                    raise_status(t.status, kDevBadPage);
+                }
             }
             row[c] = -1;
         }
@@ -372,27 +389,35 @@ __global__ void __launch_bounds__(kThreads) k_pages_free(const __grid_constant__
 
 // ---------------------------------------------------------------- compact
 
-// With L held pages, the held ones at L and above move to the free ones below it: the highest
-// to the lowest.  A free page `id` below L is the (id - held before it)-th hole, a held page
-// at or above L has L - 1 - held before it higher movers: both know their place in the lists.
+// A pinned page stays where it is and takes no part: the others have their places between them,
+// place = id - pinned pages before it.  With L held ones of those, the held ones at places from L on
+// move to the free places below L: the highest to the lowest.  A free page at place p < L is
+// the (p - held before it)-th hole, a held one at p >= L has L - 1 - held before it higher movers:
+// both know their position in the lists.
 __global__ void __launch_bounds__(kThreads) k_pages_compact(const __grid_constant__ TableView t, int32_t *src,
                                                             int32_t *dst, int n, int32_t *top, int n_cta)
 {
-    __shared__ int counts[kWarps];
+    __shared__ int counts[2][kWarps];
     const int lane = threadIdx.x & 31, at = int(cluster_ctarank()) * kThreads + int(threadIdx.x), all = n_cta * kThreads;
     grid_dep_wait();
     grid_dep_launch();
     for (int k = at; k < n; k += all)
         src[k] = dst[k] = -1;
-    const Run run = my_run(t.n_pages, n_cta);
-    const int held = count_held(t.refs, run);
-    int first, total;
-    rank_warps(held, counts, n_cta, first, total);
-    int before = first;
     if (at == 0 && top)
-        *top = total;                                // unless a mover stays (below)
-    // a run of free pages at or above L, or of held ones below it, has nothing to say
-    if (!(held == 0 && run.lo >= total) && !(held == run.hi - run.lo && run.hi <= total))
+        *top = 0;
+    const Run run = my_run(t.n_pages, n_cta);
+    int mine[2], first[2], sums[2];                  // held pages, and how many of them are pinned
+    count_pages(t.refs, run, {1, LORA_PAGE_PINNED}, mine);
+    rank_warps(mine, counts, n_cta, first, sums);
+    const int pinned = mine[1], held = mine[0] - pinned, total = sums[0] - sums[1];
+    const int held0 = first[0] - first[1], pinned0 = first[1];
+    int end = 0;                                     // of the highest page that this lane knows is held in the end
+    // a run of free pages at or above L, or of held ones below it, has nothing to move
+    if (pinned == 0 && ((held == 0 && run.lo - pinned0 >= total) || (held == run.hi - run.lo && run.hi - pinned0 <= total))) {
+        if (held > 0 && run.hi - pinned0 == total)
+            end = run.hi;
+    } else {
+        int before = held0, pins = pinned0;
         for (int base = run.lo; base < run.hi; base += 32 * 4) {
             int v[4];
 #pragma unroll
@@ -401,32 +426,50 @@ __global__ void __launch_bounds__(kThreads) k_pages_compact(const __grid_constan
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int id = base + u * 32 + lane;
-                const unsigned m = __ballot_sync(0xffffffffu, v[u] > 0);
-                const int ahead = before + __popc(m & ((1u << lane) - 1));
+                const bool pin = v[u] >= LORA_PAGE_PINNED, on = v[u] > 0 && !pin;
+                const unsigned below = (1u << lane) - 1, m = __ballot_sync(0xffffffffu, on);
+                const int ahead = before + __popc(m & below);
                 before += __popc(m);
+                int place = id - pins;
+                if (pinned) {
+                    const unsigned mp = __ballot_sync(0xffffffffu, pin);
+                    place -= __popc(mp & below);
+                    pins += __popc(mp);
+                }
                 if (id >= run.hi)
                     continue;
-                if (id < total) {
-                    if (v[u] <= 0 && id - ahead < n)
-                        dst[id - ahead] = id;
-                } else if (v[u] > 0 && total - 1 - ahead < n) {
+                if (pin || place == total - 1)       // the last place is held if all move; else one that stays is higher
+                    end = id + 1;
+                if (pin)
+                    continue;
+                if (place < total) {
+                    if (!on && place - ahead < n)
+                        dst[place - ahead] = id;
+                } else if (on && total - 1 - ahead < n) {
                     src[total - 1 - ahead] = id;
                 }
             }
         }
+    }
     cluster_barrier();
     // Where the lists are full, the mover with n higher ones is the highest that stays.
     if (top && (n == 0 || src[n - 1] >= 0) && held > 0 && run.hi > total) {
-        int b = first;
+        int b = held0;
         for (int base = run.lo; base < run.hi; base += 32) {
             const int id = base + lane;
-            const bool on = id < run.hi && t.refs[id] > 0;
+            const int v = id < run.hi ? t.refs[id] : 0;
+            const bool on = v > 0 && v < LORA_PAGE_PINNED;
             const unsigned m = __ballot_sync(0xffffffffu, on);
             const int ahead = b + __popc(m & ((1u << lane) - 1));
             b += __popc(m);
-            if (on && id >= total && total - 1 - ahead == n)
-                *top = id + 1;
+            if (on && total - 1 - ahead == n)
+                end = max(end, id + 1);
         }
+    }
+    if (top) {
+        end = __reduce_max_sync(0xffffffffu, end);
+        if (lane == 0 && end)
+            atomicMax(top, end);
     }
     cluster_barrier();
     // The counts move; the old place holds where to (as its complement) until the tables know.

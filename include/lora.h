@@ -562,13 +562,19 @@ int lora_kv_write_rope(lora_ctx *ctx, const lora_kv *kv, const lora_rope *rope,
  * calls below change all three; they run in stream order, never read them on the host, and can be
  * captured.  The first ceil(lens[s] / page_size) entries of a row count; others are not looked
  * at (the calls leave -1 behind).  A model's layers share one table: what has to be copied
- * is listed, and lora_kv_copy does it in every layer's cache.  A page that something other than
- * these sequences uses is kept out of the free ones by a count of its own in refs.
+ * is listed, and lora_kv_copy does it in every layer's cache.
+ *
+ * A page that something other than these sequences uses is kept out of the free ones by a count
+ * of its own in refs.  Compaction moves such a page like any other, and its user has to follow
+ * the moves.  One whose user cannot, an adapter's page in a unified pool for instance, has
+ * LORA_PAGE_PINNED added to its count: it is neither handed out nor moved, nor written into (a
+ * sequence that holds it too grows in a copy).  Sequences come and go on it as on any other.
  *
  * Results do not depend on timing.  What is out of range is left as it was, and
  * lora_sync_status returns LORA_E_INVAL (a sequence, a length, a list) or LORA_E_PAGE (a page
  * id, or a count that would fall below 0).  LORA_E_CAPACITY: more than 16384 sequences (or
  * entries of a list), 2^30 pages, page_size above 2^20. */
+#define LORA_PAGE_PINNED (1 << 30)
 typedef struct {
     int32_t *lens;                 /* [n_seqs] */
     int32_t *pages;                /* [n_seqs][ld_pages], n_cols of them used */
@@ -602,10 +608,11 @@ int lora_pages_fork(lora_ctx *ctx, const lora_page_table *table, const int32_t *
 int lora_pages_free(lora_ctx *ctx, const lora_page_table *table, const int32_t *seqs,
                     const int32_t *keep, int64_t n, void *stream);
 
-/* Moves the held pages to the front of the pool: with L of them, the highest one goes to the
- * lowest free page, and so on until all are below L, or n have moved.  src and dst [n] are the
- * moves, for lora_kv_copy, then -1; the tables and refs already name the new places.  *top (or
- * null) becomes the end of the highest held page: what is behind it can serve something else. */
+/* Moves the held pages that are not pinned to the front of the pool: the highest one goes to the
+ * lowest free page, and so on until none of them has a free page below it, or n have moved.  src
+ * and dst [n] are the moves, for lora_kv_copy, then -1; the tables and refs already name the new
+ * places.  *top (or null) becomes the end of the highest held page, pinned ones included: what is
+ * behind it can serve something else. */
 int lora_pages_compact(lora_ctx *ctx, const lora_page_table *table, int32_t *src, int32_t *dst,
                        int64_t n, int32_t *top, void *stream);
 
