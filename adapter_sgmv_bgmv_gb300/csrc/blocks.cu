@@ -9,8 +9,9 @@
 //
 // with c the codes of query head g, taken the same way.  Units that are powers of two make
 // every step exact: codes are x / unit rounded once, the sum is of integers below 2^21,
-// the products with the units only move the exponent.  The choice so depends on the inputs
-// alone, not on the order of sums, and equal scores go to the lower page.
+// the products with the units only move the exponent, which has nine bits here (score_of): in fp32 they
+// would leave its range, where keys and queries are both small or both large.  The choice so depends on
+// the inputs alone, not on the order of sums, and equal scores go to the lower page.
 //
 // Measured (heads of 128).  Bounds: 16 prompts of 1056 tokens, 32 heads, bf16 24.6 us, 5.8 TB/s (0.86
 // of a copy's rate); one decode's page of 64 tokens of 8 heads 3 us.  Choice: one row of 512 pages 6.2 us, 32
@@ -19,6 +20,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "kv.h"
 #include "kv.cuh"
@@ -289,12 +291,25 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 256;                   // of a pass over eight bits of the keys
 constexpr int kTile = 16;                    // pages a warp scores at once
 
-// An order-preserving integer of a score; no zero is negative.
-__device__ __forceinline__ uint32_t key_of(float score)
+// Scores are compared as integers: the sign, nine bits of exponent and the sum's 20 bits behind its
+// first one, in the places of an fp32 number shifted down by one (its last three bits are zeros), the
+// exponent counted from 1 at |sum| = 1 and two units of the least exponent.
+constexpr int kNoSay = INT_MIN;              // of a query head that is not finite: below every score
+
+// Bits of a unit, 2^-106 to 2^121, in that place.
+__device__ __forceinline__ int unit_bits(float unit) { return __float_as_int(unit) >> 1; }
+
+// The score of a sum; `page` is unit_bits less the exponents' offset, `query` unit_bits or kNoSay (whose
+// codes are zeros).
+__device__ __forceinline__ int score_of(int sum, int page, int query)
 {
-    const uint32_t b = __float_as_uint(score + 0.f);
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    const int size = (__float_as_int(float(abs(sum))) >> 1) + page + query;
+    return sum == 0 ? query & kNoSay : sum < 0 ? -size : size;
 }
+constexpr int kExponents = (127 + 2 * (127 - 106) - 1) << 22;
+
+constexpr uint32_t kNotThere = 0, kLowest = 1, kAbove = ~0u;     // keys of pages: a score's order, from kLowest up
+__device__ __forceinline__ uint32_t key_of(int score) { return max(uint32_t(score) ^ 0x80000000u, kLowest); }
 
 // 16 pages' bounds by 8 query heads' codes, 32 of the 2 * DIM products at once.
 __device__ __forceinline__ void mma_s8(int c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
@@ -338,7 +353,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelCtas) k_block_select(const __
     extern __shared__ __align__(16) uint8_t smem[];
     const int heads8 = (p.group + 7) & ~7;
     uint8_t *q_codes = smem;
-    float *q_unit = reinterpret_cast<float *>(smem + heads8 * kQueryBytes<DIM>);  // [heads8]
+    int *q_unit = reinterpret_cast<int *>(smem + heads8 * kQueryBytes<DIM>);      // [heads8]
     int *hist = reinterpret_cast<int *>(q_unit + heads8);                         // one for each of four passes
     uint32_t *keys = reinterpret_cast<uint32_t *>(hist + 4 * kBins);
     __shared__ int sums[2 * kSelWarps];
@@ -448,12 +463,13 @@ __global__ void __launch_bounds__(kSelThreads, kSelCtas) k_block_select(const __
             *reinterpret_cast<uint16_t *>(dst + DIM) = uint16_t(above);
         }
         if (lane == 0)
-            q_unit[h] = on ? u : __int_as_float(0x7fffffff);     // no head: no say
+            q_unit[h] = on && u == u ? unit_bits(u) : kNoSay;    // no head: no say
     }
     __syncthreads();
 
     while (base < hi) {
-        float best[2] = {-INFINITY, -INFINITY};
+        int best[2] = {kNoSay, kNoSay};
+        const int page_unit[2] = {unit_bits(unit[0]) - kExponents, unit_bits(unit[1]) - kExponents};
 #pragma unroll 1
         for (int h = 0; h < heads8; h += 8) {
             const uint4 *b = reinterpret_cast<const uint4 *>(q_codes + (h + g) * kQueryBytes<DIM>) + 2 * c;
@@ -468,22 +484,22 @@ __global__ void __launch_bounds__(kSelThreads, kSelCtas) k_block_select(const __
                     mma_s8(s[1], x0[2], x1[2], x0[3], x1[3], y.z, y.w);
                 }
             // pages g and g + 8, heads 2c and 2c + 1; a query that is not finite has no say
-            const float2 u = *reinterpret_cast<const float2 *>(q_unit + h + 2 * c);
+            const int2 u = *reinterpret_cast<const int2 *>(q_unit + h + 2 * c);
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-                best[r] = fmaxf(best[r], fmaxf(float(s[0][2 * r] + s[1][2 * r]) * unit[r] * u.x, float(s[0][2 * r + 1] + s[1][2 * r + 1]) * unit[r] * u.y));
+                best[r] = max(best[r], max(score_of(s[0][2 * r] + s[1][2 * r], page_unit[r], u.x), score_of(s[0][2 * r + 1] + s[1][2 * r + 1], page_unit[r], u.y)));
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
-            best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+            best[r] = max(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+            best[r] = max(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
             const int i = base + 8 * r + g;
             if (c == 0 && i < hi) {
                 // a page that is not there comes last; one that is not finite is looked at: its keys
                 // reach the result as they would
                 if (unit[r] < 0.f)
                     raise_status(p.status, kDevBadPage);
-                keys[i] = unit[r] < 0.f ? 0u : unit[r] != unit[r] ? key_of(INFINITY) : key_of(best[r]);
+                keys[i] = unit[r] < 0.f ? kNotThere : unit[r] != unit[r] ? kAbove : key_of(best[r]);
             }
         }
         base += kStep;

@@ -661,8 +661,8 @@ typedef struct {
  * they are more than sel->blocks, it takes the first `first`, the last `last` (at least 1: its
  * own), and of the others those with the highest score, equal ones in the order of the sequence:
  *     max over the query heads g of the key head of unit_page * unit_g * sum_d max(c_d lo_d, c_d hi_d)
- * with c, unit_g of query head g taken like the bounds' codes, in integers and fp32 products
- * with powers of two: the choice is the same in any order of summation.  A page whose unit is NaN
+ * with c, unit_g of query head g taken like the bounds' codes, in integers with the powers of two
+ * beside them: exact at any magnitude and in any order of summation.  A page whose unit is NaN
  * comes first, one the cache does not have last (and LORA_E_PAGE); a query head with an infinity or a NaN
  * has no say.  LORA_E_CAPACITY: more than 45,056 columns, 128 query heads a key head, or
  * blocks * page_size above 2^30. */
