@@ -10,7 +10,8 @@
 // Angles.  position * frequency has more bits than fp32, and near 32,768 an fp32 product is off
 // by 2e-3.  Whole turns do not matter, so the frequency is taken as a 64-bit binary fraction of
 // a turn (from a double-double product with 1 / 2 pi, once a CTA), and position times it modulo
-// 2^64 is the angle: off by at most 2^-34 turns at any position, by one integer product.
+// 2^64 is the angle: off by at most 2^-34 turns at any position, by one integer product.  Its cosine and
+// sine are taken of 32 of these bits in fp32, whose 24 are within 2^-26 turns: fp32's own step.
 //
 // A vector is one (row, head), 16 elements a lane: eight and eight that are turned with one
 // another (a lane's own pairs, so nothing is exchanged), or 16 side by side.  An item is as many
@@ -52,13 +53,15 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return y;
 }
 
-// f / 2 pi modulo 1, in units of 2^-64.
+// f / 2 pi modulo 1, in units of 2^-64.  Of |f|, whose whole turns come off without a rounding (next to
+// -0 the remainder would have to be rounded to 2^-54, 2^-24 turns at position 2^30).
 __device__ __forceinline__ uint64_t turn_fraction(float f)
 {
     // 1 / 2 pi to 106 bits
     const double c0 = 0x1.45f306dc9c883p-3, c1 = -0x1.6b01ec5417056p-57;
-    const double x = f, hi = x * c0, lo = fma(x, c0, -hi) + x * c1;
-    return uint64_t(__double2ull_rn((hi - floor(hi)) * 0x1p64)) + uint64_t(__double2ll_rn(lo * 0x1p64));
+    const double x = fabsf(f), hi = x * c0, lo = fma(x, c0, -hi) + x * c1;
+    const uint64_t t = uint64_t(__double2ull_rn((hi - floor(hi)) * 0x1p64)) + uint64_t(__double2ll_rn(lo * 0x1p64));
+    return f < 0.f ? 0 - t : t;
 }
 
 // The codes of one vector held 16 elements (fp32) a lane by LANES consecutive lanes, and its

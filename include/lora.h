@@ -527,7 +527,7 @@ int lora_attention(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *batch,
  * and the pairs of its first rot_dim elements are turned by the row's position p,
  *     (a, b) <- (a cos t - b sin t, a sin t + b cos t),   t = p * freqs[j],  j < rot_dim / 2
  * a, b = x_j, x_(j + rot_dim / 2), or x_2j, x_(2j + 1) when interleaved.  In fp32, rounded once
- * at the end; t is exact to 2^-32 turns at any position.
+ * at the end; t, modulo whole turns, is within 2^-25 turns at any position.
  *
  * head_dim is a multiple of 8 up to 256, rot_dim one of 16 up to head_dim (0: no rotation).
  * Weights are fp32 [head_dim] on 16-byte boundaries, or null: no norm on that side.  freqs are
