@@ -93,8 +93,10 @@ __global__ void __launch_bounds__(kThreads) k_kv_bounds(const __grid_constant__ 
     if (threadIdx.x == 0)
         n_pages = 0;
     __syncthreads();
-    const int row = blockIdx.x * rows + int(threadIdx.x);
-    if (int(threadIdx.x) < rows && row < p.b.n_rows) {
+    // the last CTA's rows may go past 2^31
+    const unsigned at_row = blockIdx.x * unsigned(rows) + threadIdx.x;
+    if (int(threadIdx.x) < rows && at_row < unsigned(p.b.n_rows)) {
+        const int row = int(at_row);
         int s = row;
         const bool may = row < p.b.n_seqs;
         const int start = may ? p.b.starts[row] : -1, end = may ? p.b.starts[row + 1] : -1, len = may ? p.b.lens[row] : 0;
