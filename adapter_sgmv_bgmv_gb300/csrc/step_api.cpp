@@ -126,7 +126,7 @@ int take_selection(const lora_ctx *ctx, const lora_kv *kv, const lora_block_sel 
     if (!ctx || !kv || kv->ctx != ctx || !sel || n < 0 || sel->n_rows < n || sel->blocks < 1 || n_heads < 1 ||
         n_heads % kv->view.heads || (n > 0 && (!aligned(sel->lens, 4) || !aligned(sel->pages, 4))))
         return LORA_E_INVAL;
-    if (int64_t(sel->blocks) * kv->view.page_size > kMaxPosition || n * n_heads >= (int64_t(1) << 28))
+    if (int64_t(sel->blocks) * kv->view.page_size > kMaxPosition || n >= (int64_t(1) << 28) || n * n_heads >= (int64_t(1) << 28))
         return LORA_E_CAPACITY;
     return LORA_OK;
 }
