@@ -801,7 +801,7 @@ PAGE_PINNED = 1 << 30
 class PageTable:
     """Which sequence holds which pages (see include/lora.h): lens [n_seqs], pages [n_seqs,
     n_cols] and refs [n_pages], int32 CUDA tensors that the lora_pages_* calls change.  lens and
-    pages may be a KvBatch's.  refs[page] += PAGE_PINNED keeps a page that something else uses,
+    pages may be a KvBatch's.  refs[page] |= PAGE_PINNED keeps a page that something else uses,
     an adapter's in a unified pool for instance, where it is."""
 
     def __init__(self, lens: torch.Tensor, pages: torch.Tensor, refs: torch.Tensor, page_size: int):

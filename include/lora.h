@@ -567,7 +567,7 @@ int lora_kv_write_rope(lora_ctx *ctx, const lora_kv *kv, const lora_rope *rope,
  * A page that something other than these sequences uses is kept out of the free ones by a count
  * of its own in refs.  Compaction moves such a page like any other, and its user has to follow
  * the moves.  One whose user cannot, an adapter's page in a unified pool for instance, has
- * LORA_PAGE_PINNED added to its count: it is neither handed out nor moved, nor written into (a
+ * the bit LORA_PAGE_PINNED set in its count: it is neither handed out nor moved, nor written into (a
  * sequence that holds it too grows in a copy).  Sequences come and go on it as on any other.
  *
  * Results do not depend on timing.  What is out of range is left as it was, and

@@ -102,7 +102,8 @@ def test_an_adapter_in_the_cache_s_pool_stays(ctx):
     cache = L.KvCache(ctx, pool[:, 0], pool[:, 1])
     adapter = [3, 17, 38, 39]
     refs = ints([0] * n_pages)
-    refs[adapter] += L.PAGE_PINNED
+    for _ in range(2):                                     # once is enough
+        refs[adapter] |= L.PAGE_PINNED
     was = pool[adapter].clone()
     table = L.PageTable(ints([0] * 3), torch.full((3, 40), -1, dtype=torch.int32, device="cuda"), refs, page)
     lists = [ints([0] * 3) for _ in range(4)]
