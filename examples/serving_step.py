@@ -49,7 +49,11 @@ class Block:
 
     def __call__(self, x, ids, batch, window=0, sinks=0, blocks=0):
         """x [n, d] -> y [n, d] for the batch's new tokens; ids [n] are their adapters (-1: none).
-        With `blocks`, each token attends to that many pages at most (for steps of few tokens)."""
+        With `blocks`, each token attends to that many pages at most (for steps of few tokens), and there is
+        no window.  The bounds that choose them are kept up to date by every step, so that any later one
+        can choose."""
+        if blocks and window:
+            raise ValueError("a token sees its chosen pages or a window, not both")
         n, q = x.shape[0], self.heads * self.dim
         k = q + self.kv_heads * self.dim
         qkv = torch.empty((n, self.w_qkv.shape[1]), dtype=torch.bfloat16, device=x.device)
