@@ -272,14 +272,14 @@ __global__ void __launch_bounds__(kThreads) k_kv_bounds(const __grid_constant__ 
 }
 
 template <int DIM, int FMT>
-cudaError_t launch(const BoundsParams &p, cudaStream_t stream)
+cudaError_t launch(const BoundsParams &p, int sms, cudaStream_t stream)
 {
     // A CTA has about one page: its rows of a prompt, one row where sequences have few each.
     const int64_t n = p.b.n_rows, touched = n / p.kv.page_size + p.b.n_seqs;
     const int rows = int(std::max<int64_t>(1, std::min<int64_t>(kThreads, n / std::max<int64_t>(1, touched))));
-    // The heads too are dealt out to CTAs while these are fewer than twelve a SM (of 152).
+    // The heads too are dealt out to CTAs while these are fewer than twelve a SM.
     const int64_t ctas = (n + rows - 1) / rows;
-    const int parts = int(std::max<int64_t>(1, std::min<int64_t>((p.kv.heads + kWarps - 1) / kWarps, 1824 / ctas)));
+    const int parts = int(std::max<int64_t>(1, std::min<int64_t>((p.kv.heads + kWarps - 1) / kWarps, 12 * int64_t(sms) / ctas)));
     const dim3 grid{unsigned(ctas), unsigned(parts)};
     return start(k_kv_bounds<DIM, FMT>, grid, kThreads, 0, 0, stream, p, rows);
 }
@@ -628,13 +628,13 @@ cudaError_t launch(const SelectParams &p, int sms, cudaStream_t stream)
 
 }  // namespace
 
-cudaError_t launch_kv_bounds(const BoundsParams &p, cudaStream_t stream)
+cudaError_t launch_kv_bounds(const BoundsParams &p, int sms, cudaStream_t stream)
 {
     const bool wide = p.kv.dim == 128;
     switch (p.kv.format) {
-    case kKvBf16: return wide ? launch<128, kKvBf16>(p, stream) : launch<64, kKvBf16>(p, stream);
-    case kKvInt8: return wide ? launch<128, kKvInt8>(p, stream) : launch<64, kKvInt8>(p, stream);
-    default: return wide ? launch<128, kKvFp8>(p, stream) : launch<64, kKvFp8>(p, stream);
+    case kKvBf16: return wide ? launch<128, kKvBf16>(p, sms, stream) : launch<64, kKvBf16>(p, sms, stream);
+    case kKvInt8: return wide ? launch<128, kKvInt8>(p, sms, stream) : launch<64, kKvInt8>(p, sms, stream);
+    default: return wide ? launch<128, kKvFp8>(p, sms, stream) : launch<64, kKvFp8>(p, sms, stream);
     }
 }
 

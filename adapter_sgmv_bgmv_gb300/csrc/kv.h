@@ -123,7 +123,7 @@ struct RopeParams {
     Divider per_row;          // by a row's items (rope.cu)
     unsigned *status;
 };
-cudaError_t launch_rope(const RopeParams &p, bool store, cudaStream_t stream);
+cudaError_t launch_rope(const RopeParams &p, bool store, int sms, cudaStream_t stream);
 
 // Page tables (pages.cu).
 struct TableView {
@@ -155,7 +155,7 @@ struct BoundsParams {
     BatchView b;
     unsigned *status;
 };
-cudaError_t launch_kv_bounds(const BoundsParams &p, cudaStream_t stream);
+cudaError_t launch_kv_bounds(const BoundsParams &p, int sms, cudaStream_t stream);
 
 constexpr int kMaxSelectCols = 44 << 10;
 constexpr int kMaxSelectGroup = 128;

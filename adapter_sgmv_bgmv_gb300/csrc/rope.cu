@@ -348,39 +348,39 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_rope(const __grid_constant_
 }
 
 template <int G, int FMT>
-cudaError_t launch(RopeParams p, cudaStream_t stream)
+cudaError_t launch(RopeParams p, int sms, cudaStream_t stream)
 {
     // Several rows a CTA, so that whole waves of them are on the GPU; a row cut into parts where
     // there are not enough.
-    constexpr int64_t kWave = 152 * kCtas;
-    const int64_t n = p.b.n_rows, waves = std::max<int64_t>(1, (n + kWave * kMaxRows - 1) / (kWave * kMaxRows));
-    const int rows = int(std::max<int64_t>(1, n / kWave < 1 ? 1 : (n + kWave * waves - 1) / (kWave * waves)));
+    const int64_t wave = int64_t(sms) * kCtas;
+    const int64_t n = p.b.n_rows, waves = std::max<int64_t>(1, (n + wave * kMaxRows - 1) / (wave * kMaxRows));
+    const int rows = int(std::max<int64_t>(1, n / wave < 1 ? 1 : (n + wave * waves - 1) / (wave * waves)));
     const int nvec = p.q_heads + (FMT != kNone ? 2 : 1) * p.k_heads, row_items = (nvec + 32 / G - 1) / (32 / G);
     p.per_row = Divider(row_items);
-    const int64_t parts = rows > 1 ? 1 : std::max<int64_t>(1, std::min<int64_t>((row_items + kWarps - 1) / kWarps, kWave / std::max<int64_t>(n, 1)));
+    const int64_t parts = rows > 1 ? 1 : std::max<int64_t>(1, std::min<int64_t>((row_items + kWarps - 1) / kWarps, wave / std::max<int64_t>(n, 1)));
     const dim3 grid{unsigned((n + rows - 1) / rows), unsigned(parts)};
     return start(k_rope<G, FMT>, grid, kThreads, 0, 0, stream, p, rows);
 }
 
 template <int FMT>
-cudaError_t launch(const RopeParams &p, cudaStream_t stream)
+cudaError_t launch(const RopeParams &p, int sms, cudaStream_t stream)
 {
     if constexpr (FMT == kNone)                      // a cache has heads of 64 or 128
         if (p.dim > 128)
-            return launch<16, FMT>(p, stream);
-    return p.dim <= 64 ? launch<4, FMT>(p, stream) : launch<8, FMT>(p, stream);
+            return launch<16, FMT>(p, sms, stream);
+    return p.dim <= 64 ? launch<4, FMT>(p, sms, stream) : launch<8, FMT>(p, sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeParams &p, bool store, cudaStream_t stream)
+cudaError_t launch_rope(const RopeParams &p, bool store, int sms, cudaStream_t stream)
 {
     if (!store)
-        return launch<kNone>(p, stream);
+        return launch<kNone>(p, sms, stream);
     switch (p.kv.format) {
-    case kKvBf16: return launch<kKvBf16>(p, stream);
-    case kKvInt8: return launch<kKvInt8>(p, stream);
-    default: return launch<kKvFp8>(p, stream);
+    case kKvBf16: return launch<kKvBf16>(p, sms, stream);
+    case kKvInt8: return launch<kKvInt8>(p, sms, stream);
+    default: return launch<kKvFp8>(p, sms, stream);
     }
 }
 

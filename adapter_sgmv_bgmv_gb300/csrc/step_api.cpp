@@ -79,7 +79,7 @@ int rope_call(lora_ctx *ctx, const lora_kv *kv, const lora_rope *rope, const lor
     p.q_heads = q_heads;
     p.k_heads = k_heads;
     p.status = ctx_status(ctx);
-    const cudaError_t e = launch_rope(p, kv != nullptr, stream);
+    const cudaError_t e = launch_rope(p, kv != nullptr, ctx_sms(ctx), stream);
     if (e != cudaSuccess)
         return ctx_cuda_fail(ctx, e);
     ctx_launched(ctx, stream, 256);
@@ -276,7 +276,7 @@ int lora_kv_bounds(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *b, int
     if (rc != LORA_OK || n == 0 || b->n_seqs == 0)
         return rc;
     p.status = ctx_status(ctx);
-    return done(ctx, stream, launch_kv_bounds(p, stream), 2048);
+    return done(ctx, stream, launch_kv_bounds(p, ctx_sms(ctx), stream), 2048);
 }
 
 int lora_block_select(lora_ctx *ctx, const lora_kv *kv, const lora_kv_batch *b, int64_t n, const void *q, int64_t ldq,
