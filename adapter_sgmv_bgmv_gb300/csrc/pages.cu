@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/lora.h"
 #include "kv.h"
@@ -79,28 +80,33 @@ __device__ __forceinline__ Run my_run(int n_pages, int n_cta)
     return {int(min(w * chunk, int64_t(n_pages))), int(min((w + 1) * chunk, int64_t(n_pages)))};
 }
 
-// Pages of the run with refs of `least` and more; the same in all lanes.
-template <int K>
-__device__ __forceinline__ void count_pages(const int32_t *refs, const Run &r, const int (&least)[K], int (&n)[K])
+// Pages of the run with refs > 0, and the bits that any count has; the same in all lanes.
+__device__ __forceinline__ int count_held(const int32_t *refs, const Run &r, int &bits)
 {
     const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        n[k] = 0;
+    int n = 0, seen = 0;
     for (int base = r.lo; base < r.hi; base += 32 * kUnroll) {
         int v[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
             v[u] = base + u * 32 + lane < r.hi ? refs[base + u * 32 + lane] : 0;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                n[k] += v[u] >= least[k];
+        for (int u = 0; u < kUnroll; ++u) {
+            n += v[u] > 0;
+            seen |= v[u];
+        }
     }
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        n[k] = __reduce_add_sync(0xffffffffu, n[k]);
+    bits = __reduce_or_sync(0xffffffffu, seen);
+    return __reduce_add_sync(0xffffffffu, n);
+}
+
+// Pages of the run that are pinned.
+__device__ __noinline__ int count_pinned(const int32_t *refs, const Run &r)
+{
+    int n = 0;
+    for (int id = r.lo + int(threadIdx.x & 31); id < r.hi; id += 32)
+        n += refs[id] >= LORA_PAGE_PINNED;
+    return __reduce_add_sync(0xffffffffu, n);
 }
 
 // What all warps counted, K numbers each: the sums ahead of this warp's and over the cluster.  `counts`
@@ -126,9 +132,14 @@ __device__ __forceinline__ void rank_warps(const int (&mine)[K], int (*counts)[k
             int v = counts[k][lane];
             if (n_cta > 1)
                 asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_cluster(smem_u32(&counts[k][lane]), c)) : "memory");
-            total[k] += __reduce_add_sync(0xffffffffu, v);
-            before[k] += __reduce_add_sync(0xffffffffu, c < rank || (c == rank && lane < warp) ? v : 0);
+            total[k] += v;
+            before[k] += c < rank || (c == rank && lane < warp) ? v : 0;
         }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        total[k] = __reduce_add_sync(0xffffffffu, total[k]);
+        before[k] = __reduce_add_sync(0xffffffffu, before[k]);
+    }
 }
 
 // ---------------------------------------------------------------- extend
@@ -159,8 +170,8 @@ __global__ void __launch_bounds__(kThreads) k_pages_extend(const __grid_constant
     grid_dep_launch();
 
     const Run run = my_run(t.n_pages, n_cta);
-    int held[1];
-    count_pages(t.refs, run, {1}, held);
+    int bits;
+    const int held[1] = {count_held(t.refs, run, bits)};
 
     // What each sequence wants: every CTA works it out for itself.
     int any = 0;
@@ -403,20 +414,19 @@ __global__ void __launch_bounds__(kThreads) k_pages_compact(const __grid_constan
     grid_dep_launch();
     for (int k = at; k < n; k += all)
         src[k] = dst[k] = -1;
-    if (at == 0 && top)
-        *top = 0;
     const Run run = my_run(t.n_pages, n_cta);
-    int mine[2], first[2], sums[2];                  // held pages, and how many of them are pinned
-    count_pages(t.refs, run, {1, LORA_PAGE_PINNED}, mine);
+    int bits, first[2], sums[2];
+    const int held_here = count_held(t.refs, run, bits);
+    const int mine[2] = {held_here, bits & LORA_PAGE_PINNED ? count_pinned(t.refs, run) : 0};
     rank_warps(mine, counts, n_cta, first, sums);
     const int pinned = mine[1], held = mine[0] - pinned, total = sums[0] - sums[1];
     const int held0 = first[0] - first[1], pinned0 = first[1];
+    const bool pins_there = sums[1] > 0;
+    if (at == 0 && top)
+        *top = pins_there ? 0 : total;               // and where there are pins, or a mover stays, what these say below
     int end = 0;                                     // of the highest page that this lane knows is held in the end
-    // a run of free pages at or above L, or of held ones below it, has nothing to move
-    if (pinned == 0 && ((held == 0 && run.lo - pinned0 >= total) || (held == run.hi - run.lo && run.hi - pinned0 <= total))) {
-        if (held > 0 && run.hi - pinned0 == total)
-            end = run.hi;
-    } else {
+    auto walk = [&](auto with_pins) {
+        constexpr bool kPins = decltype(with_pins)::value;
         int before = held0, pins = pinned0;
         for (int base = run.lo; base < run.hi; base += 32 * 4) {
             int v[4];
@@ -426,19 +436,19 @@ __global__ void __launch_bounds__(kThreads) k_pages_compact(const __grid_constan
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int id = base + u * 32 + lane;
-                const bool pin = v[u] >= LORA_PAGE_PINNED, on = v[u] > 0 && !pin;
+                const bool pin = kPins && v[u] >= LORA_PAGE_PINNED, on = v[u] > 0 && !pin;
                 const unsigned below = (1u << lane) - 1, m = __ballot_sync(0xffffffffu, on);
                 const int ahead = before + __popc(m & below);
                 before += __popc(m);
                 int place = id - pins;
-                if (pinned) {
+                if (kPins) {
                     const unsigned mp = __ballot_sync(0xffffffffu, pin);
                     place -= __popc(mp & below);
                     pins += __popc(mp);
                 }
                 if (id >= run.hi)
                     continue;
-                if (pin || place == total - 1)       // the last place is held if all move; else one that stays is higher
+                if (kPins && (pin || place == total - 1))
                     end = id + 1;
                 if (pin)
                     continue;
@@ -450,6 +460,17 @@ __global__ void __launch_bounds__(kThreads) k_pages_compact(const __grid_constan
                 }
             }
         }
+    };
+    // The last place below L is held if all move; else a page that stays is higher.
+    if (pinned) {
+        walk(std::true_type());
+    } else {
+        const int last = total - 1 + pinned0;
+        if (pins_there && last >= run.lo && last < run.hi)
+            end = last + 1;
+        // a run of free pages at or above L, or of held ones below it, has nothing to move
+        if (!(held == 0 && run.lo - pinned0 >= total) && !(held == run.hi - run.lo && run.hi - pinned0 <= total))
+            walk(std::false_type());
     }
     cluster_barrier();
     // Where the lists are full, the mover with n higher ones is the highest that stays.
