@@ -14,9 +14,9 @@
 // the inputs alone, not on the order of sums, and equal scores go to the lower page.
 //
 // Measured (heads of 128).  Bounds: 16 prompts of 1056 tokens, 32 heads, bf16 24.6 us, 5.8 TB/s (0.86
-// of a copy's rate); one decode's page of 64 tokens of 8 heads 3 us.  Choice: one row of 512 pages 6.2 us, 32
-// rows of up to 409 pages, 64 heads on 8, 11.6 us, 39 rows of up to 1504 pages, 28 heads on 4, 19 us: chains of
-// latencies (lengths, pages, bounds, products, three passes over the scores, output).
+// of a copy's rate); one decode's page of 64 tokens of 8 heads 3 us.  Choice: one row of 512 pages 6.3 us, 32
+// rows of up to 409 pages, 64 heads on 8, 11.7 us (128 heads 16.4), 39 rows of up to 1504 pages, 28 heads on 4, 19 us:
+// chains of latencies (lengths, pages, bounds, products, three passes over the scores, output).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -77,8 +77,9 @@ __device__ __forceinline__ int code_of(float x, float inverse) { return max(-127
 
 // A CTA looks at `rows` rows of the call: each that is its sequence's first in a page stands for
 // the page, and the page's vectors [cells][dim] of each head are a warp's, four loads a lane (two in
-// 8 bits) under way.  Every page touched is read once: DRAM bounds it in bf16, in 8 bits the conversions and
-// the registers they take (with eight loads under way 45 us for 16 prompts of 1056 tokens, 32 heads, now 31).
+// 8 bits) under way.  Every page touched is read once: DRAM bounds it in bf16, in 8 bits the rounds
+// of loads, each waited for ahead of its conversions (16 prompts of 1056 tokens, 32 heads, 31 us, of which some 7 are
+// instructions; with eight loads under way, and the registers that takes, 45).
 template <int DIM, int FMT>
 __global__ void __launch_bounds__(kThreads) k_kv_bounds(const __grid_constant__ BoundsParams p, int rows)
 {
