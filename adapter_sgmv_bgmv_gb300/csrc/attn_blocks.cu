@@ -26,8 +26,9 @@
 // scheduler), and where units are few that of start, tiles and joining.  Measured (dim 128): one row of 32
 // pages of 64, 32 heads on 8, bf16 9.2 us; 39 rows of 128 pages of 16, 28 heads on 4, 31 us (164 MB, most
 // of it from L2); 32 rows of 48 pages of 64, 64 heads on 8, int8 55 us, 3.8 TB/s, and
-// with 128 heads on 8, 16 to a key head, 64 us (bf16 75).  The few-rows kernel over the first three's lists takes 16.7, 45 and 67 us.  Registers decide: int8 with three CTAs a SM instead of two, spilling
-// 170 bytes, 124 us; with one tile at once and six warps a CTA 57; bf16 with two CTAs a SM 40 us, with four 44.
+// with 128 heads on 8, 16 to a key head, 64 us (bf16 75).  The few-rows kernel over the first
+// three's lists takes 16.7, 45 and 67 us.  Registers decide: int8 with three CTAs a SM instead of two, spilling 170
+// bytes, 124 us; with one tile at once and six warps a CTA 57; bf16 with two CTAs a SM 40 us, with four 44.
 #include <cuda_runtime.h>
 
 #include <algorithm>
