@@ -213,7 +213,12 @@ __global__ void __launch_bounds__(kThreads) k_pages_extend(const __grid_constant
             }
             writers = __reduce_add_sync(0xffffffffu, writers);
             later = __any_sync(0xffffffffu, later);
-            if (lane == 0 && (later || writers < t.refs[m])) {
+            if (lane)
+                continue;
+            if (writers > t.refs[m]) {               // more than are counted: the table is wrong
+                raise_status(status, kDevBadPage);
+                want[s].upto = -1;
+            } else if (later || writers < t.refs[m]) {
                 want[s].upto += 1;
                 want[s].first = (want[s].first - 1) | int(0x80000000u);
             }
