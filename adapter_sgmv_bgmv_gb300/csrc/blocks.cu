@@ -306,7 +306,7 @@ __device__ __forceinline__ int unit_bits(float unit) { return __float_as_int(uni
 // codes are zeros).
 __device__ __forceinline__ int score_of(int sum, int page, int query)
 {
-    const int size = (__float_as_int(float(abs(sum))) >> 1) + page + query;
+    const int size = int((__float_as_uint(float(abs(sum))) >> 1) + uint32_t(page) + uint32_t(query));
     return sum == 0 ? query & kNoSay : sum < 0 ? -size : size;
 }
 constexpr int kExponents = (127 + 2 * (127 - 106) - 1) << 22;

@@ -22,8 +22,8 @@
 //
 // Measured: 16,896 rows of 32 + 32 heads of 128 without norms 86 us, 6.4 TB/s (0.95 of a copy's
 // rate); 8191 rows of 32 + 8 heads with norms and the store into a bf16 cache 41 us (36 without the
-// norms), 4.9 TB/s, into int8 45.5 and e4m3 46.6 us.  Eight elements a lane, pairs in two lanes and exchanged, took 173 and 58 us, bound by
-// instructions; three CTAs a SM instead of four 89 and 41, five 91 and 53.
+// norms), 4.9 TB/s, into int8 45.5 and e4m3 46.6 us.  Eight elements a lane, pairs in two lanes and
+// exchanged, took 173 and 58 us, bound by instructions; three CTAs a SM instead of four 89 and 41, five 91 and 53.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 

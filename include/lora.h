@@ -572,7 +572,7 @@ int lora_kv_write_rope(lora_ctx *ctx, const lora_kv *kv, const lora_rope *rope,
  *
  * Results do not depend on timing.  What is out of range is left as it was, and
  * lora_sync_status returns LORA_E_INVAL (a sequence, a length, a list) or LORA_E_PAGE (a page
- * id, or a count that would fall below 0).  LORA_E_CAPACITY: more than 16384 sequences (or
+ * id, or a count below what the rows show).  LORA_E_CAPACITY: more than 16384 sequences (or
  * entries of a list), 2^30 pages, page_size above 2^20. */
 #define LORA_PAGE_PINNED (1 << 30)
 typedef struct {
